@@ -95,12 +95,16 @@ typedef enum {
     GEMM_DF32 = 8    /* dual, fp32 parts */
 } gemm_dtype_t;
 
-/* bias: bias[j] added to every row; relu: max(0, .) applied last. */
+/*
+ * bias: bias[j] added to every row; relu: max(0, .) applied last.  gate (grouped products only):
+ * D = C > 0 ? alpha * product : 0, the gradient of a ReLU whose output is C.
+ */
 typedef enum {
     GEMM_EPI_NONE = 0,
     GEMM_EPI_RELU = 1,
     GEMM_EPI_BIAS = 2,
-    GEMM_EPI_BIAS_RELU = 3
+    GEMM_EPI_BIAS_RELU = 3,
+    GEMM_EPI_GATE = 4
 } gemm_epilogue_t;
 
 typedef enum {
@@ -333,6 +337,97 @@ const char *gemm_status_string(gemm_status_t status);
  * Returns INVALID_VALUE for a NULL plan or buffer.
  */
 gemm_status_t gemm_plan_describe(gemm_plan_t plan, char *buf, size_t len);
+
+/* ---- products grouped by expert ------------------------------------------------------------
+ *
+ * The rows of a token buffer, sorted by the expert they were routed to: range e = [offsets[e],
+ * offsets[e+1]) of the rows belongs to expert e.  offsets are groups + 1 int32 values in DEVICE
+ * memory, read by the kernels (the host never waits for a routing decision, and a captured graph
+ * follows the offsets it finds at each replay); they must be ordered and within [0, rows].  Rows
+ * before the first and behind the last range are neither read nor written.  Ranges may be empty.
+ * Offsets that are out of order or out of bounds give undefined results in D, but never an access
+ * outside the operands.
+ *
+ *   rows:     D[r,:] = act(alpha * A[r,:] * op(B_e) + beta * C[r,:] + bias_e)   for r in range e,
+ *             or, with GEMM_EPI_GATE, D[r,j] = C[r,j] > 0 ? alpha * (A[r,:] * op(B_e))[j] : 0
+ *   gradient: D_e = alpha * A_e^T * B_e + beta * C_e, summed over the rows of range e (A_e, B_e:
+ *             those rows of A and B), and bias_grad_e[j] = the sum of B[r,j] over them
+ *
+ * A layer D = act(A * W_e + bias_e) therefore trains with a rows plan for its output, a rows plan
+ * with W_e transposed for the gradient towards A (gated by the ReLU in front of the layer, if
+ * there is one), and a gradient plan for W_e and bias_e.
+ *
+ * Types: F32 -> F32, F16 -> F16 | F32, BF16 -> BF16 | F32, accumulated in fp32; bias and bias_grad
+ * are fp32.  Any leading dimension and alignment is allowed (the element's own alignment is
+ * required); the fast kernels need 16-byte aligned A and B, leading dimensions and strides.  A
+ * plan holds no device memory: it may be shared between host threads, streams and graphs.
+ */
+typedef struct gemm_grouped_plan *gemm_grouped_plan_t;
+
+/*
+ * Description of a rows plan.  rows: rows of A, C and D; B_e is K x N (op_b N; ldb >= N) or stored
+ * N x K (op_b T; ldb >= K) at B + e * stride_b, bias_e at bias + e * stride_bias (a zero stride
+ * shares it).  algo: AUTO, or FAST (with tile 256 or 128; 0: the plan's choice), GENERAL (tile 128
+ * or 64) or SKINNY (tile 16, 32, 48 or 64: rows per workgroup) to pin a kernel, which falls back
+ * to the general one where its preconditions do not hold.
+ */
+typedef struct {
+    int64_t rows, N, K, groups;
+    gemm_op_t op_b;
+    int64_t lda, ldb, ldc, stride_b, stride_bias;
+    gemm_dtype_t ab_type, cd_type;
+    gemm_epilogue_t epilogue;
+    gemm_algo_t algo;
+    int32_t tile;
+} gemm_grouped_desc_t;
+
+/*
+ * Description of a gradient plan.  A is rows x M (lda >= M), B rows x N (ldb >= N); D_e and C_e
+ * are M x N at D, C + e * stride_c (ldc >= N; stride_c at least one D_e).  An expert without rows
+ * gets beta * C_e and a zero bias_grad.  algo and tile as above, without SKINNY.
+ */
+typedef struct {
+    int64_t rows, M, N, groups;
+    int64_t lda, ldb, ldc, stride_c;
+    gemm_dtype_t ab_type, cd_type;
+    gemm_algo_t algo;
+    int32_t tile;
+} gemm_grouped_grad_desc_t;
+
+/*
+ * Host-only, like gemm_plan_create.  Return INVALID_VALUE for a NULL argument, a negative size,
+ * groups < 1, a leading dimension or stride below its minimum, or an enum or tile out of range;
+ * NOT_SUPPORTED for a type pair outside the table, a size, leading dimension or group count of
+ * 2^31, 2^31 or 2^20 and more, one expert's B spanning 2^31 bytes or more, or a grid of 2^31
+ * workgroups; ALLOC_FAILED without host memory.
+ */
+gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grouped_desc_t *desc);
+gemm_status_t gemm_grouped_grad_plan_create(gemm_grouped_plan_t *out,
+                                            const gemm_grouped_grad_desc_t *desc);
+
+/*
+ * Enqueues a rows plan on `stream`: one kernel, no allocation, no synchronisation.  C is read when
+ * beta != 0 or the epilogue is GATE (then beta must be 0); C == D is allowed.  bias: required when
+ * the epilogue has one.  Returns INVALID_VALUE for a NULL plan, a gradient plan, a missing
+ * pointer, a pointer off its element's alignment or a NaN scalar; HIP_ERROR when the launch fails.
+ */
+gemm_status_t gemm_grouped_run(gemm_grouped_plan_t plan, const void *A, const void *B, const void *C,
+                               void *D, const void *bias, const int32_t *offsets, float alpha,
+                               float beta, void *stream);
+
+/*
+ * Enqueues a gradient plan on `stream`: one kernel.  bias_grad: groups x N fp32 values, written
+ * (not added to); NULL leaves it out.  C as above.  Errors as gemm_grouped_run's.
+ */
+gemm_status_t gemm_grouped_grad_run(gemm_grouped_plan_t plan, const void *A, const void *B,
+                                    const void *C, void *D, float *bias_grad,
+                                    const int32_t *offsets, float alpha, float beta, void *stream);
+
+/* Frees a plan (NULL is a no-op).  Always returns SUCCESS. */
+gemm_status_t gemm_grouped_plan_destroy(gemm_grouped_plan_t plan);
+
+/* The plan's kernel as text, like gemm_plan_describe. */
+gemm_status_t gemm_grouped_plan_describe(gemm_grouped_plan_t plan, char *buf, size_t len);
 
 #ifdef __cplusplus
 }

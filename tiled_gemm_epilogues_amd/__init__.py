@@ -6,7 +6,8 @@ Argument marshalling only: every step of the computation runs in the HIP kernels
 ABI (include/gemm.h).  The low-level functions carry the C names (gemm_plan_create, gemm_run,
 gemm_run_noalloc, gemm_plan_create_batched, gemm_plan_create_desc, gemm_plan_destroy,
 gemm_status_string, gemm_plan_describe); `Plan` wraps them for torch tensors, whose device
-memory and streams are the only things taken from PyTorch.
+memory and streams are the only things taken from PyTorch.  `GroupedPlan` and `GroupedGradPlan`
+wrap the products grouped by expert (gemm_grouped_*) the same way.
 
 The library is loaded on first use, not at import, so that the build module of this package
 can run on a checkout that has no library yet.  There is no fallback: the first call fails with
@@ -24,7 +25,7 @@ DTYPE = {"f32": 0, "f16": 1, "bf16": 2, "i8": 3, "i32": 4, "cf16": 5, "cf32": 6,
          "df32": 8}
 ELEM_BYTES = {"f32": 4, "f16": 2, "bf16": 2, "i8": 1, "i32": 4, "cf16": 4, "cf32": 8, "df16": 4,
               "df32": 8}
-EPILOGUE = {"none": 0, "relu": 1, "bias": 2, "bias_relu": 3}
+EPILOGUE = {"none": 0, "relu": 1, "bias": 2, "bias_relu": 3, "gate": 4}
 TRANSFORM = {"none": 0, "relu": 1, "from_f32": 2, "from_i8": 3}
 # stored element type of an operand whose load transform converts it to the input type
 STORED_BY_TRANSFORM = {"from_f32": "f32", "from_i8": "i8"}
@@ -37,7 +38,9 @@ ALGO = {"auto": 0, "fast": 1, "staged": 2, "general": 3, "skinny": 4, "split": 5
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 EXPORTED = ("gemm_plan_create", "gemm_plan_create_batched", "gemm_plan_create_desc", "gemm_run",
-            "gemm_run_noalloc", "gemm_plan_destroy", "gemm_status_string", "gemm_plan_describe")
+            "gemm_run_noalloc", "gemm_plan_destroy", "gemm_status_string", "gemm_plan_describe",
+            "gemm_grouped_plan_create", "gemm_grouped_grad_plan_create", "gemm_grouped_run",
+            "gemm_grouped_grad_run", "gemm_grouped_plan_destroy", "gemm_grouped_plan_describe")
 
 _i64, _vp, _ci, _f = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
 
@@ -51,6 +54,21 @@ class GemmDesc(ctypes.Structure):
                 ("transform_b", _ci), ("transform_c", _ci), ("kind_a", _ci), ("kind_b", _ci),
                 ("algo", _ci), ("tile", _ci), ("batch2", _i64), ("stride2_a", _i64),
                 ("stride2_b", _i64), ("stride2_c", _i64), ("stride2_bias", _i64)]
+
+
+class GroupedDesc(ctypes.Structure):
+    """gemm_grouped_desc_t of include/gemm.h."""
+    _fields_ = [("rows", _i64), ("N", _i64), ("K", _i64), ("groups", _i64), ("op_b", _ci),
+                ("lda", _i64), ("ldb", _i64), ("ldc", _i64), ("stride_b", _i64),
+                ("stride_bias", _i64), ("ab_type", _ci), ("cd_type", _ci), ("epilogue", _ci),
+                ("algo", _ci), ("tile", ctypes.c_int32)]
+
+
+class GroupedGradDesc(ctypes.Structure):
+    """gemm_grouped_grad_desc_t of include/gemm.h."""
+    _fields_ = [("rows", _i64), ("M", _i64), ("N", _i64), ("groups", _i64), ("lda", _i64),
+                ("ldb", _i64), ("ldc", _i64), ("stride_c", _i64), ("ab_type", _ci),
+                ("cd_type", _ci), ("algo", _ci), ("tile", ctypes.c_int32)]
 
 
 _lib = None
@@ -87,6 +105,15 @@ def lib():
     L.gemm_status_string.restype = ctypes.c_char_p
     L.gemm_plan_describe.argtypes = [_vp, ctypes.c_char_p, ctypes.c_size_t]
     L.gemm_plan_describe.restype = _ci
+    L.gemm_grouped_plan_create.argtypes = [ctypes.POINTER(_vp), ctypes.POINTER(GroupedDesc)]
+    L.gemm_grouped_grad_plan_create.argtypes = [ctypes.POINTER(_vp), ctypes.POINTER(GroupedGradDesc)]
+    L.gemm_grouped_run.argtypes = [_vp] * 7 + [_f, _f, _vp]
+    L.gemm_grouped_grad_run.argtypes = [_vp] * 7 + [_f, _f, _vp]
+    L.gemm_grouped_plan_destroy.argtypes = [_vp]
+    L.gemm_grouped_plan_describe.argtypes = [_vp, ctypes.c_char_p, ctypes.c_size_t]
+    for fn in ("gemm_grouped_plan_create", "gemm_grouped_grad_plan_create", "gemm_grouped_run",
+               "gemm_grouped_grad_run", "gemm_grouped_plan_destroy", "gemm_grouped_plan_describe"):
+        getattr(L, fn).restype = _ci
     _lib = L
     return _lib
 
@@ -155,6 +182,47 @@ def gemm_plan_destroy(plan):
 def gemm_plan_describe(plan):
     buf = ctypes.create_string_buffer(256)
     st = lib().gemm_plan_describe(plan, buf, 256)
+    return st, buf.value.decode()
+
+
+def gemm_grouped_plan_create(rows, N, K, groups, op_b, lda, ldb, ldc, stride_b, stride_bias,
+                             ab_type, cd_type, epilogue, algo="auto", tile=0):
+    """Returns (status, handle) of a rows plan (products grouped by expert)."""
+    d = GroupedDesc(rows, N, K, groups, _enum(OP, op_b), lda, ldb, ldc, stride_b, stride_bias,
+                    _enum(DTYPE, ab_type), _enum(DTYPE, cd_type), _enum(EPILOGUE, epilogue),
+                    _enum(ALGO, algo), int(tile))
+    h = _vp()
+    st = lib().gemm_grouped_plan_create(ctypes.byref(h), ctypes.byref(d))
+    return st, h.value
+
+
+def gemm_grouped_grad_plan_create(rows, M, N, groups, lda, ldb, ldc, stride_c, ab_type, cd_type,
+                                  algo="auto", tile=0):
+    """Returns (status, handle) of a gradient plan (weight gradients grouped by expert)."""
+    d = GroupedGradDesc(rows, M, N, groups, lda, ldb, ldc, stride_c, _enum(DTYPE, ab_type),
+                        _enum(DTYPE, cd_type), _enum(ALGO, algo), int(tile))
+    h = _vp()
+    st = lib().gemm_grouped_grad_plan_create(ctypes.byref(h), ctypes.byref(d))
+    return st, h.value
+
+
+def gemm_grouped_run(plan, A, B, C, D, bias, offsets, alpha, beta, stream):
+    """Raw pointers (ints or None) and a hipStream_t handle (int or None)."""
+    return lib().gemm_grouped_run(plan, A, B, C, D, bias, offsets, alpha, beta, stream)
+
+
+def gemm_grouped_grad_run(plan, A, B, C, D, bias_grad, offsets, alpha, beta, stream):
+    """Raw pointers (ints or None) and a hipStream_t handle (int or None)."""
+    return lib().gemm_grouped_grad_run(plan, A, B, C, D, bias_grad, offsets, alpha, beta, stream)
+
+
+def gemm_grouped_plan_destroy(plan):
+    return lib().gemm_grouped_plan_destroy(plan)
+
+
+def gemm_grouped_plan_describe(plan):
+    buf = ctypes.create_string_buffer(256)
+    st = lib().gemm_grouped_plan_describe(plan, buf, 256)
     return st, buf.value.decode()
 
 
@@ -347,3 +415,157 @@ class Plan:
             self.close()
         except Exception:
             pass
+
+
+class _GroupedBase:
+    """What the plans over row ranges share: the handle, and the checks of a run's tensors."""
+
+    _h = None
+
+    @property
+    def handle(self):
+        return self._h
+
+    def describe(self):
+        return gemm_grouped_plan_describe(self._h)[1]
+
+    def close(self):
+        if getattr(self, "_h", None):
+            gemm_grouped_plan_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def check(self, what, t):
+        """Checks tensor t against the plan's storage for operand `what`: its dtype, that it is
+        contiguous, that a 2-D or higher tensor's rows are the leading dimension long, and that it
+        holds every element the plan's runs may touch.  Raises TypeError or ValueError; the device
+        is checked by run()."""
+        dtype, need, row_len = self._spec[what]
+        if t.dtype is not dtype:
+            raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous (the plan's leading dimension and "
+                             "strides describe its layout)")
+        if row_len is not None and t.dim() >= 2 and t.shape[-1] != row_len:
+            raise ValueError(f"{what}: rows of {t.shape[-1]} elements, the plan's leading "
+                             f"dimension is {row_len}")
+        if t.numel() < need:
+            raise ValueError(f"{what} holds {t.numel()} elements, the plan spans {need}")
+
+    def _ptr(self, what, t, device):
+        """Device pointer of tensor t after checking it; raw ints and None pass as is."""
+        if t is None or isinstance(t, int):
+            return t
+        if t.get_device() != device:
+            raise ValueError(f"{what} is on {t.device}, the current device is cuda:{device}"
+                             if t.is_cuda else f"{what} must be a device tensor")
+        self.check(what, t)
+        return t.data_ptr()
+
+    @staticmethod
+    def _stream(stream, device):
+        import torch
+        if stream is None:
+            return torch.cuda.current_stream(device).cuda_stream
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+class GroupedPlan(_GroupedBase):
+    """Products of row ranges with one matrix each (see include/gemm.h): rows offsets[e] ..
+    offsets[e+1]-1 of A (rows x K) times op(B_e), with the plan's epilogue ("gate": D = C > 0 ?
+    alpha * product : 0).  B is the stack of the experts' matrices, K x N each (op_b "N") or
+    N x K ("T"); bias holds N fp32 values per expert.  stride_b and stride_bias default to a packed
+    stack."""
+
+    def __init__(self, rows, N, K, groups, op_b="N", lda=None, ldb=None, ldc=None, stride_b=None,
+                 stride_bias=None, ab="f16", cd="f16", epilogue="none", algo="auto", tile=0):
+        import torch
+        self.rows, self.N, self.K, self.groups = rows, N, K, groups
+        self.op_b, self.ab, self.cd, self.epilogue = op_b, ab, cd, epilogue
+        b_rows, b_cols = (K, N) if op_b in ("N", 0) else (N, K)
+        self.lda = lda if lda is not None else max(1, K)
+        self.ldb = ldb if ldb is not None else max(1, b_cols)
+        self.ldc = ldc if ldc is not None else max(1, N)
+        self.stride_b = stride_b if stride_b is not None else b_rows * self.ldb
+        self.stride_bias = stride_bias if stride_bias is not None else N
+        st, h = gemm_grouped_plan_create(rows, N, K, groups, op_b, self.lda, self.ldb, self.ldc,
+                                         self.stride_b, self.stride_bias, ab, cd, epilogue, algo, tile)
+        if st != STATUS_SUCCESS:
+            raise GemmError(st, "gemm_grouped_plan_create")
+        self._h = h
+        tab, tcd = _torch_dtype(ab), _torch_dtype(cd)
+        b = _span(b_rows, b_cols, self.ldb)
+        cdn = _span(rows, N, self.ldc)
+        self._spec = {
+            "A": (tab, _span(rows, K, self.lda), self.lda),
+            "B": (tab, (groups - 1) * self.stride_b + b if b else 0, self.ldb),
+            "C": (tcd, cdn, self.ldc), "D": (tcd, cdn, self.ldc),
+            "bias": (torch.float32, (groups - 1) * self.stride_bias + N if N else 0, None),
+            "offsets": (torch.int32, groups + 1, None)}
+        self._has_bias = epilogue in ("bias", "bias_relu", 2, 3)
+        self._gate = epilogue in ("gate", 4)
+
+    def run(self, A, B, C, D, offsets, bias=None, alpha=1.0, beta=0.0, stream=None):
+        """Enqueue on `stream` (as Plan.run).  offsets: groups + 1 int32 values on the device.
+        C is read when beta != 0 or the epilogue is "gate".  Rows of D outside the ranges are left
+        as they are.  Raises ValueError / TypeError before anything is enqueued when a tensor does
+        not fit the plan."""
+        import torch
+        dev = torch.cuda.current_device()
+        ptr = self._ptr
+        st = lib().gemm_grouped_run(
+            self._h, ptr("A", A, dev), ptr("B", B, dev),
+            ptr("C", C, dev) if beta != 0 or self._gate else None, ptr("D", D, dev),
+            ptr("bias", bias, dev) if self._has_bias else None, ptr("offsets", offsets, dev),
+            float(alpha), float(beta), self._stream(stream, dev))
+        if st != STATUS_SUCCESS:
+            raise GemmError(st, "gemm_grouped_run")
+
+
+class GroupedGradPlan(_GroupedBase):
+    """Weight gradients over row ranges (see include/gemm.h): D_e = alpha * A_e^T * B_e + beta *
+    C_e with the rows offsets[e] .. offsets[e+1]-1 of A (rows x M) and B (rows x N), and the
+    column sums of those rows of B as the gradient of the expert's bias.  D is the stack of M x N
+    matrices, packed unless stride_c says otherwise."""
+
+    def __init__(self, rows, M, N, groups, lda=None, ldb=None, ldc=None, stride_c=None, ab="f16",
+                 cd="f32", algo="auto", tile=0):
+        import torch
+        self.rows, self.M, self.N, self.groups = rows, M, N, groups
+        self.ab, self.cd = ab, cd
+        self.lda = lda if lda is not None else max(1, M)
+        self.ldb = ldb if ldb is not None else max(1, N)
+        self.ldc = ldc if ldc is not None else max(1, N)
+        self.stride_c = stride_c if stride_c is not None else M * self.ldc
+        st, h = gemm_grouped_grad_plan_create(rows, M, N, groups, self.lda, self.ldb, self.ldc,
+                                              self.stride_c, ab, cd, algo, tile)
+        if st != STATUS_SUCCESS:
+            raise GemmError(st, "gemm_grouped_grad_plan_create")
+        self._h = h
+        tab, tcd = _torch_dtype(ab), _torch_dtype(cd)
+        c = _span(M, N, self.ldc)
+        cdn = (groups - 1) * self.stride_c + c if c else 0
+        self._spec = {
+            "A": (tab, _span(rows, M, self.lda), self.lda),
+            "B": (tab, _span(rows, N, self.ldb), self.ldb),
+            "C": (tcd, cdn, self.ldc), "D": (tcd, cdn, self.ldc),
+            "bias_grad": (torch.float32, groups * N, None),
+            "offsets": (torch.int32, groups + 1, None)}
+
+    def run(self, A, B, C, D, offsets, bias_grad=None, alpha=1.0, beta=0.0, stream=None):
+        """Enqueue on `stream` (as Plan.run).  C is read when beta != 0 (C == D adds into the
+        gradients); bias_grad (groups x N, fp32) is overwritten, None leaves it out."""
+        import torch
+        dev = torch.cuda.current_device()
+        ptr = self._ptr
+        st = lib().gemm_grouped_grad_run(
+            self._h, ptr("A", A, dev), ptr("B", B, dev), ptr("C", C, dev) if beta != 0 else None,
+            ptr("D", D, dev), ptr("bias_grad", bias_grad, dev), ptr("offsets", offsets, dev),
+            float(alpha), float(beta), self._stream(stream, dev))
+        if st != STATUS_SUCCESS:
+            raise GemmError(st, "gemm_grouped_grad_run")

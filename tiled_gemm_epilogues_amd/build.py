@@ -17,6 +17,7 @@ LIB = os.path.join(HERE, "libtge.so")
 PAIRS = ["F32_F32", "F16_F16", "F16_F32", "BF16_BF16", "BF16_F32", "I8_I32"]
 FAST_PAIRS = ["F16_F16", "F16_F32", "BF16_BF16", "BF16_F32", "I8_I32"]
 SKINNY_PAIRS = ["F16_F16", "F16_F32", "BF16_BF16", "BF16_F32", "I8_I32"]
+GROUPED_PAIRS = ["F16_F16", "F16_F32", "BF16_BF16", "BF16_F32"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -35,30 +36,36 @@ def _run(cmd, verbose):
     return r
 
 
+def steps():
+    """The compile commands, one per object (the object is each command's last word)."""
+    out = []
+
+    def add(source, obj, *defines, host=False):
+        out.append([HIPCC, *FLAGS, *defines, *(["-x", "hip"] if host else []), "-c",
+                    os.path.join(CSRC, source), "-o", os.path.join(BUILD, obj + ".o")])
+
+    for name, pairs in (("gemm_kernels", PAIRS), ("gemm_fast", FAST_PAIRS), ("gemm_skinny", SKINNY_PAIRS)):
+        for pair in pairs:
+            add(name + ".hip", f"{name}_{pair.lower()}", f"-DTGE_PAIR_{pair}")
+    # the same kernels on products grouped by expert (float types)
+    for name, pairs in (("gemm_kernels", GROUPED_PAIRS + ["F32_F32"]), ("gemm_fast", GROUPED_PAIRS),
+                        ("gemm_skinny", GROUPED_PAIRS)):
+        for pair in pairs:
+            add(name + ".hip", f"grouped_{name}_{pair.lower()}", f"-DTGE_PAIR_{pair}", "-DTGE_GROUPED")
+    for name in ("gemm_complex", "gemm_diag", "gemm_repack"):
+        add(name + ".hip", name)
+    for name in ("gemm_api", "grouped_api"):
+        add(name + ".cpp", name, host=True)
+    return out
+
+
 def build(verbose=False, jobs=None):
     os.makedirs(BUILD, exist_ok=True)
     jobs = jobs or min(8, os.cpu_count() or 1)
-    steps = []
-    for pair in PAIRS:
-        obj = os.path.join(BUILD, f"gemm_kernels_{pair.lower()}.o")
-        steps.append([HIPCC, *FLAGS, f"-DTGE_PAIR_{pair}", "-c",
-                      os.path.join(CSRC, "gemm_kernels.hip"), "-o", obj])
-    for pair in FAST_PAIRS:
-        obj = os.path.join(BUILD, f"gemm_fast_{pair.lower()}.o")
-        steps.append([HIPCC, *FLAGS, f"-DTGE_PAIR_{pair}", "-c",
-                      os.path.join(CSRC, "gemm_fast.hip"), "-o", obj])
-    for pair in SKINNY_PAIRS:
-        obj = os.path.join(BUILD, f"gemm_skinny_{pair.lower()}.o")
-        steps.append([HIPCC, *FLAGS, f"-DTGE_PAIR_{pair}", "-c",
-                      os.path.join(CSRC, "gemm_skinny.hip"), "-o", obj])
-    for name in ("gemm_complex", "gemm_diag", "gemm_repack"):
-        steps.append([HIPCC, *FLAGS, "-c", os.path.join(CSRC, name + ".hip"), "-o",
-                      os.path.join(BUILD, name + ".o")])
-    api_obj = os.path.join(BUILD, "gemm_api.o")
-    steps.append([HIPCC, *FLAGS, "-x", "hip", "-c", os.path.join(CSRC, "gemm_api.cpp"), "-o", api_obj])
+    cmds = steps()
     with cf.ThreadPoolExecutor(jobs) as ex:
-        list(ex.map(lambda c: _run(c, verbose), steps))
-    objs = [s[-1] for s in steps]
+        list(ex.map(lambda c: _run(c, verbose), cmds))
+    objs = [s[-1] for s in cmds]
     tmp = LIB + ".tmp"
     _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB)

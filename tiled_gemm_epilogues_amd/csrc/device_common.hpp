@@ -246,6 +246,183 @@ __device__ __forceinline__ void raster(int id, int tiles_m, int tiles_n, int gro
     tn = in / gm;
 }
 
+// ---- groups ----------------------------------------------------------------------------------
+
+template <int GRP>
+using ParamsOf = typename std::conditional<GRP == GROUP_NONE, GemmParams, GroupedParams>::type;
+
+// A pointer that is the same in every lane, in scalar registers (the direct-to-LDS loads take
+// their base from there).
+__device__ __forceinline__ const uint8_t *uniform_ptr(const uint8_t *q) {
+    const uint64_t v = reinterpret_cast<uint64_t>(q);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return reinterpret_cast<const uint8_t *>((uint64_t)hi << 32 | lo);
+}
+
+// Range e of the offsets, clamped to [0, rows] and never negative.
+__device__ __forceinline__ void group_range(const GroupedParams &p, int e, int &lo, int &hi) {
+    lo = min(max(p.offs[e], 0), p.rows);
+    hi = max(min(p.offs[e + 1], p.rows), lo);
+}
+
+// Inclusive scans over the wave's 64 lanes (values >= 0), with the data-parallel lane moves: a
+// shift by 1, 2, 4, 8 inside each row of 16 lanes, then the last lane of rows 0 and 2 into rows 1
+// and 3, then lane 31 into rows 2 and 3.  Lanes without a source keep 0.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int lane_move(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ int wave_scan_add(int v) {
+    v += lane_move<0x111, 0xf>(v);
+    v += lane_move<0x112, 0xf>(v);
+    v += lane_move<0x114, 0xf>(v);
+    v += lane_move<0x118, 0xf>(v);
+    v += lane_move<0x142, 0xa>(v);
+    v += lane_move<0x143, 0xc>(v);
+    return v;
+}
+__device__ __forceinline__ int wave_scan_max(int v) {
+    v = max(v, lane_move<0x111, 0xf>(v));
+    v = max(v, lane_move<0x112, 0xf>(v));
+    v = max(v, lane_move<0x114, 0xf>(v));
+    v = max(v, lane_move<0x118, 0xf>(v));
+    v = max(v, lane_move<0x142, 0xa>(v));
+    v = max(v, lane_move<0x143, 0xc>(v));
+    return v;
+}
+
+// The ranges e0 .. e0+63, one per lane, with their tiles of bm rows: starts are the running
+// maximum of the clamped offsets (ordered offsets are their own), so that the ranges never overlap
+// and the launch's bound on the number of tiles holds for any offsets.  `carry`: the maximum
+// before e0, moved on.
+struct RangeChunk {
+    int lo, hi, mine, incl;   // the lane's range, its tiles, and the tiles of lanes 0 .. lane
+};
+__device__ __forceinline__ RangeChunk range_chunk(const GroupedParams &p, int e0, int bm, int &carry) {
+    const int e = e0 + (int)(threadIdx.x & 63);
+    const bool in = e < p.groups;
+    const int a = in ? p.offs[e] : 0, b = in ? p.offs[e + 1] : 0;
+    RangeChunk c;
+    c.lo = max(wave_scan_max(min(max(a, 0), p.rows)), carry);
+    c.hi = max(min(b, p.rows), c.lo);
+    carry = __builtin_amdgcn_readlane(c.hi, 63);
+    c.mine = in ? (c.hi - c.lo + bm - 1) / bm * p.tiles_n : 0;
+    c.incl = wave_scan_add(c.mine);
+    return c;
+}
+
+// GROUP_ROWS: workgroup wg -> an expert, bm of its rows and a column tile.  The launch has a
+// workgroup for every tile that `rows` rows in `groups` ranges can need; the real count is known
+// from the offsets, read here by every wave (64 ranges at a time, one per lane): a workgroup past
+// it has no tile (false).  The tiles of one expert are consecutive and each XCD takes a contiguous
+// run of them, so an expert's weights stay with few XCDs' L2.  On return the pointers stand at
+// the tile's first row (so that 32-bit offsets inside the tile are enough however long A and D
+// are), p.M is the number of the expert's rows from there on, and tn the column tile.
+template <int EAB, int ECD>
+__device__ __forceinline__ bool select_rows(GroupedParams &p, int wg, int bm, int &tn) {
+    int carry = 0, total = 0, e0 = 0;
+    RangeChunk c;
+    for (;; e0 += 64) {
+        c = range_chunk(p, e0, bm, carry);
+        total += __builtin_amdgcn_readlane(c.incl, 63);
+        if (e0 + 64 >= p.groups) break;
+    }
+    if (wg >= total) return false;
+    int id = xcd_remap(wg, total);
+    if (p.groups > 64) {   // more than one chunk: find the one that holds id
+        carry = 0;
+        for (e0 = 0;; e0 += 64) {
+            c = range_chunk(p, e0, bm, carry);
+            const int n = __builtin_amdgcn_readlane(c.incl, 63);
+            if (id < n) break;
+            id -= n;
+        }
+    }
+    const int src = __ffsll((unsigned long long)__ballot(c.incl > id)) - 1;   // id < the chunk's tiles
+    id -= __builtin_amdgcn_readlane(c.incl, src) - __builtin_amdgcn_readlane(c.mine, src);
+    const int lo = __builtin_amdgcn_readlane(c.lo, src), hi = __builtin_amdgcn_readlane(c.hi, src);
+    const int e = e0 + src;
+    int tm;
+    raster(id, (hi - lo + bm - 1) / bm, p.tiles_n, p.group_m, tm, tn);
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    tn = __builtin_amdgcn_readfirstlane(tn);
+    const int64_t row = lo + (int64_t)tm * bm;
+    p.M = __builtin_amdgcn_readfirstlane(hi - (int)row);
+    p.A = uniform_ptr(static_cast<const uint8_t *>(p.A) + row * p.lda * EAB);
+    p.B = uniform_ptr(static_cast<const uint8_t *>(p.B) + e * p.stride_b * EAB);
+    if (p.C) p.C = static_cast<const uint8_t *>(p.C) + row * p.ldc * ECD;
+    p.D = static_cast<uint8_t *>(p.D) + row * p.ldc * ECD;
+    if (p.bias) p.bias = static_cast<const uint8_t *>(p.bias) + e * p.stride_bias * 4;
+    return true;
+}
+
+// GROUP_K: workgroup id -> a product and a tile of it.  All products have the same tiles; the
+// tiles of one product are spread over the XCDs in contiguous runs (the ranges' lengths differ,
+// so whole products per XCD would leave some XCDs with the long ones).
+template <int EAB, int ECD>
+__device__ __forceinline__ void select_k(GroupedParams &p, int id, int &tm, int &tn) {
+    const int per = p.tiles_m * p.tiles_n;
+    const int e = __builtin_amdgcn_readfirstlane(id / per);
+    int lo, hi;
+    group_range(p, e, lo, hi);
+    raster(xcd_remap(id - e * per, per), p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    tn = __builtin_amdgcn_readfirstlane(tn);
+    p.K = __builtin_amdgcn_readfirstlane(hi - lo);
+    p.A = uniform_ptr(static_cast<const uint8_t *>(p.A) + (int64_t)lo * p.lda * EAB);
+    p.B = uniform_ptr(static_cast<const uint8_t *>(p.B) + (int64_t)lo * p.ldb * EAB);
+    if (p.C) p.C = static_cast<const uint8_t *>(p.C) + e * p.stride_c * ECD;
+    p.D = static_cast<uint8_t *>(p.D) + e * p.stride_c * ECD;
+}
+
+// GROUP_K: the column sums of B over one range (the gradient of a bias added to its rows), as
+// extra workgroups of 256 threads in front of the products': COLSUM_COLS columns of one range,
+// 16 rows at a time, the 16 partial sums of a column added through `part` (256 x 8 floats of LDS).
+// Sums are in fp32 and in a fixed order.  These workgroups read B once more (a part of what the
+// products' workgroups read, N / M-th of A's bytes per tile row) beside the MFMA-bound ones.
+constexpr int COLSUM_COLS = 128;
+template <class T>
+__device__ __forceinline__ void colsum_block(const GroupedParams &p, int id, float *part) {
+    const int nb = (p.N + COLSUM_COLS - 1) / COLSUM_COLS;
+    const int e = id / nb, tid = threadIdx.x;
+    const int n = (id - e * nb) * COLSUM_COLS + (tid & 15) * 8;
+    int lo, hi;
+    group_range(p, e, lo, hi);
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = 0.0f;
+    const T *B = static_cast<const T *>(p.B);
+    if (n + 8 <= p.N) {
+#pragma unroll 4
+        for (int r = lo + (tid >> 4); r < hi; r += 16) {
+            T v[8];
+            __builtin_memcpy(v, B + (int64_t)r * p.ldb + n, sizeof(v));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] += (float)v[i];
+        }
+    } else if (n < p.N) {
+        for (int r = lo + (tid >> 4); r < hi; r += 16)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (n + i < p.N) s[i] += (float)B[(int64_t)r * p.ldb + n + i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[tid * 8 + i] = s[i];
+    __syncthreads();
+    if (tid < COLSUM_COLS) {
+        const int col = (id - e * nb) * COLSUM_COLS + tid;
+        float t = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) t += part[(r * 16 + (tid >> 3)) * 8 + (tid & 7)];
+        if (col < p.N) p.colsum[(int64_t)e * p.N + col] = t;
+    }
+}
+// how many of them a launch has
+__device__ __forceinline__ int colsum_blocks(const GroupedParams &p) {
+    return p.colsum ? p.groups * ((p.N + COLSUM_COLS - 1) / COLSUM_COLS) : 0;
+}
+
 // ---- epilogue --------------------------------------------------------------------------------
 
 // Epilogue of a wave's MFMA tiles.  Lane l holds, for 32x32 tile (i, j), accumulator register
@@ -253,9 +430,10 @@ __device__ __forceinline__ void raster(int id, int tiles_m, int tiles_n, int gro
 // columns are loaded once, the C values of one 32-row block are loaded together before any of
 // its stores (C == D is allowed: every element is read before the same lane writes it), so the
 // loads overlap instead of each waiting for the store before it.
+// gate (float outputs): D = C > 0 ? alpha * acc : 0 in place of the sum with beta * C.
 template <class O, class Acc, class AccV, int TM, int TN>
 __device__ __forceinline__ void store_tile(const GemmParams &p, int mbase, int nbase, int lane,
-                                           AccV (&acc)[TM][TN]) {
+                                           AccV (&acc)[TM][TN], const bool gate = false) {
     using T = typename O::T;
     constexpr bool INT = std::is_same<Acc, int>::value;
     using B = typename std::conditional<INT, int, float>::type;
@@ -316,7 +494,8 @@ __device__ __forceinline__ void store_tile(const GemmParams &p, int mbase, int n
                         out[e] = (T)t;
                     } else {
                         float t = p.alpha * acc[i][j][4 * g + e];
-                        if (p.has_beta) t += p.beta * c_in_f(cv[j][g][e], p.xform_c);
+                        if (gate) t = (float)cv[j][g][e] > 0.0f ? t : 0.0f;
+                        else if (p.has_beta) t += p.beta * c_in_f(cv[j][g][e], p.xform_c);
                         t += bv[j][g][e];
                         if (p.relu) t = t > 0.0f ? t : 0.0f;
                         out[e] = (T)t;

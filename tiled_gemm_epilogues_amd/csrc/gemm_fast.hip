@@ -362,8 +362,10 @@ struct EpiMap {
     __device__ static int bgroup(int q) { return MF == 32 ? q : (q % NBG); }
 };
 
-template <class O, class Acc, int MF, bool BETA, bool FULL, class AccV, int NF>
-__device__ __forceinline__ void store_tile_staged(const GemmParams &p, int mbase, int nbase, int lane,
+// GATE (grouped products, float outputs): with p.gate, D = C > 0 ? alpha * acc : 0 in place of
+// the sum with beta * C.
+template <class O, class Acc, int MF, bool BETA, bool FULL, int GRP, class AccV, int NF>
+__device__ __forceinline__ void store_tile_staged(const ParamsOf<GRP> &p, int mbase, int nbase, int lane,
                                                   AccV (&acc)[NF][NF], uint8_t *stg) {
     using T = typename O::T;
     constexpr int WT = NF * MF;            // wave tile
@@ -386,7 +388,8 @@ __device__ __forceinline__ void store_tile_staged(const GemmParams &p, int mbase
     // workgroups than CUs), streaming stores keep the L2 and the infinity cache for the A and B
     // panels those rounds read (measured with the 16x16 shape: 3-8 % faster at 8192^3); in a
     // single round, and with the 32x32 shape, the plain stores measured faster
-    const bool stream_d = MF == 16 && (int64_t)p.tiles_m * p.tiles_n * p.batch > (WT == 128 ? 256 : 512);
+    const bool stream_d = GRP != GROUP_NONE ? gridDim.x > (WT == 128 ? 256 : 512)
+                          : MF == 16 && (int64_t)p.tiles_m * p.tiles_n * p.batch > (WT == 128 ? 256 : 512);
     typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
     // accumulator value e of group q in block b
     auto accv = [&](int b, int q, int e) -> Acc {
@@ -451,7 +454,12 @@ __device__ __forceinline__ void store_tile_staged(const GemmParams &p, int mbase
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     t[e] = __builtin_fmaf(p.alpha, accv(b, q, e), bq[e]);
-                    if constexpr (BETA) t[e] = __builtin_fmaf(p.beta, c_in_f(cv[q][e], p.xform_c), t[e]);
+                    if constexpr (BETA && GRP == GROUP_ROWS) {
+                        const float c = (float)cv[q][e];
+                        t[e] = p.gate ? (c > 0.0f ? t[e] : 0.0f) : __builtin_fmaf(p.beta, c, t[e]);
+                    } else if constexpr (BETA) {
+                        t[e] = __builtin_fmaf(p.beta, c_in_f(cv[q][e], p.xform_c), t[e]);
+                    }
                     if (p.relu) t[e] = __builtin_fmaxf(t[e], 0.0f);
                 }
                 if constexpr (ES == 2) {
@@ -500,18 +508,18 @@ __device__ __forceinline__ void store_tile_staged(const GemmParams &p, int mbase
     }
 }
 
-template <class O, class Acc, int MF, class AccV, int NF>
-__device__ __forceinline__ void epilogue(const GemmParams &p, int mbase, int nbase, int lane,
+template <class O, class Acc, int MF, int GRP, class AccV, int NF>
+__device__ __forceinline__ void epilogue(const ParamsOf<GRP> &p, int mbase, int nbase, int lane,
                                          AccV (&acc)[NF][NF], uint8_t *stg) {
     // interior wave tiles (the common case) take a path with no edge checks
     constexpr int WT = NF * MF;
     const bool full = mbase + WT <= p.M && nbase + WT <= p.N;
     if (full) {
-        if (p.has_beta) store_tile_staged<O, Acc, MF, true, true>(p, mbase, nbase, lane, acc, stg);
-        else store_tile_staged<O, Acc, MF, false, true>(p, mbase, nbase, lane, acc, stg);
+        if (p.has_beta) store_tile_staged<O, Acc, MF, true, true, GRP>(p, mbase, nbase, lane, acc, stg);
+        else store_tile_staged<O, Acc, MF, false, true, GRP>(p, mbase, nbase, lane, acc, stg);
     } else {
-        if (p.has_beta) store_tile_staged<O, Acc, MF, true, false>(p, mbase, nbase, lane, acc, stg);
-        else store_tile_staged<O, Acc, MF, false, false>(p, mbase, nbase, lane, acc, stg);
+        if (p.has_beta) store_tile_staged<O, Acc, MF, true, false, GRP>(p, mbase, nbase, lane, acc, stg);
+        else store_tile_staged<O, Acc, MF, false, false, GRP>(p, mbase, nbase, lane, acc, stg);
     }
 }
 
@@ -535,9 +543,10 @@ struct Sched {
 // (global -> VGPR -> LDS, same LDS image) for layouts the direct loads cannot take; the load
 // transforms are then applied once per element on the way to LDS (XF stays off).  TL: the
 // workgroup tile (256; 128 for mid-size products: two workgroups per CU, 16x16 shape, direct
-// loads, no load transforms).
-template <class TI, class TO, bool AK, bool BK, int MF, bool XF, bool RS = false, int TL = 256>
-__global__ __launch_bounds__(NT, TL == 256 ? 1 : 2) void gemm_fast(GemmParams p) {
+// loads, no load transforms).  GRP: GroupMode of the launch (products grouped by expert).
+template <class TI, class TO, bool AK, bool BK, int MF, bool XF, bool RS = false, int TL = 256,
+          int GRP = GROUP_NONE>
+__global__ __launch_bounds__(NT, TL == 256 ? 1 : 2) void gemm_fast(ParamsOf<GRP> p) {
     static_assert(TL == 256 || (TL == 128 && MF == 16 && !XF && !RS), "tile variants");
     using acc_t = typename TI::acc_t;
     using accv_t = typename std::conditional<MF == 32, typename TI::accv_t, typename TI::accv16_t>::type;
@@ -563,9 +572,19 @@ __global__ __launch_bounds__(NT, TL == 256 ? 1 : 2) void gemm_fast(GemmParams p)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
 
-    // this workgroup's product and raster id inside it
-    const int lid = select_batch<TI::E, (int)sizeof(typename TO::T)>(p, xcd_remap(blockIdx.x, gridDim.x),
-                                                                    p.tiles_m * p.tiles_n);
+    // this workgroup's product and raster id inside it (grouped: the tile itself)
+    int lid = 0, gtm = 0, gtn = 0;
+    if constexpr (GRP == GROUP_ROWS) {
+        if (!select_rows<TI::E, (int)sizeof(typename TO::T)>(p, blockIdx.x, TL, gtn)) return;
+    } else if constexpr (GRP == GROUP_K) {
+        using TS = typename std::conditional<std::is_same<TI, TF16>::value, _Float16, __bf16>::type;
+        const int nc = colsum_blocks(p);
+        if ((int)blockIdx.x < nc) return colsum_block<TS>(p, blockIdx.x, reinterpret_cast<float *>(smem));
+        select_k<TI::E, (int)sizeof(typename TO::T)>(p, blockIdx.x - nc, gtm, gtn);
+    } else {
+        lid = select_batch<TI::E, (int)sizeof(typename TO::T)>(p, xcd_remap(blockIdx.x, gridDim.x),
+                                                               p.tiles_m * p.tiles_n);
+    }
 
     const uint8_t *A = static_cast<const uint8_t *>(p.A);
     const uint8_t *B = static_cast<const uint8_t *>(p.B);
@@ -580,8 +599,8 @@ __global__ __launch_bounds__(NT, TL == 256 ? 1 : 2) void gemm_fast(GemmParams p)
     u32x4 ra[RS ? NL : 1], rb[RS ? NL : 1];
     int m0 = 0, n0 = 0;
     auto set_tile = [&](int id) {
-        int tm, tn;
-        raster(id, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+        int tm = gtm, tn = gtn;
+        if constexpr (GRP == GROUP_NONE) raster(id, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
         m0 = tm * TL;
         n0 = tn * TL;
         la.init(wave, lane, m0, p.M, p.lda);
@@ -790,7 +809,7 @@ __global__ __launch_bounds__(NT, TL == 256 ? 1 : 2) void gemm_fast(GemmParams p)
     }
 
     // every wave's reads of the stage-1 buffers ended before the last slab's barrier
-    epilogue<TO, acc_t, MF>(p, m0 + wm * G::WT, n0 + wn * G::WT, lane, acc, stg);
+    epilogue<TO, acc_t, MF, GRP>(p, m0 + wm * G::WT, n0 + wn * G::WT, lane, acc, stg);
 }
 
 // MFMA shape of the fast path.  Both shapes give the same results (fp32/int32 accumulation of
@@ -863,9 +882,48 @@ const KernelEntry *lookup_fast128(int op_a, int op_b) {
     return &e[op_a * 2 + op_b];
 }
 
+// ---- grouped instances -------------------------------------------------------------------------
+
+template <class TI, class TO, int TL, bool AT, bool BT, int GRP>
+hipError_t launch_grouped(const GroupedParams &p, unsigned grid, hipStream_t s) {
+    constexpr int MF = TL == 256 ? fast_mf<AT, BT>() : 16;
+    hipLaunchKernelGGL((gemm_fast<TI, TO, !AT, BT, MF, false, false, TL, GRP>), dim3(grid), dim3(NT), 0, s, p);
+    return hipGetLastError();
+}
+
+template <class TI, class TO>
+const GroupedEntry *lookup_grouped(int mode, int op_b, int tile) {
+    if (tile != 256 && tile != 128) return nullptr;
+    const int i = tile == 256 ? 0 : 1;
+    static const GroupedEntry rows[4] = {
+        {launch_grouped<TI, TO, 256, false, false, GROUP_ROWS>, 256, 256, "gemm_fast_256x256"},
+        {launch_grouped<TI, TO, 128, false, false, GROUP_ROWS>, 128, 128, "gemm_fast_128x128"},
+        {launch_grouped<TI, TO, 256, false, true, GROUP_ROWS>, 256, 256, "gemm_fast_256x256"},
+        {launch_grouped<TI, TO, 128, false, true, GROUP_ROWS>, 128, 128, "gemm_fast_128x128"}};
+    static const GroupedEntry k[2] = {
+        {launch_grouped<TI, TO, 256, true, false, GROUP_K>, 256, 256, "gemm_fast_256x256"},
+        {launch_grouped<TI, TO, 128, true, false, GROUP_K>, 128, 128, "gemm_fast_128x128"}};
+    if (mode == GROUP_ROWS && (op_b == 0 || op_b == 1)) return &rows[2 * op_b + i];
+    if (mode == GROUP_K && op_b == 0) return &k[i];
+    return nullptr;
+}
+
 }  // namespace
 
+#if defined(TGE_GROUPED)
+// the grouped instances are a build of their own (one object per type pair)
 #if defined(TGE_PAIR_F16_F16)
+const GroupedEntry *grouped_fast_f16_f16(int m, int b, int t) { return lookup_grouped<TF16, OF16>(m, b, t); }
+#elif defined(TGE_PAIR_F16_F32)
+const GroupedEntry *grouped_fast_f16_f32(int m, int b, int t) { return lookup_grouped<TF16, OF32>(m, b, t); }
+#elif defined(TGE_PAIR_BF16_BF16)
+const GroupedEntry *grouped_fast_bf16_bf16(int m, int b, int t) { return lookup_grouped<TBF16, OBF16>(m, b, t); }
+#elif defined(TGE_PAIR_BF16_F32)
+const GroupedEntry *grouped_fast_bf16_f32(int m, int b, int t) { return lookup_grouped<TBF16, OF32>(m, b, t); }
+#else
+#error "define one TGE_PAIR_* macro of a 16-bit float type"
+#endif
+#elif defined(TGE_PAIR_F16_F16)
 const KernelEntry *fast_f16_f16(int a, int b, int rs) { return lookup_fast<TF16, OF16>(a, b, rs); }
 const KernelEntry *fast128_f16_f16(int a, int b) { return lookup_fast128<TF16, OF16>(a, b); }
 #elif defined(TGE_PAIR_F16_F32)

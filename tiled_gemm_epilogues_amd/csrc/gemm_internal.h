@@ -33,6 +33,28 @@ struct GemmParams {
 
 using LaunchFn = hipError_t (*)(const GemmParams &, unsigned grid, hipStream_t);
 
+// One launch of products grouped by expert: the operands' rows are cut into `groups` ranges,
+// range e = [offs[e], offs[e+1]) with offs in device memory (groups + 1 values).
+//   GROUP_ROWS  the ranges cut the rows of A, C and D; range e is multiplied by B + e * stride_b
+//               (bias + e * stride_bias); M is set per workgroup
+//   GROUP_K     the ranges cut the product's K, the stored rows of both operands (A stored
+//               transposed, B not): product e sums over range e into D + e * stride_c; K is set
+//               per workgroup
+// A range is clamped to [0, rows], so that no offset makes a kernel leave the operands.
+enum GroupMode { GROUP_NONE = 0, GROUP_ROWS = 1, GROUP_K = 2 };
+struct GroupedParams : GemmParams {
+    const int32_t *offs;
+    int groups, rows;
+    int gate;                // GROUP_ROWS: D = C > 0 ? alpha * product : 0 (has_beta set: C is read)
+    float *colsum;           // GROUP_K: column sums of B per range, groups x N (nullptr: none)
+};
+using GroupedLaunchFn = hipError_t (*)(const GroupedParams &, unsigned grid, hipStream_t);
+struct GroupedEntry {
+    GroupedLaunchFn launch;
+    int bm, bn;              // workgroup tile
+    const char *name;
+};
+
 // One compiled kernel variant and its tile shape.
 struct KernelEntry {
     LaunchFn launch;
@@ -169,5 +191,25 @@ hipError_t finish_bf16_bf16(const GemmParams &p, hipStream_t s);
 hipError_t finish_bf16_f32(const GemmParams &p, hipStream_t s);
 // int8 -> int32 (gemm_repack.hip): int32 partial sums in ws, one product (batch 1)
 hipError_t finish_i8_i32(const GemmParams &p, hipStream_t s);
+
+// Grouped products (the same kernels with the group selection compiled in).  mode: GroupMode;
+// op_b: 0 = N, 1 = T (GROUP_K: 0).  Preconditions as for the kernels above, for every range:
+//   any    the general kernel, tile CFG_128 or CFG_64: none
+//   fast   tile 256 or 128, direct loads: 16-byte aligned pointers, leading dimensions and strides;
+//          GROUP_ROWS: K >= 64, N % 8 == 0 when op_b is N; GROUP_K: M % 8 == 0 and N % 8 == 0
+//   skinny GROUP_ROWS, 16 * mt rows per workgroup: fast's, and K % 32 == 0
+const GroupedEntry *grouped_any_f32_f32(int mode, int op_b, int cfg);
+const GroupedEntry *grouped_any_f16_f16(int mode, int op_b, int cfg);
+const GroupedEntry *grouped_any_f16_f32(int mode, int op_b, int cfg);
+const GroupedEntry *grouped_any_bf16_bf16(int mode, int op_b, int cfg);
+const GroupedEntry *grouped_any_bf16_f32(int mode, int op_b, int cfg);
+const GroupedEntry *grouped_fast_f16_f16(int mode, int op_b, int tile);
+const GroupedEntry *grouped_fast_f16_f32(int mode, int op_b, int tile);
+const GroupedEntry *grouped_fast_bf16_bf16(int mode, int op_b, int tile);
+const GroupedEntry *grouped_fast_bf16_f32(int mode, int op_b, int tile);
+const GroupedEntry *grouped_skinny_f16_f16(int op_b, int mt);
+const GroupedEntry *grouped_skinny_f16_f32(int op_b, int mt);
+const GroupedEntry *grouped_skinny_bf16_bf16(int op_b, int mt);
+const GroupedEntry *grouped_skinny_bf16_f32(int op_b, int mt);
 
 }  // namespace tge

@@ -141,8 +141,9 @@ struct Stager<E, BMN, NT, false> {
 
 // ---- the kernel ------------------------------------------------------------------------------
 
-template <int BM, int BN, int WGM, int WGN, class TI, class TO, bool AT, bool BT>
-__global__ __launch_bounds__(WGM * WGN * 64, 1) void gemm_mfma(GemmParams p) {
+// GRP: GroupMode of the launch (products grouped by expert; GROUP_NONE: a plain or batched one)
+template <int BM, int BN, int WGM, int WGN, class TI, class TO, bool AT, bool BT, int GRP = GROUP_NONE>
+__global__ __launch_bounds__(WGM * WGN * 64, 1) void gemm_mfma(ParamsOf<GRP> p) {
     constexpr int NT = WGM * WGN * 64;
     constexpr int E = TI::E;
     constexpr int BK = 128 / E;            // K elements per slab (128 bytes)
@@ -158,10 +159,21 @@ __global__ __launch_bounds__(WGM * WGN * 64, 1) void gemm_mfma(GemmParams p) {
     const int lane = tid & 63, wave = tid >> 6;
     const int wm = wave / WGN, wn = wave % WGN;
 
-    int tile_m, tile_n;
-    const int tid_in = select_batch<TI::E, (int)sizeof(typename TO::T)>(
-        p, xcd_remap(blockIdx.x, gridDim.x), p.tiles_m * p.tiles_n);
-    raster(tid_in, p.tiles_m, p.tiles_n, p.group_m, tile_m, tile_n);
+    int tile_m = 0, tile_n;
+    if constexpr (GRP == GROUP_ROWS) {
+        if (!select_rows<TI::E, (int)sizeof(typename TO::T)>(p, blockIdx.x, BM, tile_n)) return;
+    } else if constexpr (GRP == GROUP_K) {
+        static_assert(NT == 256 && STAGE >= 256 * 8 * 4, "column sums: 256 threads and their LDS");
+        using TS = typename std::conditional<std::is_same<TI, TF16>::value, _Float16,
+                   typename std::conditional<std::is_same<TI, TBF16>::value, __bf16, float>::type>::type;
+        const int nc = colsum_blocks(p);
+        if ((int)blockIdx.x < nc) return colsum_block<TS>(p, blockIdx.x, reinterpret_cast<float *>(smem));
+        select_k<TI::E, (int)sizeof(typename TO::T)>(p, blockIdx.x - nc, tile_m, tile_n);
+    } else {
+        const int tid_in = select_batch<TI::E, (int)sizeof(typename TO::T)>(
+            p, xcd_remap(blockIdx.x, gridDim.x), p.tiles_m * p.tiles_n);
+        raster(tid_in, p.tiles_m, p.tiles_n, p.group_m, tile_m, tile_n);
+    }
     const int m0 = tile_m * BM, n0 = tile_n * BN;
     const int m_valid = p.M - m0, n_valid = p.N - n0;
     const bool mn_interior = m_valid >= BM && n_valid >= BN;
@@ -230,7 +242,8 @@ __global__ __launch_bounds__(WGM * WGN * 64, 1) void gemm_mfma(GemmParams p) {
         __syncthreads();
     }
 
-    store_tile<TO, acc_t>(p, m0 + wm * WTM, n0 + wn * WTN, lane, acc);
+    if constexpr (GRP == GROUP_ROWS) store_tile<TO, acc_t>(p, m0 + wm * WTM, n0 + wn * WTN, lane, acc, p.gate);
+    else store_tile<TO, acc_t>(p, m0 + wm * WTM, n0 + wn * WTN, lane, acc);
 }
 
 template <int BM, int BN, int WGM, int WGN, class TI, class TO, bool AT, bool BT>
@@ -265,9 +278,49 @@ const KernelEntry *lookup(int op_a, int op_b, int cfg) {
     return nullptr;
 }
 
+// ---- grouped instances: 128- and 64-wide tiles, any alignment ---------------------------------
+
+template <int BM, class TI, class TO, bool AT, bool BT, int GRP>
+hipError_t launch_grouped(const GroupedParams &p, unsigned grid, hipStream_t s) {
+    hipLaunchKernelGGL((gemm_mfma<BM, BM, 2, 2, TI, TO, AT, BT, GRP>), dim3(grid), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+template <class TI, class TO>
+const GroupedEntry *lookup_grouped(int mode, int op_b, int cfg) {
+    if (cfg != CFG_128 && cfg != CFG_64) return nullptr;
+    const int i = cfg == CFG_128 ? 0 : 1;
+    static const GroupedEntry rows[4] = {
+        {launch_grouped<128, TI, TO, false, false, GROUP_ROWS>, 128, 128, "gemm_mfma_128x128"},
+        {launch_grouped<64, TI, TO, false, false, GROUP_ROWS>, 64, 64, "gemm_mfma_64x64"},
+        {launch_grouped<128, TI, TO, false, true, GROUP_ROWS>, 128, 128, "gemm_mfma_128x128"},
+        {launch_grouped<64, TI, TO, false, true, GROUP_ROWS>, 64, 64, "gemm_mfma_64x64"}};
+    static const GroupedEntry k[2] = {
+        {launch_grouped<128, TI, TO, true, false, GROUP_K>, 128, 128, "gemm_mfma_128x128"},
+        {launch_grouped<64, TI, TO, true, false, GROUP_K>, 64, 64, "gemm_mfma_64x64"}};
+    if (mode == GROUP_ROWS && (op_b == 0 || op_b == 1)) return &rows[2 * op_b + i];
+    if (mode == GROUP_K && op_b == 0) return &k[i];
+    return nullptr;
+}
+
 }  // namespace
 
+#if defined(TGE_GROUPED)
+// the grouped instances are a build of their own (one object per type pair)
 #if defined(TGE_PAIR_F32_F32)
+const GroupedEntry *grouped_any_f32_f32(int m, int b, int c) { return lookup_grouped<TF32, OF32>(m, b, c); }
+#elif defined(TGE_PAIR_F16_F16)
+const GroupedEntry *grouped_any_f16_f16(int m, int b, int c) { return lookup_grouped<TF16, OF16>(m, b, c); }
+#elif defined(TGE_PAIR_F16_F32)
+const GroupedEntry *grouped_any_f16_f32(int m, int b, int c) { return lookup_grouped<TF16, OF32>(m, b, c); }
+#elif defined(TGE_PAIR_BF16_BF16)
+const GroupedEntry *grouped_any_bf16_bf16(int m, int b, int c) { return lookup_grouped<TBF16, OBF16>(m, b, c); }
+#elif defined(TGE_PAIR_BF16_F32)
+const GroupedEntry *grouped_any_bf16_f32(int m, int b, int c) { return lookup_grouped<TBF16, OF32>(m, b, c); }
+#else
+#error "define one TGE_PAIR_* macro of a float type"
+#endif
+#elif defined(TGE_PAIR_F32_F32)
 const KernelEntry *kernels_f32_f32(int a, int b, int c) { return lookup<TF32, OF32>(a, b, c); }
 #elif defined(TGE_PAIR_F16_F16)
 const KernelEntry *kernels_f16_f16(int a, int b, int c) { return lookup<TF16, OF16>(a, b, c); }

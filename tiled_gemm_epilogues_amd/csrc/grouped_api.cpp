@@ -1,0 +1,289 @@
+// C ABI of the products grouped by expert: plan creation and validation, kernel choice, launch.
+// Host code only; the kernels are the grouped instances of gemm_kernels.hip, gemm_fast.hip and
+// gemm_skinny.hip.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <stdio.h>
+#include <string.h>
+
+#include <new>
+
+#include "../../include/gemm.h"
+#include "gemm_internal.h"
+
+using tge::GroupedEntry;
+using tge::GroupedParams;
+
+struct gemm_grouped_plan {
+    int mode;                        // tge::GROUP_ROWS or GROUP_K
+    int64_t rows, M, N, K, groups;   // K unused by GROUP_K, M by GROUP_ROWS
+    int64_t lda, ldb, ldc, stride_b, stride_bias, stride_c;
+    int ab, cd, epi;
+    const GroupedEntry *any;         // general kernel (always valid)
+    const GroupedEntry *fast;        // aligned pointers: the fast or skinny kernel, else nullptr
+    char desc[256];
+};
+
+namespace {
+
+constexpr int64_t LIM31 = (int64_t)1 << 31;
+constexpr int64_t MAX_GROUPS = (int64_t)1 << 20;
+constexpr int64_t FAST_MIN_K = 64;         // one slab of the fast kernel (16-bit inputs)
+constexpr int GROUP_M = 8;                 // tile rows per raster group, as in plain plans
+
+// The integer held by an enum field (C callers may store any int).
+template <class E>
+int bits(const E &e) {
+    static_assert(sizeof(E) == sizeof(int), "C ABI enums are int-sized");
+    int v;
+    memcpy(&v, &e, sizeof v);
+    return v;
+}
+
+bool in(int v, int lo, int hi) { return v >= lo && v <= hi; }
+
+int elem_bytes(int t) { return t == GEMM_F16 || t == GEMM_BF16 ? 2 : 4; }
+
+const char *type_name(int t) {
+    return t == GEMM_F16 ? "f16" : t == GEMM_BF16 ? "bf16" : "f32";
+}
+
+using TableFn = const GroupedEntry *(*)(int, int, int);
+using SkinnyFn = const GroupedEntry *(*)(int, int);
+
+TableFn any_table(int ab, int cd) {
+    if (ab == GEMM_F32 && cd == GEMM_F32) return tge::grouped_any_f32_f32;
+    if (ab == GEMM_F16 && cd == GEMM_F16) return tge::grouped_any_f16_f16;
+    if (ab == GEMM_F16 && cd == GEMM_F32) return tge::grouped_any_f16_f32;
+    if (ab == GEMM_BF16 && cd == GEMM_BF16) return tge::grouped_any_bf16_bf16;
+    if (ab == GEMM_BF16 && cd == GEMM_F32) return tge::grouped_any_bf16_f32;
+    return nullptr;
+}
+
+TableFn fast_table(int ab, int cd) {
+    if (ab == GEMM_F16) return cd == GEMM_F16 ? tge::grouped_fast_f16_f16 : tge::grouped_fast_f16_f32;
+    if (ab == GEMM_BF16) return cd == GEMM_BF16 ? tge::grouped_fast_bf16_bf16 : tge::grouped_fast_bf16_f32;
+    return nullptr;
+}
+
+SkinnyFn skinny_table(int ab, int cd) {
+    if (ab == GEMM_F16) return cd == GEMM_F16 ? tge::grouped_skinny_f16_f16 : tge::grouped_skinny_f16_f32;
+    if (ab == GEMM_BF16) return cd == GEMM_BF16 ? tge::grouped_skinny_bf16_bf16 : tge::grouped_skinny_bf16_f32;
+    return nullptr;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Row tiles of `bm` rows that `rows` rows in `groups` ranges can need at most: every non-empty
+// range has one begun tile, and the other rows fill whole ones.
+int64_t row_tiles(int64_t rows, int64_t groups, int64_t bm) {
+    const int64_t n = rows < groups ? rows : groups;
+    return n + (rows - n) / bm;
+}
+
+int64_t grid_of(const gemm_grouped_plan &p, const GroupedEntry &k, bool colsum) {
+    const int64_t tn = ceil_div(p.N, k.bn);
+    if (p.mode == tge::GROUP_ROWS) return row_tiles(p.rows, p.groups, k.bm) * tn;
+    return p.groups * (ceil_div(p.M, k.bm) * tn + (colsum ? ceil_div(p.N, 128) : 0));
+}
+
+// What both descriptions have in common: ranges, types, algorithm.  SUCCESS when they hold.
+gemm_status_t check_common(int64_t rows, int64_t N, int64_t MK, int64_t groups, int64_t lda, int64_t ldb,
+                           int64_t ldc, int ab, int cd) {
+    if (rows < 0 || N < 0 || MK < 0 || groups < 1) return GEMM_STATUS_INVALID_VALUE;
+    if (rows >= LIM31 || N >= LIM31 || MK >= LIM31 || lda >= LIM31 || ldb >= LIM31 || ldc >= LIM31 ||
+        groups >= MAX_GROUPS)
+        return GEMM_STATUS_NOT_SUPPORTED;
+    return any_table(ab, cd) ? GEMM_STATUS_SUCCESS : GEMM_STATUS_NOT_SUPPORTED;
+}
+
+bool aligned(const void *p, uintptr_t to) { return (uintptr_t)p % to == 0; }
+
+// The launch of either mode; the arguments have been checked.
+gemm_status_t launch(const gemm_grouped_plan &p, const void *A, const void *B, const void *C, void *D,
+                     const void *bias, float *colsum, const int32_t *offsets, float alpha, float beta,
+                     void *stream) {
+    GroupedParams prm = {};
+    prm.A = A; prm.B = B; prm.C = C; prm.D = D; prm.bias = bias;
+    prm.M = (int)p.M; prm.N = (int)p.N; prm.K = (int)p.K;
+    prm.lda = (int)p.lda; prm.ldb = (int)p.ldb; prm.ldc = (int)p.ldc;
+    prm.alpha = alpha; prm.beta = beta;
+    prm.gate = p.epi == GEMM_EPI_GATE;
+    prm.has_beta = beta != 0.0f || prm.gate;
+    prm.has_bias = bias != nullptr;
+    prm.relu = p.epi == GEMM_EPI_RELU || p.epi == GEMM_EPI_BIAS_RELU;
+    prm.group_m = GROUP_M;
+    prm.batch = prm.batch2 = 1;
+    prm.stride_b = p.stride_b; prm.stride_bias = p.stride_bias; prm.stride_c = p.stride_c;
+    prm.offs = offsets;
+    prm.groups = (int)p.groups;
+    prm.rows = (int)p.rows;
+    prm.colsum = colsum;
+    const GroupedEntry *k = p.fast && aligned(A, 16) && aligned(B, 16) ? p.fast : p.any;
+    prm.tiles_m = (int)ceil_div(p.M, k->bm);
+    prm.tiles_n = (int)ceil_div(p.N, k->bn);
+    const unsigned grid = (unsigned)grid_of(p, *k, colsum != nullptr);
+    if (grid == 0) return GEMM_STATUS_SUCCESS;
+    return k->launch(prm, grid, static_cast<hipStream_t>(stream)) == hipSuccess ? GEMM_STATUS_SUCCESS
+                                                                                : GEMM_STATUS_HIP_ERROR;
+}
+
+// Hands a finished plan out, with its description.
+gemm_status_t finish_plan(gemm_grouped_plan_t *out, const gemm_grouped_plan &p, const char *what) {
+    const GroupedEntry *k = p.fast ? p.fast : p.any;
+    if (grid_of(p, *p.any, true) >= LIM31 || grid_of(p, *k, true) >= LIM31) return GEMM_STATUS_NOT_SUPPORTED;
+    gemm_grouped_plan *q = new (std::nothrow) gemm_grouped_plan(p);
+    if (!q) return GEMM_STATUS_ALLOC_FAILED;
+    snprintf(q->desc, sizeof q->desc, "grouped %s %s %s->%s tile %dx%d groups %lld grid %lld", what, k->name,
+             type_name(p.ab), type_name(p.cd), k->bm, k->bn, (long long)p.groups,
+             (long long)grid_of(p, *k, false));
+    *out = q;
+    return GEMM_STATUS_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grouped_desc_t *d) {
+    if (!out) return GEMM_STATUS_INVALID_VALUE;
+    *out = nullptr;
+    if (!d) return GEMM_STATUS_INVALID_VALUE;
+    const int op_b = bits(d->op_b), ab = bits(d->ab_type), cd = bits(d->cd_type), epi = bits(d->epilogue),
+              algo = bits(d->algo), tile = d->tile;
+    if (!in(op_b, GEMM_OP_N, GEMM_OP_T) || !in(ab, GEMM_F32, GEMM_DF32) || !in(cd, GEMM_F32, GEMM_DF32) ||
+        !in(epi, GEMM_EPI_NONE, GEMM_EPI_GATE))
+        return GEMM_STATUS_INVALID_VALUE;
+    switch (algo) {
+    case GEMM_ALGO_AUTO: if (tile != 0) return GEMM_STATUS_INVALID_VALUE; break;
+    case GEMM_ALGO_FAST: if (tile != 0 && tile != 256 && tile != 128) return GEMM_STATUS_INVALID_VALUE; break;
+    case GEMM_ALGO_GENERAL: if (tile != 0 && tile != 128 && tile != 64) return GEMM_STATUS_INVALID_VALUE; break;
+    case GEMM_ALGO_SKINNY:
+        if (tile != 0 && tile != 16 && tile != 32 && tile != 48 && tile != 64) return GEMM_STATUS_INVALID_VALUE;
+        break;
+    default: return GEMM_STATUS_INVALID_VALUE;
+    }
+    const gemm_status_t st = check_common(d->rows, d->N, d->K, d->groups, d->lda, d->ldb, d->ldc, ab, cd);
+    if (st != GEMM_STATUS_SUCCESS) return st;
+    const int64_t min_ldb = op_b == GEMM_OP_N ? d->N : d->K;
+    if (d->lda < (d->K > 1 ? d->K : 1) || d->ldb < (min_ldb > 1 ? min_ldb : 1) ||
+        d->ldc < (d->N > 1 ? d->N : 1) || d->stride_b < 0 || d->stride_bias < 0)
+        return GEMM_STATUS_INVALID_VALUE;
+    const int eab = elem_bytes(ab);
+    // 32-bit offsets inside one expert's weights, 63-bit ones between them
+    const int64_t b_rows = op_b == GEMM_OP_N ? d->K : d->N;
+    const int64_t big = ((int64_t)1 << 62) / 8 / d->groups;
+    if ((b_rows > 0 && ((b_rows - 1) * d->ldb + min_ldb) * eab >= LIM31) || d->stride_b > big || d->stride_bias > big)
+        return GEMM_STATUS_NOT_SUPPORTED;
+
+    gemm_grouped_plan p = {};
+    p.mode = tge::GROUP_ROWS;
+    p.rows = d->rows; p.N = d->N; p.K = d->K; p.groups = d->groups;
+    p.lda = d->lda; p.ldb = d->ldb; p.ldc = d->ldc; p.stride_b = d->stride_b; p.stride_bias = d->stride_bias;
+    p.ab = ab; p.cd = cd; p.epi = epi;
+    const int64_t avg = ceil_div(d->rows, d->groups);   // rows of an expert, on average
+    const bool small = algo == GEMM_ALGO_GENERAL && tile ? tile == 64 : avg < 128 || d->N < 128;
+    p.any = any_table(ab, cd)(tge::GROUP_ROWS, op_b, small ? tge::CFG_64 : tge::CFG_128);
+    // direct loads: whole 16-byte chunks, and 32-bit offsets within a tile's rows
+    const bool fast_ok = eab == 2 && d->K >= FAST_MIN_K && d->lda % 8 == 0 && d->ldb % 8 == 0 &&
+                         d->stride_b % 8 == 0 && (op_b == GEMM_OP_T || (d->N % 8 == 0 && d->N > 0)) &&
+                         d->lda * eab * 256 < LIM31;
+    const bool skinny_ok = fast_ok && d->K % 32 == 0;
+    if (algo == GEMM_ALGO_SKINNY) {
+        if (skinny_ok) p.fast = skinny_table(ab, cd)(op_b, tile ? tile / 16 : 1);
+    } else if (algo == GEMM_ALGO_FAST) {
+        if (fast_ok) p.fast = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, tile ? tile : 128);
+    } else if (algo == GEMM_ALGO_AUTO && fast_ok) {
+        if (skinny_ok && avg <= 32) p.fast = skinny_table(ab, cd)(op_b, avg <= 8 ? 1 : avg <= 16 ? 2 : 4);
+        else p.fast = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, avg >= 1024 ? 256 : 128);
+    }
+    char what[16];
+    snprintf(what, sizeof what, "rows N%c", op_b == GEMM_OP_N ? 'N' : 'T');
+    return finish_plan(out, p, what);
+}
+
+gemm_status_t gemm_grouped_grad_plan_create(gemm_grouped_plan_t *out, const gemm_grouped_grad_desc_t *d) {
+    if (!out) return GEMM_STATUS_INVALID_VALUE;
+    *out = nullptr;
+    if (!d) return GEMM_STATUS_INVALID_VALUE;
+    const int ab = bits(d->ab_type), cd = bits(d->cd_type), algo = bits(d->algo), tile = d->tile;
+    if (!in(ab, GEMM_F32, GEMM_DF32) || !in(cd, GEMM_F32, GEMM_DF32)) return GEMM_STATUS_INVALID_VALUE;
+    switch (algo) {
+    case GEMM_ALGO_AUTO: if (tile != 0) return GEMM_STATUS_INVALID_VALUE; break;
+    case GEMM_ALGO_FAST: if (tile != 0 && tile != 256 && tile != 128) return GEMM_STATUS_INVALID_VALUE; break;
+    case GEMM_ALGO_GENERAL: if (tile != 0 && tile != 128 && tile != 64) return GEMM_STATUS_INVALID_VALUE; break;
+    default: return GEMM_STATUS_INVALID_VALUE;
+    }
+    const gemm_status_t st = check_common(d->rows, d->N, d->M, d->groups, d->lda, d->ldb, d->ldc, ab, cd);
+    if (st != GEMM_STATUS_SUCCESS) return st;
+    const int64_t span = d->M > 0 && d->N > 0 ? (d->M - 1) * d->ldc + d->N : 0;
+    if (d->lda < (d->M > 1 ? d->M : 1) || d->ldb < (d->N > 1 ? d->N : 1) || d->ldc < (d->N > 1 ? d->N : 1) ||
+        d->stride_c < 0 || (d->groups > 1 && d->stride_c < span))
+        return GEMM_STATUS_INVALID_VALUE;
+    if (d->stride_c > ((int64_t)1 << 62) / 8 / d->groups) return GEMM_STATUS_NOT_SUPPORTED;
+
+    gemm_grouped_plan p = {};
+    p.mode = tge::GROUP_K;
+    p.rows = d->rows; p.M = d->M; p.N = d->N; p.groups = d->groups;
+    p.lda = d->lda; p.ldb = d->ldb; p.ldc = d->ldc; p.stride_c = d->stride_c;
+    p.ab = ab; p.cd = cd; p.epi = GEMM_EPI_NONE;
+    const int eab = elem_bytes(ab);
+    const bool small = algo == GEMM_ALGO_GENERAL && tile ? tile == 64 : d->M < 128 || d->N < 128;
+    p.any = any_table(ab, cd)(tge::GROUP_K, 0, small ? tge::CFG_64 : tge::CFG_128);
+    const bool fast_ok = eab == 2 && d->M % 8 == 0 && d->N % 8 == 0 && d->M > 0 && d->N > 0 && d->lda % 8 == 0 &&
+                         d->ldb % 8 == 0 && d->lda * eab * 256 < LIM31 && d->ldb * eab * 256 < LIM31;
+    if (fast_ok && algo == GEMM_ALGO_FAST) p.fast = fast_table(ab, cd)(tge::GROUP_K, 0, tile ? tile : 128);
+    else if (fast_ok && algo == GEMM_ALGO_AUTO) p.fast = fast_table(ab, cd)(tge::GROUP_K, 0, 128);
+    return finish_plan(out, p, "gradient TN");
+}
+
+// Checks shared by the two runs.
+static gemm_status_t check_run(gemm_grouped_plan_t p, int mode, const void *A, const void *B, const void *C,
+                               const void *D, const int32_t *offsets, float alpha, float beta, bool needs_c) {
+    if (!p || p->mode != mode) return GEMM_STATUS_INVALID_VALUE;
+    if (alpha != alpha || beta != beta) return GEMM_STATUS_INVALID_VALUE;   // NaN scalars
+    const int eab = elem_bytes(p->ab), ecd = elem_bytes(p->cd);
+    const bool has_d = mode == tge::GROUP_ROWS || p->M > 0;   // a gradient plan may have only sums
+    if ((has_d && !D) || !offsets || !aligned(offsets, 4) || !aligned(D, ecd)) return GEMM_STATUS_INVALID_VALUE;
+    const bool has_k = mode == tge::GROUP_ROWS ? p->K > 0 : p->rows > 0;
+    if (has_k && (!A || !B || !aligned(A, eab) || !aligned(B, eab))) return GEMM_STATUS_INVALID_VALUE;
+    if (needs_c && (!C || !aligned(C, ecd))) return GEMM_STATUS_INVALID_VALUE;
+    return GEMM_STATUS_SUCCESS;
+}
+
+gemm_status_t gemm_grouped_run(gemm_grouped_plan_t p, const void *A, const void *B, const void *C, void *D,
+                               const void *bias, const int32_t *offsets, float alpha, float beta, void *stream) {
+    if (!p || p->mode != tge::GROUP_ROWS) return GEMM_STATUS_INVALID_VALUE;
+    if (p->rows == 0 || p->N == 0) return GEMM_STATUS_SUCCESS;
+    const bool gate = p->epi == GEMM_EPI_GATE;
+    const gemm_status_t st = check_run(p, tge::GROUP_ROWS, A, B, C, D, offsets, alpha, beta, gate || beta != 0.0f);
+    if (st != GEMM_STATUS_SUCCESS) return st;
+    if (gate && beta != 0.0f) return GEMM_STATUS_INVALID_VALUE;
+    const bool has_bias = p->epi == GEMM_EPI_BIAS || p->epi == GEMM_EPI_BIAS_RELU;
+    if (has_bias && (!bias || !aligned(bias, 4))) return GEMM_STATUS_INVALID_VALUE;
+    return launch(*p, A, B, C, D, has_bias ? bias : nullptr, nullptr, offsets, alpha, beta, stream);
+}
+
+gemm_status_t gemm_grouped_grad_run(gemm_grouped_plan_t p, const void *A, const void *B, const void *C, void *D,
+                                    float *bias_grad, const int32_t *offsets, float alpha, float beta,
+                                    void *stream) {
+    if (!p || p->mode != tge::GROUP_K) return GEMM_STATUS_INVALID_VALUE;
+    if (p->N == 0 || (p->M == 0 && !bias_grad)) return GEMM_STATUS_SUCCESS;
+    const gemm_status_t st = check_run(p, tge::GROUP_K, A, B, C, D, offsets, alpha, beta, beta != 0.0f);
+    if (st != GEMM_STATUS_SUCCESS) return st;
+    if (!aligned(bias_grad, 4)) return GEMM_STATUS_INVALID_VALUE;
+    return launch(*p, A, B, C, D, nullptr, bias_grad, offsets, alpha, beta, stream);
+}
+
+gemm_status_t gemm_grouped_plan_destroy(gemm_grouped_plan_t p) {
+    delete p;
+    return GEMM_STATUS_SUCCESS;
+}
+
+gemm_status_t gemm_grouped_plan_describe(gemm_grouped_plan_t p, char *buf, size_t len) {
+    if (!p || !buf || len == 0) return GEMM_STATUS_INVALID_VALUE;
+    snprintf(buf, len, "%s", p->desc);
+    return GEMM_STATUS_SUCCESS;
+}
+
+}  // extern "C"
