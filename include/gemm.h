@@ -397,8 +397,8 @@ typedef struct {
 /*
  * Host-only, like gemm_plan_create.  Return INVALID_VALUE for a NULL argument, a negative size,
  * groups < 1, a leading dimension or stride below its minimum, or an enum or tile out of range;
- * NOT_SUPPORTED for a type pair outside the table, a size, leading dimension or group count of
- * 2^31, 2^31 or 2^20 and more, one expert's B spanning 2^31 bytes or more, or a grid of 2^31
+ * NOT_SUPPORTED for a type pair outside the table, a size or leading dimension of 2^31 or more, 2^20
+ * groups or more, one expert's B spanning 2^31 bytes or more, or a grid of 2^31
  * workgroups; ALLOC_FAILED without host memory.
  */
 gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grouped_desc_t *desc);
@@ -428,6 +428,66 @@ gemm_status_t gemm_grouped_plan_destroy(gemm_grouped_plan_t plan);
 
 /* The plan's kernel as text, like gemm_plan_describe. */
 gemm_status_t gemm_grouped_plan_describe(gemm_grouped_plan_t plan, char *buf, size_t len);
+
+/* ---- products with 4-bit weights ------------------------------------------------------------
+ *
+ *   D = act(alpha * A * W^T + beta * C + bias),
+ *   W[n][k] = scales[n][k / block] * (code[n][k] - zeros[n][k / block])
+ *
+ * A is rows x K, C and D rows x N, row-major; W has N rows of K codes of 4 bits (0 .. 15), two per
+ * byte along k: the low half of byte k / 2 is an even k.  scales have the type of A, zeros are
+ * uint8; without zeros the zero point is 8.  The sum over a block is taken with exact weights
+ * (code - zero) in fp32, multiplied by its scale in fp32 and added up in fp32: no weight is
+ * rounded.  With groups > 1 there is one W (and bias) per expert and D is computed for the row
+ * ranges that offsets give, as for the products grouped by expert above; with groups == 1 offsets
+ * may be NULL (all rows).
+ *
+ * Types: F16 -> F16 | F32, BF16 -> BF16 | F32; bias is fp32.  No alignment beyond the elements'
+ * own is required.  A plan holds no device memory.
+ */
+typedef struct gemm_quant_plan *gemm_quant_plan_t;
+
+/*
+ * block: 32, 64 or a multiple of 128; K is a multiple of it.  lda, ldc in elements; ldq: bytes
+ * between rows of codes (>= K / 2); lds: elements between rows of scales and of zeros (>= K /
+ * block); stride_q (bytes), stride_s, stride_bias: from expert to expert.  zeros: 1 when the runs
+ * pass zero points, 0 otherwise.  algo: AUTO, or SKINNY (tile 16, 32 or 64 rows: K split over the
+ * waves of a workgroup, for few rows) or FAST (128 x 128 tiles) to pin a kernel.
+ */
+typedef struct {
+    int64_t rows, N, K, block, groups;
+    int64_t lda, ldq, lds, ldc, stride_q, stride_s, stride_bias;
+    gemm_dtype_t ab_type, cd_type;
+    gemm_epilogue_t epilogue;
+    int32_t zeros;
+    gemm_algo_t algo;
+    int32_t tile;
+} gemm_quant_desc_t;
+
+/*
+ * Host-only.  Returns INVALID_VALUE for a NULL argument, a negative size or stride, groups or block
+ * < 1, K not a multiple of block, a leading dimension below its minimum, or an enum, flag or tile
+ * out of range (GATE included); NOT_SUPPORTED for another type pair or block, or a size beyond
+ * the limits (rows, N, 2 K and leading dimensions below 2^31, groups below 2^20, a grid below 2^31
+ * workgroups); ALLOC_FAILED without host memory.
+ */
+gemm_status_t gemm_quant_plan_create(gemm_quant_plan_t *out, const gemm_quant_desc_t *desc);
+
+/*
+ * Enqueues the product on `stream`: one kernel, no allocation, no synchronisation.  zeros is read
+ * by a plan with zeros only, C when beta != 0 (C == D is allowed), bias when the epilogue has one.
+ * Returns INVALID_VALUE for a NULL plan, a missing pointer (offsets with groups > 1 included), a
+ * pointer off its element's alignment or a NaN scalar; HIP_ERROR when the launch fails.
+ */
+gemm_status_t gemm_quant_run(gemm_quant_plan_t plan, const void *A, const void *Q, const void *scales,
+                             const void *zeros, const void *C, void *D, const void *bias,
+                             const int32_t *offsets, float alpha, float beta, void *stream);
+
+/* Frees a plan (NULL is a no-op).  Always returns SUCCESS. */
+gemm_status_t gemm_quant_plan_destroy(gemm_quant_plan_t plan);
+
+/* The plan's kernel as text, like gemm_plan_describe. */
+gemm_status_t gemm_quant_plan_describe(gemm_quant_plan_t plan, char *buf, size_t len);
 
 #ifdef __cplusplus
 }

@@ -7,7 +7,8 @@ ABI (include/gemm.h).  The low-level functions carry the C names (gemm_plan_crea
 gemm_run_noalloc, gemm_plan_create_batched, gemm_plan_create_desc, gemm_plan_destroy,
 gemm_status_string, gemm_plan_describe); `Plan` wraps them for torch tensors, whose device
 memory and streams are the only things taken from PyTorch.  `GroupedPlan` and `GroupedGradPlan`
-wrap the products grouped by expert (gemm_grouped_*) the same way.
+wrap the products grouped by expert (gemm_grouped_*) the same way, `QuantPlan` the products with
+4-bit weights (gemm_quant_*).
 
 The library is loaded on first use, not at import, so that the build module of this package
 can run on a checkout that has no library yet.  There is no fallback: the first call fails with
@@ -40,7 +41,9 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 EXPORTED = ("gemm_plan_create", "gemm_plan_create_batched", "gemm_plan_create_desc", "gemm_run",
             "gemm_run_noalloc", "gemm_plan_destroy", "gemm_status_string", "gemm_plan_describe",
             "gemm_grouped_plan_create", "gemm_grouped_grad_plan_create", "gemm_grouped_run",
-            "gemm_grouped_grad_run", "gemm_grouped_plan_destroy", "gemm_grouped_plan_describe")
+            "gemm_grouped_grad_run", "gemm_grouped_plan_destroy", "gemm_grouped_plan_describe",
+            "gemm_quant_plan_create", "gemm_quant_run", "gemm_quant_plan_destroy",
+            "gemm_quant_plan_describe")
 
 _i64, _vp, _ci, _f = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
 
@@ -69,6 +72,15 @@ class GroupedGradDesc(ctypes.Structure):
     _fields_ = [("rows", _i64), ("M", _i64), ("N", _i64), ("groups", _i64), ("lda", _i64),
                 ("ldb", _i64), ("ldc", _i64), ("stride_c", _i64), ("ab_type", _ci),
                 ("cd_type", _ci), ("algo", _ci), ("tile", ctypes.c_int32)]
+
+
+class QuantDesc(ctypes.Structure):
+    """gemm_quant_desc_t of include/gemm.h."""
+    _fields_ = [("rows", _i64), ("N", _i64), ("K", _i64), ("block", _i64), ("groups", _i64),
+                ("lda", _i64), ("ldq", _i64), ("lds", _i64), ("ldc", _i64), ("stride_q", _i64),
+                ("stride_s", _i64), ("stride_bias", _i64), ("ab_type", _ci), ("cd_type", _ci),
+                ("epilogue", _ci), ("zeros", ctypes.c_int32), ("algo", _ci),
+                ("tile", ctypes.c_int32)]
 
 
 _lib = None
@@ -111,8 +123,14 @@ def lib():
     L.gemm_grouped_grad_run.argtypes = [_vp] * 7 + [_f, _f, _vp]
     L.gemm_grouped_plan_destroy.argtypes = [_vp]
     L.gemm_grouped_plan_describe.argtypes = [_vp, ctypes.c_char_p, ctypes.c_size_t]
+    L.gemm_quant_plan_create.argtypes = [ctypes.POINTER(_vp), ctypes.POINTER(QuantDesc)]
+    L.gemm_quant_run.argtypes = [_vp] * 9 + [_f, _f, _vp]
+    L.gemm_quant_plan_destroy.argtypes = [_vp]
+    L.gemm_quant_plan_describe.argtypes = [_vp, ctypes.c_char_p, ctypes.c_size_t]
     for fn in ("gemm_grouped_plan_create", "gemm_grouped_grad_plan_create", "gemm_grouped_run",
-               "gemm_grouped_grad_run", "gemm_grouped_plan_destroy", "gemm_grouped_plan_describe"):
+               "gemm_grouped_grad_run", "gemm_grouped_plan_destroy", "gemm_grouped_plan_describe",
+               "gemm_quant_plan_create", "gemm_quant_run", "gemm_quant_plan_destroy",
+               "gemm_quant_plan_describe"):
         getattr(L, fn).restype = _ci
     _lib = L
     return _lib
@@ -223,6 +241,32 @@ def gemm_grouped_plan_destroy(plan):
 def gemm_grouped_plan_describe(plan):
     buf = ctypes.create_string_buffer(256)
     st = lib().gemm_grouped_plan_describe(plan, buf, 256)
+    return st, buf.value.decode()
+
+
+def gemm_quant_plan_create(rows, N, K, block, groups, lda, ldq, lds, ldc, stride_q, stride_s,
+                           stride_bias, ab_type, cd_type, epilogue, zeros, algo="auto", tile=0):
+    """Returns (status, handle) of a plan with 4-bit weights."""
+    d = QuantDesc(rows, N, K, block, groups, lda, ldq, lds, ldc, stride_q, stride_s, stride_bias,
+                  _enum(DTYPE, ab_type), _enum(DTYPE, cd_type), _enum(EPILOGUE, epilogue), int(zeros),
+                  _enum(ALGO, algo), int(tile))
+    h = _vp()
+    st = lib().gemm_quant_plan_create(ctypes.byref(h), ctypes.byref(d))
+    return st, h.value
+
+
+def gemm_quant_run(plan, A, Q, scales, zeros, C, D, bias, offsets, alpha, beta, stream):
+    """Raw pointers (ints or None) and a hipStream_t handle (int or None)."""
+    return lib().gemm_quant_run(plan, A, Q, scales, zeros, C, D, bias, offsets, alpha, beta, stream)
+
+
+def gemm_quant_plan_destroy(plan):
+    return lib().gemm_quant_plan_destroy(plan)
+
+
+def gemm_quant_plan_describe(plan):
+    buf = ctypes.create_string_buffer(256)
+    st = lib().gemm_quant_plan_describe(plan, buf, 256)
     return st, buf.value.decode()
 
 
@@ -421,17 +465,18 @@ class _GroupedBase:
     """What the plans over row ranges share: the handle, and the checks of a run's tensors."""
 
     _h = None
+    _destroy, _describe = staticmethod(gemm_grouped_plan_destroy), staticmethod(gemm_grouped_plan_describe)
 
     @property
     def handle(self):
         return self._h
 
     def describe(self):
-        return gemm_grouped_plan_describe(self._h)[1]
+        return self._describe(self._h)[1]
 
     def close(self):
         if getattr(self, "_h", None):
-            gemm_grouped_plan_destroy(self._h)
+            self._destroy(self._h)
             self._h = None
 
     def __del__(self):
@@ -569,3 +614,63 @@ class GroupedGradPlan(_GroupedBase):
             float(alpha), float(beta), self._stream(stream, dev))
         if st != STATUS_SUCCESS:
             raise GemmError(st, "gemm_grouped_grad_run")
+
+
+class QuantPlan(_GroupedBase):
+    """Products with 4-bit weights (see include/gemm.h): D = act(alpha * A * W^T + beta * C + bias),
+    W[n][k] = scales[n][k // block] * (code[n][k] - zeros[n][k // block]).  Q is uint8, N x K / 2
+    (low half of a byte: even k), scales (A's type) and zeros (uint8, where the plan has them) are N
+    x K / block; with groups > 1 all of them, and bias, are stacks with one entry per expert, and
+    the rows of an expert are those the offsets give.  Strides default to packed stacks."""
+
+    _destroy, _describe = staticmethod(gemm_quant_plan_destroy), staticmethod(gemm_quant_plan_describe)
+
+    def __init__(self, rows, N, K, block, groups=1, zeros=False, lda=None, ldq=None, lds=None,
+                 ldc=None, stride_q=None, stride_s=None, stride_bias=None, ab="f16", cd="f16",
+                 epilogue="none", algo="auto", tile=0):
+        import torch
+        self.rows, self.N, self.K, self.block, self.groups = rows, N, K, block, groups
+        self.zeros, self.ab, self.cd, self.epilogue = bool(zeros), ab, cd, epilogue
+        nb = K // block if block > 0 else 0
+        self.lda = lda if lda is not None else max(1, K)
+        self.ldq = ldq if ldq is not None else K // 2
+        self.lds = lds if lds is not None else nb
+        self.ldc = ldc if ldc is not None else max(1, N)
+        self.stride_q = stride_q if stride_q is not None else N * self.ldq
+        self.stride_s = stride_s if stride_s is not None else N * self.lds
+        self.stride_bias = stride_bias if stride_bias is not None else N
+        st, h = gemm_quant_plan_create(rows, N, K, block, groups, self.lda, self.ldq, self.lds,
+                                       self.ldc, self.stride_q, self.stride_s, self.stride_bias, ab,
+                                       cd, epilogue, self.zeros, algo, tile)
+        if st != STATUS_SUCCESS:
+            raise GemmError(st, "gemm_quant_plan_create")
+        self._h = h
+        tab, tcd = _torch_dtype(ab), _torch_dtype(cd)
+        cdn = _span(rows, N, self.ldc)
+        more = groups - 1
+        sn = more * self.stride_s + _span(N, nb, self.lds) if N and nb else 0
+        self._spec = {
+            "A": (tab, _span(rows, K, self.lda), self.lda),
+            "Q": (torch.uint8, more * self.stride_q + _span(N, K // 2, self.ldq) if N and K else 0,
+                  self.ldq),
+            "scales": (tab, sn, self.lds), "zeros": (torch.uint8, sn, self.lds),
+            "C": (tcd, cdn, self.ldc), "D": (tcd, cdn, self.ldc),
+            "bias": (torch.float32, more * self.stride_bias + N if N else 0, None),
+            "offsets": (torch.int32, groups + 1, None)}
+        self._has_bias = epilogue in ("bias", "bias_relu", 2, 3)
+
+    def run(self, A, Q, scales, zeros, C, D, offsets=None, bias=None, alpha=1.0, beta=0.0,
+            stream=None):
+        """Enqueue on `stream` (as Plan.run).  zeros: None for a plan without them; offsets: as in
+        GroupedPlan.run, None with one weight matrix for all rows; C is read when beta != 0.  Raises
+        ValueError / TypeError before anything is enqueued when a tensor does not fit the plan."""
+        import torch
+        dev = torch.cuda.current_device()
+        ptr = self._ptr
+        st = lib().gemm_quant_run(
+            self._h, ptr("A", A, dev), ptr("Q", Q, dev), ptr("scales", scales, dev),
+            ptr("zeros", zeros, dev) if self.zeros else None, ptr("C", C, dev) if beta != 0 else None,
+            ptr("D", D, dev), ptr("bias", bias, dev) if self._has_bias else None,
+            ptr("offsets", offsets, dev), float(alpha), float(beta), self._stream(stream, dev))
+        if st != STATUS_SUCCESS:
+            raise GemmError(st, "gemm_quant_run")

@@ -52,9 +52,11 @@ def steps():
                         ("gemm_skinny", GROUPED_PAIRS)):
         for pair in pairs:
             add(name + ".hip", f"grouped_{name}_{pair.lower()}", f"-DTGE_PAIR_{pair}", "-DTGE_GROUPED")
+    for pair in GROUPED_PAIRS:
+        add("gemm_quant.hip", f"gemm_quant_{pair.lower()}", f"-DTGE_PAIR_{pair}")
     for name in ("gemm_complex", "gemm_diag", "gemm_repack"):
         add(name + ".hip", name)
-    for name in ("gemm_api", "grouped_api"):
+    for name in ("gemm_api", "grouped_api", "quant_api"):
         add(name + ".cpp", name, host=True)
     return out
 

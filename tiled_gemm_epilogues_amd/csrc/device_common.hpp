@@ -318,9 +318,10 @@ __device__ __forceinline__ RangeChunk range_chunk(const GroupedParams &p, int e0
 // it has no tile (false).  The tiles of one expert are consecutive and each XCD takes a contiguous
 // run of them, so an expert's weights stay with few XCDs' L2.  On return the pointers stand at
 // the tile's first row (so that 32-bit offsets inside the tile are enough however long A and D
-// are), p.M is the number of the expert's rows from there on, and tn the column tile.
+// are), p.M is the number of the expert's rows from there on, and tn the column tile; `expert`,
+// where given, receives the expert.
 template <int EAB, int ECD>
-__device__ __forceinline__ bool select_rows(GroupedParams &p, int wg, int bm, int &tn) {
+__device__ __forceinline__ bool select_rows(GroupedParams &p, int wg, int bm, int &tn, int *expert = nullptr) {
     int carry = 0, total = 0, e0 = 0;
     RangeChunk c;
     for (;; e0 += 64) {
@@ -343,6 +344,7 @@ __device__ __forceinline__ bool select_rows(GroupedParams &p, int wg, int bm, in
     id -= __builtin_amdgcn_readlane(c.incl, src) - __builtin_amdgcn_readlane(c.mine, src);
     const int lo = __builtin_amdgcn_readlane(c.lo, src), hi = __builtin_amdgcn_readlane(c.hi, src);
     const int e = e0 + src;
+    if (expert) *expert = e;
     int tm;
     raster(id, (hi - lo + bm - 1) / bm, p.tiles_n, p.group_m, tm, tn);
     tm = __builtin_amdgcn_readfirstlane(tm);

@@ -212,4 +212,33 @@ const GroupedEntry *grouped_skinny_f16_f32(int op_b, int mt);
 const GroupedEntry *grouped_skinny_bf16_bf16(int op_b, int mt);
 const GroupedEntry *grouped_skinny_bf16_f32(int op_b, int mt);
 
+// Products with 4-bit weights (gemm_quant.hip): W_e[n][k] = scale * (code - zero), codes packed
+// two per byte along k (low half: even k), one scale (of A's type) and zero point (uint8; nullptr:
+// 8) per `block` consecutive k.  offs == nullptr: one weight matrix for all rows.
+struct QuantParams : GroupedParams {
+    const uint8_t *Q;        // codes: expert e, row n at Q + e * stride_q + n * ldq (bytes)
+    const void *scales;      // expert e, row n, block b at e * stride_s + n * lds + b (elements)
+    const uint8_t *zeros;    // laid out like the scales
+    int64_t stride_q, stride_s;
+    int ldq, lds, block;
+};
+using QuantLaunchFn = hipError_t (*)(const QuantParams &, unsigned grid, hipStream_t);
+struct QuantEntry {
+    QuantLaunchFn launch;
+    int bm, bn;              // workgroup tile
+    const char *name;
+};
+// block: 32, 64, or 128 for every multiple of 128 (K a multiple of the block).  No alignment
+// preconditions beyond the elements' own.
+//   rows:  16 * mt rows (mt 1, 2 or 4), K split over the waves of a workgroup
+//   tile:  128 x 128 tiles
+const QuantEntry *quant_rows_f16_f16(int block, int mt);
+const QuantEntry *quant_rows_f16_f32(int block, int mt);
+const QuantEntry *quant_rows_bf16_bf16(int block, int mt);
+const QuantEntry *quant_rows_bf16_f32(int block, int mt);
+const QuantEntry *quant_tile_f16_f16(int block);
+const QuantEntry *quant_tile_f16_f32(int block);
+const QuantEntry *quant_tile_bf16_bf16(int block);
+const QuantEntry *quant_tile_bf16_f32(int block);
+
 }  // namespace tge

@@ -4,13 +4,14 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
-#include <string.h>
 
 #include <new>
 
 #include "../../include/gemm.h"
 #include "gemm_internal.h"
+#include "host_common.h"
 
+using namespace tge::host;
 using tge::GroupedEntry;
 using tge::GroupedParams;
 
@@ -26,27 +27,7 @@ struct gemm_grouped_plan {
 
 namespace {
 
-constexpr int64_t LIM31 = (int64_t)1 << 31;
-constexpr int64_t MAX_GROUPS = (int64_t)1 << 20;
 constexpr int64_t FAST_MIN_K = 64;         // one slab of the fast kernel (16-bit inputs)
-constexpr int GROUP_M = 8;                 // tile rows per raster group, as in plain plans
-
-// The integer held by an enum field (C callers may store any int).
-template <class E>
-int bits(const E &e) {
-    static_assert(sizeof(E) == sizeof(int), "C ABI enums are int-sized");
-    int v;
-    memcpy(&v, &e, sizeof v);
-    return v;
-}
-
-bool in(int v, int lo, int hi) { return v >= lo && v <= hi; }
-
-int elem_bytes(int t) { return t == GEMM_F16 || t == GEMM_BF16 ? 2 : 4; }
-
-const char *type_name(int t) {
-    return t == GEMM_F16 ? "f16" : t == GEMM_BF16 ? "bf16" : "f32";
-}
 
 using TableFn = const GroupedEntry *(*)(int, int, int);
 using SkinnyFn = const GroupedEntry *(*)(int, int);
@@ -72,15 +53,6 @@ SkinnyFn skinny_table(int ab, int cd) {
     return nullptr;
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Row tiles of `bm` rows that `rows` rows in `groups` ranges can need at most: every non-empty
-// range has one begun tile, and the other rows fill whole ones.
-int64_t row_tiles(int64_t rows, int64_t groups, int64_t bm) {
-    const int64_t n = rows < groups ? rows : groups;
-    return n + (rows - n) / bm;
-}
-
 int64_t grid_of(const gemm_grouped_plan &p, const GroupedEntry &k, bool colsum) {
     const int64_t tn = ceil_div(p.N, k.bn);
     if (p.mode == tge::GROUP_ROWS) return row_tiles(p.rows, p.groups, k.bm) * tn;
@@ -96,8 +68,6 @@ gemm_status_t check_common(int64_t rows, int64_t N, int64_t MK, int64_t groups, 
         return GEMM_STATUS_NOT_SUPPORTED;
     return any_table(ab, cd) ? GEMM_STATUS_SUCCESS : GEMM_STATUS_NOT_SUPPORTED;
 }
-
-bool aligned(const void *p, uintptr_t to) { return (uintptr_t)p % to == 0; }
 
 // The launch of either mode; the arguments have been checked.
 gemm_status_t launch(const gemm_grouped_plan &p, const void *A, const void *B, const void *C, void *D,
