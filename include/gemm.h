@@ -468,8 +468,8 @@ typedef struct {
  * Host-only.  Returns INVALID_VALUE for a NULL argument, a negative size or stride, groups or block
  * < 1, K not a multiple of block, a leading dimension below its minimum, or an enum, flag or tile
  * out of range (GATE included); NOT_SUPPORTED for another type pair or block, or a size beyond
- * the limits (rows, N, 2 K and leading dimensions below 2^31, groups below 2^20, a grid below 2^31
- * workgroups); ALLOC_FAILED without host memory.
+ * the limits (rows, N and leading dimensions below 2^31, K below 2^23, groups below 2^20, a grid
+ * below 2^31 workgroups); ALLOC_FAILED without host memory.
  */
 gemm_status_t gemm_quant_plan_create(gemm_quant_plan_t *out, const gemm_quant_desc_t *desc);
 

@@ -251,13 +251,19 @@ __device__ __forceinline__ void raster(int id, int tiles_m, int tiles_n, int gro
 template <int GRP>
 using ParamsOf = typename std::conditional<GRP == GROUP_NONE, GemmParams, GroupedParams>::type;
 
-// A pointer that is the same in every lane, in scalar registers (the direct-to-LDS loads take
-// their base from there).
-__device__ __forceinline__ const uint8_t *uniform_ptr(const uint8_t *q) {
-    const uint64_t v = reinterpret_cast<uint64_t>(q);
+// A value that is the same in every lane, in scalar registers.
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-    return reinterpret_cast<const uint8_t *>((uint64_t)hi << 32 | lo);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+// The base of a grouped kernel's direct-to-LDS loads, which take it from scalar registers.  Only
+// for those: ordinary loads through a pointer rebuilt from its halves would be flat loads, which
+// also wait for LDS.
+template <int GRP>
+__device__ __forceinline__ const uint8_t *dma_base(const void *q) {
+    if constexpr (GRP == GROUP_NONE) return static_cast<const uint8_t *>(q);
+    else return reinterpret_cast<const uint8_t *>(uniform64(reinterpret_cast<int64_t>(q)));
 }
 
 // Range e of the offsets, clamped to [0, rows] and never negative.
@@ -302,7 +308,8 @@ struct RangeChunk {
 __device__ __forceinline__ RangeChunk range_chunk(const GroupedParams &p, int e0, int bm, int &carry) {
     const int e = e0 + (int)(threadIdx.x & 63);
     const bool in = e < p.groups;
-    const int a = in ? p.offs[e] : 0, b = in ? p.offs[e + 1] : 0;
+    // lanes past the last range read the last offset: both loads are in flight together
+    const int a = p.offs[min(e, p.groups)], b = p.offs[min(e + 1, p.groups)];
     RangeChunk c;
     c.lo = max(wave_scan_max(min(max(a, 0), p.rows)), carry);
     c.hi = max(min(b, p.rows), c.lo);
@@ -351,8 +358,8 @@ __device__ __forceinline__ bool select_rows(GroupedParams &p, int wg, int bm, in
     tn = __builtin_amdgcn_readfirstlane(tn);
     const int64_t row = lo + (int64_t)tm * bm;
     p.M = __builtin_amdgcn_readfirstlane(hi - (int)row);
-    p.A = uniform_ptr(static_cast<const uint8_t *>(p.A) + row * p.lda * EAB);
-    p.B = uniform_ptr(static_cast<const uint8_t *>(p.B) + e * p.stride_b * EAB);
+    p.A = static_cast<const uint8_t *>(p.A) + uniform64(row * p.lda * EAB);
+    p.B = static_cast<const uint8_t *>(p.B) + uniform64(e * p.stride_b * EAB);
     if (p.C) p.C = static_cast<const uint8_t *>(p.C) + row * p.ldc * ECD;
     p.D = static_cast<uint8_t *>(p.D) + row * p.ldc * ECD;
     if (p.bias) p.bias = static_cast<const uint8_t *>(p.bias) + e * p.stride_bias * 4;
@@ -372,8 +379,8 @@ __device__ __forceinline__ void select_k(GroupedParams &p, int id, int &tm, int 
     tm = __builtin_amdgcn_readfirstlane(tm);
     tn = __builtin_amdgcn_readfirstlane(tn);
     p.K = __builtin_amdgcn_readfirstlane(hi - lo);
-    p.A = uniform_ptr(static_cast<const uint8_t *>(p.A) + (int64_t)lo * p.lda * EAB);
-    p.B = uniform_ptr(static_cast<const uint8_t *>(p.B) + (int64_t)lo * p.ldb * EAB);
+    p.A = static_cast<const uint8_t *>(p.A) + uniform64((int64_t)lo * p.lda * EAB);
+    p.B = static_cast<const uint8_t *>(p.B) + uniform64((int64_t)lo * p.ldb * EAB);
     if (p.C) p.C = static_cast<const uint8_t *>(p.C) + e * p.stride_c * ECD;
     p.D = static_cast<uint8_t *>(p.D) + e * p.stride_c * ECD;
 }

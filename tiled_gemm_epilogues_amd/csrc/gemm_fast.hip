@@ -586,8 +586,8 @@ __global__ __launch_bounds__(NT, TL == 256 ? 1 : 2) void gemm_fast(ParamsOf<GRP>
                                                                p.tiles_m * p.tiles_n);
     }
 
-    const uint8_t *A = static_cast<const uint8_t *>(p.A);
-    const uint8_t *B = static_cast<const uint8_t *>(p.B);
+    const uint8_t *A = dma_base<GRP>(p.A);
+    const uint8_t *B = dma_base<GRP>(p.B);
     const uint32_t lds0 = lds_addr(smem);
     uint8_t *const stg = smem + (wave < 2 ? 0 : G::OPND) + G::KC + (wave & 1) * STG;
 
@@ -793,8 +793,8 @@ __global__ __launch_bounds__(NT, TL == 256 ? 1 : 2) void gemm_fast(ParamsOf<GRP>
     if (k0 < p.K) {
         TailStage<E, AK, MF, TL> ta;
         TailStage<E, BK, MF, TL> tb;
-        ta.fetch(A, p.lda, m0, p.M, k0, p.K, tid);
-        tb.fetch(B, p.ldb, n0, p.N, k0, p.K, tid);
+        ta.fetch(static_cast<const uint8_t *>(p.A), p.lda, m0, p.M, k0, p.K, tid);
+        tb.fetch(static_cast<const uint8_t *>(p.B), p.ldb, n0, p.N, k0, p.K, tid);
         __syncthreads();
         ta.put(smem, tid, RS ? p.xform_a : 0);
         tb.put(smem + G::OPND, tid, RS ? p.xform_b : 0);

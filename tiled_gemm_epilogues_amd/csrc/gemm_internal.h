@@ -221,6 +221,7 @@ struct QuantParams : GroupedParams {
     const uint8_t *zeros;    // laid out like the scales
     int64_t stride_q, stride_s;
     int ldq, lds, block;
+    uint64_t block_rcp;      // ceil(2^32 / (block / 128)) for blocks of 128 and more
 };
 using QuantLaunchFn = hipError_t (*)(const QuantParams &, unsigned grid, hipStream_t);
 struct QuantEntry {
@@ -230,12 +231,13 @@ struct QuantEntry {
 };
 // block: 32, 64, or 128 for every multiple of 128 (K a multiple of the block).  No alignment
 // preconditions beyond the elements' own.
-//   rows:  16 * mt rows (mt 1, 2 or 4), K split over the waves of a workgroup
+//   rows:  16 * mt x 16 * cg tiles, K split over the waves of a workgroup; (mt, cg) = (1, 1), (1, 4),
+//          (2, 1), (2, 2), (4, 1) or (4, 2)
 //   tile:  128 x 128 tiles
-const QuantEntry *quant_rows_f16_f16(int block, int mt);
-const QuantEntry *quant_rows_f16_f32(int block, int mt);
-const QuantEntry *quant_rows_bf16_bf16(int block, int mt);
-const QuantEntry *quant_rows_bf16_f32(int block, int mt);
+const QuantEntry *quant_rows_f16_f16(int block, int mt, int cg);
+const QuantEntry *quant_rows_f16_f32(int block, int mt, int cg);
+const QuantEntry *quant_rows_bf16_bf16(int block, int mt, int cg);
+const QuantEntry *quant_rows_bf16_f32(int block, int mt, int cg);
 const QuantEntry *quant_tile_f16_f16(int block);
 const QuantEntry *quant_tile_f16_f32(int block);
 const QuantEntry *quant_tile_bf16_bf16(int block);

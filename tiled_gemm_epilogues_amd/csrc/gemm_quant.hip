@@ -18,12 +18,13 @@
 // with sum A from one more matrix instruction per A fragment, against a fragment of ones.  The
 // terms are at most 31 / 8 times larger than a centred sum's: two bits of fp32's 24.
 //
-// A lane of a 16x16x32 matrix instruction holds 8 k of one weight row (n = lane % 16).  A 16-byte
-// load of a lane covers 32 k of its row: lanes g = lane / 16 hold k = 32g .. 32g+31 of a chunk of
-// 128.  With G >= 128 the chunk's four instructions may take any 8 of each lane.  With G = 64 and
-// 32 an instruction must stay inside one block: the four words are exchanged between the lane
-// groups (permlane32_swap, then permlane16_swap) so that word i belongs to block i / 2, or i.
-// kofs() is the resulting k of word i in lane group g; A is loaded to match.
+// A lane of a 16x16x32 matrix instruction holds 8 k of one weight row (n = lane % 16), its lane
+// group g = lane / 16 saying which 8 of 32.  A 16-byte load of a lane covers 32 k of its row: lane
+// group g holds k = 32g .. 32g+31 of a chunk of 128, while instruction i is to take k = 32i .. 32i+31
+// (so that it stays inside one block, and a load of A's rows covers whole 64-byte pieces): word i
+// of lane group g and word g of lane group i change places, a 4 x 4 transposition over the lane
+// groups with two exchanges between the halves of the wave (permlane32_swap) and two between
+// neighbouring groups (permlane16_swap).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -38,28 +39,13 @@ using namespace dev;
 
 constexpr int CHUNK = 128;    // k per step: 16 bytes of codes per lane
 
-// first of the 8 k (within a chunk) of word i in lane group g
-template <int G>
-__device__ __forceinline__ int kofs(int i, int g) {
-    if constexpr (G >= 128) return 32 * g + 8 * i;
-    else if constexpr (G == 64) return 64 * (i >> 1) + 32 * (g & 1) + 16 * (g >> 1) + 8 * (i & 1);
-    else return 32 * i + 8 * g;
-}
-
-// the four words of a lane's 16 code bytes, exchanged between the lane groups (see above)
-template <int G>
+// the four words of a lane's 16 code bytes, transposed over the lane groups (see above)
 __device__ __forceinline__ u32x4 exchange(u32x4 w) {
-    if constexpr (G <= 64) {
-        const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-        const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-        w = u32x4{a[0], b[0], a[1], b[1]};
-    }
-    if constexpr (G <= 32) {
-        const auto a = __builtin_amdgcn_permlane16_swap(w[0], w[1], false, false);
-        const auto b = __builtin_amdgcn_permlane16_swap(w[2], w[3], false, false);
-        w = u32x4{a[0], a[1], b[0], b[1]};
-    }
-    return w;
+    const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    return u32x4{c[0], c[1], d[0], d[1]};
 }
 
 // 8 values of A in the order of the code pairs: (0,4) (1,5) (2,6) (3,7)
@@ -68,28 +54,27 @@ __device__ __forceinline__ u32x4 pair_order(u32x4 a) {
                  __builtin_amdgcn_perm(a[3], a[1], 0x05040100u), __builtin_amdgcn_perm(a[3], a[1], 0x07060302u)};
 }
 
+// Holds the mask in a scalar and the offset in a vector register, for one and-or instruction per
+// pair (with literals it would be two).
+__device__ __forceinline__ void in_registers(uint32_t &m, uint32_t &o) { asm("" : "+s"(m), "+v"(o)); }
+
 // 16 + q of the 8 codes of a word, as pairs (0,4) (1,5) (2,6) (3,7)
 template <class TI>
 __device__ __forceinline__ u32x4 codes16(uint32_t w);
 template <>
 __device__ __forceinline__ u32x4 codes16<TF16>(uint32_t w) {
-    constexpr uint32_t m = 0x03c003c0u, o = 0x4c004c00u;   // mantissa bits 6-9; 16.0
+    uint32_t m = 0x03c003c0u, o = 0x4c004c00u;   // mantissa bits 6-9; 16.0
+    in_registers(m, o);
     return u32x4{((w << 6) & m) | o, ((w << 2) & m) | o, ((w >> 2) & m) | o, ((w >> 6) & m) | o};
 }
 template <>
 __device__ __forceinline__ u32x4 codes16<TBF16>(uint32_t w) {
-    constexpr uint32_t m = 0x00780078u, o = 0x41804180u;   // mantissa bits 3-6; 16.0
+    uint32_t m = 0x00780078u, o = 0x41804180u;   // mantissa bits 3-6; 16.0
+    in_registers(m, o);
     return u32x4{((w << 3) & m) | o, ((w >> 1) & m) | o, ((w >> 5) & m) | o, ((w >> 9) & m) | o};
 }
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-
-// What one lane's weight row contributes to a block: scale, and the offset 16 + z to take off.
-template <class TI>
-struct Block {
-    float s;
-    float off;               // 16 + z
-};
 
 template <class TI>
 struct Quant;
@@ -118,15 +103,77 @@ struct Quant<TBF16> {
     __device__ static constexpr uint32_t ones() { return 0x3f803f80u; }
 };
 
-// Scale and offset of block b of the weight row whose blocks start at `row`; a chunk's blocks past
-// K get the last block's offset and a zero scale (A is zero there).
-template <class TI>
-__device__ __forceinline__ Block<TI> block_of(const QuantParams &p, int64_t row, int b, int nblk) {
-    const int64_t i = row + min(b, nblk - 1);
-    Block<TI> x;
-    x.s = b < nblk ? (float)static_cast<const typename Quant<TI>::T *>(p.scales)[i] : 0.0f;
-    x.off = 16.0f + (p.zeros ? (float)p.zeros[i] : 8.0f);
+// Scales and offsets 16 + z of a weight row's blocks in one chunk.
+template <int NBLK>
+struct Blocks {
+    float s[NBLK], off[NBLK];
+};
+
+// Eight consecutive scales (16 bytes) and zero points (8 bytes) of one weight row, as loaded; a
+// scale load touches one cache line per row however few scales it takes, so eight at once.  Those
+// past the row's end are zero.  Z: the weights have zero points (else every one is 8).
+constexpr int SCALES = 8;
+template <bool Z>
+struct ScaleRegs {
+    u32x4 s;
+    uint2 z;
+    __device__ __forceinline__ void load(const QuantParams &p, int64_t row, int b, int nblk) {
+        const uint8_t *sp = static_cast<const uint8_t *>(p.scales) + (row + b) * 2;
+        const uint8_t *zp = p.zeros + row + b;
+        if (b + SCALES <= nblk) {
+            s = ldg16(sp);
+            if constexpr (Z) __builtin_memcpy(&z, zp, 8);
+        } else {
+            uint16_t v[SCALES];
+            uint8_t w[SCALES];
+#pragma unroll
+            for (int i = 0; i < SCALES; ++i) {
+                v[i] = 0;
+                w[i] = 0;
+                if (b + i < nblk) {
+                    __builtin_memcpy(&v[i], sp + 2 * i, 2);
+                    if constexpr (Z) w[i] = zp[i];
+                }
+            }
+            __builtin_memcpy(&s, v, 16);
+            if constexpr (Z) __builtin_memcpy(&z, w, 8);
+        }
+    }
+};
+// A row's eight in LDS (16 bytes of scales; 8 of zero points), and the NBLK from block i on.
+template <class TI, int NBLK, bool Z>
+__device__ __forceinline__ Blocks<NBLK> read_blocks(const uint8_t *s, const uint8_t *z, int i) {
+    using T = typename Quant<TI>::T;
+    T v[NBLK];
+    uint8_t w[NBLK];
+    __builtin_memcpy(v, __builtin_assume_aligned(s + 2 * i, 2 * NBLK), sizeof v);
+    if constexpr (Z) __builtin_memcpy(w, __builtin_assume_aligned(z + i, NBLK), sizeof w);
+    Blocks<NBLK> x;
+#pragma unroll
+    for (int b = 0; b < NBLK; ++b) {
+        x.s[b] = (float)v[b];
+        x.off[b] = Z ? 16.0f + (float)w[b] : 24.0f;
+    }
     return x;
+}
+
+// 16 rows x 64 bytes in LDS: 16-byte piece q of row r.  Global loads take 4 consecutive lanes per
+// row (lane / 4, lane % 4), so that the address unit sees whole 64-byte pieces (16 lanes on 16
+// different rows cost four times as many cache accesses, which bound the first version of this
+// kernel); a fragment takes row lane % 16, piece lane / 16.  LDS carries the data from one lane
+// order to the other.
+__device__ __forceinline__ int piece16(int r, int q) { return r * 64 + ((q ^ ((r >> 2) & 3)) << 4); }
+
+// Orders this wave's LDS accesses (they execute in order; no instruction).
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The block that holds chunk ch (blocks of whole chunks): ch / (block / 128) by the reciprocal
+// ceil(2^32 / (block / 128)), exact while the number of chunks is below 2^16.
+__device__ __forceinline__ int block_of(const QuantParams &p, int ch) {
+    return (int)((uint64_t)(uint32_t)ch * p.block_rcp >> 32);
 }
 
 // The expert, row tile and column tile of a workgroup; false: none.  With one weight matrix the
@@ -163,140 +210,214 @@ __device__ __forceinline__ void store_one(const QuantParams &p, int m, int n, fl
 }
 
 // ---- few rows ----------------------------------------------------------------------------------
-// 16 * MT rows and 16 columns per workgroup: the weights are read once, straight into registers
-// (they are used once: LDS would only add a trip), by WAVES waves that take every WAVES-th chunk
-// of K, so that a workgroup reads whole lines of its 16 weight rows and enough loads are in
-// flight; DEPTH chunks per wave are loaded ahead.  A comes from L2 (every workgroup reads it).
+// 16 * MT rows and 16 * CG columns per workgroup, K divided over its WAVES waves; each wave reads
+// its weights once, through registers (one chunk ahead) and a private LDS slot that only changes
+// the lane order.  A comes from L2: every workgroup reads it, CG column groups share one reading.
 // The waves' sums are added through LDS in wave order.
-constexpr int WAVES = 8;
-constexpr int NB = 16;
+#ifndef QW
+#define QW 8
+#endif
+constexpr int WAVES = QW;
 
-template <class TI, int G, int MT>
-struct RowsChunk {
-    static constexpr int NBLK = G >= 128 ? 1 : CHUNK / G;    // blocks per chunk
-    u32x4 q;
-    u32x4 a[MT][4];
-    Block<TI> blk[NBLK];
-};
-
-template <class TI, class TO, int G, int MT>
+template <class TI, class TO, int G, bool Z, int MT, int CG>
 __global__ __launch_bounds__(WAVES * 64) void quant_rows(QuantParams p) {
     using T = typename TO::T;
     using QT = Quant<TI>;
-    using CH = RowsChunk<TI, G, MT>;
-    constexpr int DEPTH = MT == 1 ? 4 : 2;
-    constexpr int SUB = G >= 128 ? 4 : G / 32;               // matrix instructions per block
-    __shared__ f32x4 part[WAVES][MT][64];
+    constexpr int NBLK = G >= 128 ? 1 : CHUNK / G;           // blocks per chunk
+    constexpr int SUB = 4 / NBLK;                            // matrix instructions per block
+    constexpr int SC = SCALES / NBLK;                        // chunks per scale load
+    constexpr int COLS = 16 * CG;
+    // a wave's slots: codes, one 16-row tile of A, scales and zero points
+    constexpr int OFF_A = CG * 1024, OFF_S = OFF_A + 4096, OFF_Z = OFF_S + COLS * 16;
+    constexpr int SLOT = OFF_Z + (Z ? COLS * 8 : 0);
+    constexpr int PART = MT * CG * 1024;                     // a wave's sums
+    __shared__ __attribute__((aligned(16))) uint8_t smem[WAVES * (SLOT > PART ? SLOT : PART)];
+    struct Chunk {
+        u32x4 q[CG], a[MT][4];
+    };
 
     int tn;
     if (!select_tile<(int)sizeof(T)>(p, 16 * MT, tn)) return;
     const int lane = threadIdx.x & 63, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = tn * NB + (lane & 15), nc = min(n, p.N - 1);
-    const uint8_t *qrow = p.Q + (int64_t)nc * p.ldq + 16 * g;
-    const int64_t srow = (int64_t)nc * p.lds;
-    const uint8_t *arow[MT];
+    const int lr = lane >> 2, lq = lane & 3;                 // load order: row, piece
+    const int nch = (p.K + CHUNK - 1) / CHUNK, nblk = p.K / p.block;
+    const int c0 = (int)((int64_t)nch * wave / WAVES), c1 = (int)((int64_t)nch * (wave + 1) / WAVES);
+    const uint8_t *qrow[CG], *arow[MT];
+#pragma unroll
+    for (int j = 0; j < CG; ++j) qrow[j] = p.Q + (int64_t)min(tn * COLS + 16 * j + lr, p.N - 1) * p.ldq;
 #pragma unroll
     for (int t = 0; t < MT; ++t)
-        arow[t] = static_cast<const uint8_t *>(p.A) + (int64_t)min(16 * t + (lane & 15), p.M - 1) * p.lda * 2;
-    const int nch = (p.K + CHUNK - 1) / CHUNK, nblk = p.K / p.block;
+        arow[t] = static_cast<const uint8_t *>(p.A) + (int64_t)min(16 * t + lr, p.M - 1) * p.lda * 2;
+    const int64_t srow = (int64_t)min(tn * COLS + lane, p.N - 1) * p.lds;
+    uint8_t *const slot = smem + wave * SLOT;
+    const int put = piece16(lr, lq), get = piece16(lane & 15, g);
 
-    auto load = [&](CH &c, int ch) {
+    // The last chunk may end inside K (after whole blocks of 32): its loads stay in the row, and A
+    // counts as zero past K.
+    auto load = [&](Chunk &c, int ch) {
         const int k0 = ch * CHUNK;
-        // the last chunk may end inside (whole blocks of 32): zeros there
-        c.q = u32x4{0, 0, 0, 0};
-        if (k0 + 32 * g < p.K) c.q = ldg16(qrow + k0 / 2);
+        const int at = G >= 128 ? k0 / 2 + 16 * lq : min(k0 / 2 + 16 * lq, p.K / 2 - 16);
+#pragma unroll
+        for (int j = 0; j < CG; ++j) c.q[j] = ldg16(qrow[j] + at);
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int k = k0 + kofs<G>(i, g);
-                c.a[t][i] = u32x4{0, 0, 0, 0};
-                if (k < p.K) c.a[t][i] = ldg16(arow[t] + 2 * k);
+                const int k = k0 + 32 * i + 8 * lq;
+                c.a[t][i] = ldg16(arow[t] + 2 * (G >= 128 ? k : min(k, p.K - 8)));
             }
-        const int b0 = G >= 128 ? k0 / p.block : k0 / G;
-#pragma unroll
-        for (int b = 0; b < CH::NBLK; ++b) c.blk[b] = block_of<TI>(p, srow, b0 + b, nblk);
     };
+    auto first_block = [&](int ch) { return G >= 128 ? block_of(p, ch) : ch * NBLK; };
 
-    f32x4 acc[MT];
+    f32x4 acc[MT][CG];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = f32x4{0, 0, 0, 0};
-    auto compute = [&](const CH &c) {
-        const u32x4 w = exchange<G>(c.q);
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < CG; ++j) acc[t][j] = f32x4{0, 0, 0, 0};
+    // chunk ch in c, its scales from index bi of the slot on
+    auto compute = [&](const Chunk &c, int ch, int bi) {
         const u32x4 one = u32x4{QT::ones(), QT::ones(), QT::ones(), QT::ones()};
+        u32x4 a[MT][4], w[CG];
+        Blocks<NBLK> blk[CG];
+        wave_order();
 #pragma unroll
-        for (int b = 0; b < CH::NBLK; ++b) {
-            f32x4 t[MT], sum[MT];
+        for (int j = 0; j < CG; ++j) *reinterpret_cast<u32x4 *>(slot + 1024 * j + put) = c.q[j];
 #pragma unroll
-            for (int r = 0; r < MT; ++r) t[r] = sum[r] = f32x4{0, 0, 0, 0};
+        for (int t = 0; t < MT; ++t) {
 #pragma unroll
-            for (int i = b * SUB; i < (b + 1) * SUB; ++i) {
-                const u32x4 v = QT::values(w[i], c.blk[b].off);
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4 *>(slot + OFF_A + 1024 * i + put) = c.a[t][i];
+            wave_order();
 #pragma unroll
-                for (int r = 0; r < MT; ++r) {
-                    const u32x4 a = pair_order(c.a[r][i]);
-                    t[r] = TI::mma16(a, v, t[r]);
-                    if constexpr (QT::SUMS) sum[r] = TI::mma16(a, one, sum[r]);
+            for (int i = 0; i < 4; ++i) a[t][i] = *reinterpret_cast<const u32x4 *>(slot + OFF_A + 1024 * i + get);
+            wave_order();
+        }
+#pragma unroll
+        for (int j = 0; j < CG; ++j) {
+            w[j] = *reinterpret_cast<const u32x4 *>(slot + 1024 * j + get);
+            const int row = 16 * j + (lane & 15);
+            blk[j] = read_blocks<TI, NBLK, Z>(slot + OFF_S + 16 * row, slot + OFF_Z + 8 * row, bi);
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[t][i] = pair_order(a[t][i]);
+                if constexpr (G < 128) {   // an instruction's 32 k are inside K or past it
+                    if (ch * CHUNK + 32 * i >= p.K) a[t][i] = u32x4{0, 0, 0, 0};
                 }
             }
+        f32x4 sum[MT][NBLK];
+        if constexpr (QT::SUMS)
 #pragma unroll
-            for (int r = 0; r < MT; ++r)
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = QT::SUMS ? __builtin_fmaf(-c.blk[b].off, sum[r][e], t[r][e]) : t[r][e];
-                    acc[r][e] = __builtin_fmaf(c.blk[b].s, x, acc[r][e]);
+                for (int b = 0; b < NBLK; ++b) {
+                    sum[t][b] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int i = b * SUB; i < (b + 1) * SUB; ++i) sum[t][b] = TI::mma16(a[t][i], one, sum[t][b]);
                 }
+#pragma unroll
+        for (int j = 0; j < CG; ++j) {
+            const u32x4 x = exchange(w[j]);
+#pragma unroll
+            for (int b = 0; b < NBLK; ++b) {
+                f32x4 t[MT];
+#pragma unroll
+                for (int r = 0; r < MT; ++r) t[r] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int i = b * SUB; i < (b + 1) * SUB; ++i) {
+                    const u32x4 v = QT::values(x[i], blk[j].off[b]);
+#pragma unroll
+                    for (int r = 0; r < MT; ++r) t[r] = TI::mma16(a[r][i], v, t[r]);
+                }
+#pragma unroll
+                for (int r = 0; r < MT; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y = QT::SUMS ? __builtin_fmaf(-blk[j].off[b], sum[r][b][e], t[r][e]) : t[r][e];
+                        acc[r][j][e] = __builtin_fmaf(blk[j].s[b], y, acc[r][j][e]);
+                    }
+            }
         }
     };
 
-    CH buf[DEPTH];
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-        if (wave + d * WAVES < nch) load(buf[d], wave + d * WAVES);
-    for (int c0 = wave; c0 < nch; c0 += DEPTH * WAVES) {
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            const int c = c0 + d * WAVES;
-            if (c < nch) {
-                compute(buf[d]);
-                if (c + DEPTH * WAVES < nch) load(buf[d], c + DEPTH * WAVES);
+    if (c0 < c1) {
+        ScaleRegs<Z> sr;
+        Chunk x, y;
+        sr.load(p, srow, first_block(c0), nblk);
+        load(x, c0);
+        int base = 0;                                        // block at index 0 of the slot
+        // every SC chunks: the scales loaded SC chunks ago go to the slot, the next ones are loaded
+        auto scales = [&](int ch) {
+            if ((ch - c0) % SC == 0) {
+                base = first_block(ch);
+                wave_order();
+                if (lane < COLS) {
+                    *reinterpret_cast<u32x4 *>(slot + OFF_S + 16 * lane) = sr.s;
+                    if constexpr (Z) *reinterpret_cast<uint2 *>(slot + OFF_Z + 8 * lane) = sr.z;
+                }
+                if (ch + SC < c1) sr.load(p, srow, first_block(ch + SC), nblk);
             }
+            return first_block(ch) - base;
+        };
+        int ch = c0;
+#pragma unroll 1
+        for (;;) {
+            const int bx = scales(ch);
+            if (ch + 1 < c1) load(y, ch + 1);
+            compute(x, ch, bx);
+            if (++ch >= c1) break;
+            const int by = scales(ch);
+            if (ch + 1 < c1) load(x, ch + 1);
+            compute(y, ch, by);
+            if (++ch >= c1) break;
         }
     }
 
+    __syncthreads();                                         // the slots become the sums
+    f32x4 *part = reinterpret_cast<f32x4 *>(smem);           // [wave][t][j][lane]
 #pragma unroll
-    for (int t = 0; t < MT; ++t) part[wave][t][lane] = acc[t];
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < CG; ++j) part[((wave * MT + t) * CG + j) * 64 + lane] = acc[t][j];
     __syncthreads();
-    if (wave >= MT) return;
-    // wave t finishes row tile t: lane holds rows 4 * (lane / 16) + r of column n
-    f32x4 sum = part[0][wave][lane];
+    // wave w finishes tiles w, w + WAVES, ...: lane holds rows 4 * (lane / 16) + r of one column
+    for (int tile = wave; tile < MT * CG; tile += WAVES) {
+        const int t = tile / CG, j = tile % CG;
+        f32x4 sum = part[tile * 64 + lane];
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) sum += part[w][wave][lane];
-    if (n >= p.N) return;
-    const float bias = p.has_bias ? static_cast<const float *>(p.bias)[n] : 0.0f;
+        for (int w = 1; w < WAVES; ++w) sum += part[(w * MT * CG + tile) * 64 + lane];
+        const int n = tn * COLS + 16 * j + (lane & 15);
+        if (n >= p.N) continue;
+        const float bias = p.has_bias ? static_cast<const float *>(p.bias)[n] : 0.0f;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int m = 16 * wave + 4 * g + r;
-        if (m < p.M) store_one<T>(p, m, n, sum[r], bias);
+        for (int r = 0; r < 4; ++r) {
+            const int m = 16 * t + 4 * g + r;
+            if (m < p.M) store_one<T>(p, m, n, sum[r], bias);
+        }
     }
 }
 
 // ---- many rows ---------------------------------------------------------------------------------
-// 128 x 128 output tile, 4 waves of 64 x 64.  A is staged in LDS once per workgroup, already in
-// pair order (global -> registers -> permute -> LDS, two stages of 128 k, rows of 256 bytes whose
-// 16-byte piece c stands at c ^ (row % 16)); each wave turns the codes of its 64 columns into
-// fragments in registers, straight from global memory one chunk ahead.
+// 128 x 128 output tile, 4 waves of 64 x 64.  Per chunk of 128 k, A (in pair order: permuted on
+// the way from registers to LDS) and the codes are staged in LDS once per workgroup, two stages,
+// the next chunk's loads in flight during the current one; each wave turns the codes of its 64
+// columns into fragments in registers, one group of 16 at a time.
 constexpr int TM = 128, TN = 128, TNT = 256;
 
-template <class TI, class TO, int G>
+template <class TI, class TO, int G, bool Z>
 __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
     using T = typename TO::T;
     using QT = Quant<TI>;
     constexpr int NBLK = G >= 128 ? 1 : CHUNK / G;
-    constexpr int SUB = G >= 128 ? 4 : G / 32;
-    constexpr int STAGE = TM * CHUNK * 2;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * STAGE];
+    constexpr int SUB = 4 / NBLK;
+    constexpr int SC = SCALES / NBLK;
+    // a stage: A in 8 groups of 16 rows x 4 pieces of 32 k, codes in 8 groups of 16 columns; scales
+    // and zero points once (replaced every SC chunks, between two barriers)
+    constexpr int A_BYTES = TM * CHUNK * 2, STAGE = A_BYTES + TN * CHUNK / 2;
+    constexpr int OFF_S = 2 * STAGE, OFF_Z = OFF_S + TN * 16;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[OFF_Z + (Z ? TN * 8 : 0)];
 
     int tn;
     if (!select_tile<(int)sizeof(T)>(p, TM, tn)) return;
@@ -304,50 +425,48 @@ __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     const int nch = (p.K + CHUNK - 1) / CHUNK, nblk = p.K / p.block;
+    const int lr = lane >> 2, lq = lane & 3;
 
-    // staging: thread -> piece tid % 16 of rows tid / 16 + 16 i
-    const uint8_t *asrc[8];
+    // this wave loads A's row groups 2w, 2w+1 (4 pieces each) and the codes' column groups 2w, 2w+1
+    const uint8_t *arow[2], *qrow[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        asrc[i] = static_cast<const uint8_t *>(p.A) + (int64_t)min((tid >> 4) + 16 * i, p.M - 1) * p.lda * 2 + (tid & 15) * 16;
-    u32x4 st[8];
-    auto fetch = [&](int ch) {
-        const bool in = ch * CHUNK + (tid & 15) * 8 < p.K;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            st[i] = u32x4{0, 0, 0, 0};
-            if (in) st[i] = ldg16(asrc[i] + ch * CHUNK * 2);
-        }
-    };
-    auto put = [&](int stage) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int row = (tid >> 4) + 16 * i;
-            *reinterpret_cast<u32x4 *>(smem + stage * STAGE + row * 256 + (((tid & 15) ^ (row & 15)) << 4)) = pair_order(st[i]);
-        }
-    };
-    // weights: column group j of the wave
-    const uint8_t *qrow[4];
-    int64_t srow[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int n = min(tn * TN + wn * 64 + 16 * j + (lane & 15), p.N - 1);
-        qrow[j] = p.Q + (int64_t)n * p.ldq + 16 * g;
-        srow[j] = (int64_t)n * p.lds;
+    for (int i = 0; i < 2; ++i) {
+        const int r = 16 * (2 * wave + i) + lr;
+        arow[i] = static_cast<const uint8_t *>(p.A) + (int64_t)min(r, p.M - 1) * p.lda * 2;
+        qrow[i] = p.Q + (int64_t)min(tn * TN + r, p.N - 1) * p.ldq;
     }
-    u32x4 q[4];
-    Block<TI> blk[4][NBLK];
-    auto weights = [&](int ch) {
+    const int64_t srow = (int64_t)min(tn * TN + tid, p.N - 1) * p.lds;
+    const int put = piece16(lr, lq), get = piece16(lane & 15, g);
+    u32x4 st[2][4], sq[2];
+    auto fetch = [&](int ch) {
         const int k0 = ch * CHUNK;
-        const int b0 = G >= 128 ? k0 / p.block : k0 / G;
+        const int at = G >= 128 ? k0 / 2 + 16 * lq : min(k0 / 2 + 16 * lq, p.K / 2 - 16);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            q[j] = u32x4{0, 0, 0, 0};
-            if (k0 + 32 * g < p.K) q[j] = ldg16(qrow[j] + k0 / 2);
+        for (int i = 0; i < 2; ++i) {
+            sq[i] = ldg16(qrow[i] + at);
 #pragma unroll
-            for (int b = 0; b < NBLK; ++b) blk[j][b] = block_of<TI>(p, srow[j], b0 + b, nblk);
+            for (int s = 0; s < 4; ++s) {
+                const int k = k0 + 32 * s + 8 * lq;
+                st[i][s] = ldg16(arow[i] + 2 * (G >= 128 ? k : min(k, p.K - 8)));
+            }
         }
     };
+    auto stage = [&](int ch) {
+        uint8_t *d = smem + (ch & 1) * STAGE;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            *reinterpret_cast<u32x4 *>(d + A_BYTES + 1024 * (2 * wave + i) + put) = sq[i];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                u32x4 v = pair_order(st[i][s]);
+                if constexpr (G < 128) {
+                    if (ch * CHUNK + 32 * s >= p.K) v = u32x4{0, 0, 0, 0};
+                }
+                *reinterpret_cast<u32x4 *>(d + (4 * (2 * wave + i) + s) * 1024 + put) = v;
+            }
+        }
+    };
+    auto first_block = [&](int ch) { return G >= 128 ? block_of(p, ch) : ch * NBLK; };
 
     f32x4 acc[4][4];
 #pragma unroll
@@ -355,67 +474,79 @@ __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
+    ScaleRegs<Z> sr;
+    auto put_scales = [&]() {
+        if (tid < TN) {
+            *reinterpret_cast<u32x4 *>(smem + OFF_S + 16 * tid) = sr.s;
+            if constexpr (Z) *reinterpret_cast<uint2 *>(smem + OFF_Z + 8 * tid) = sr.z;
+        }
+    };
+    int base = 0;
     if (nch > 0) {
+        sr.load(p, srow, 0, nblk);
         fetch(0);
-        weights(0);
-        put(0);
+        put_scales();
+        stage(0);
     }
     __syncthreads();
     const u32x4 one = u32x4{QT::ones(), QT::ones(), QT::ones(), QT::ones()};
+#pragma unroll 1
     for (int ch = 0; ch < nch; ++ch) {
         const bool more = ch + 1 < nch;
-        u32x4 w[4];
-        Block<TI> bl[4][NBLK];
+        const bool new_scales = more && (ch + 1) % SC == 0;
+        if (more) fetch(ch + 1);
+        if (new_scales) sr.load(p, srow, first_block(ch + 1), nblk);
+        const uint8_t *la = smem + (ch & 1) * STAGE + wm * 16384 + get;
+        const uint8_t *lq_ = smem + (ch & 1) * STAGE + A_BYTES + wn * 4096 + get;
+        const int bi = first_block(ch) - base;
+        u32x4 a[4][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            w[j] = exchange<G>(q[j]);
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int b = 0; b < NBLK; ++b) bl[j][b] = blk[j][b];
-        }
-        if (more) {
-            fetch(ch + 1);
-            weights(ch + 1);
-        }
-        const uint8_t *la = smem + (ch & 1) * STAGE + (wm * 64 + (lane & 15)) * 256;
-#pragma unroll
-        for (int b = 0; b < NBLK; ++b) {
-            f32x4 t[4][4], sum[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sum[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) t[i][j] = f32x4{0, 0, 0, 0};
-            }
-#pragma unroll
-            for (int s = b * SUB; s < (b + 1) * SUB; ++s) {
-                u32x4 a[4];
-                const int piece = kofs<G>(s, g) / 8;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    a[i] = *reinterpret_cast<const u32x4 *>(la + i * 16 * 256 + ((piece ^ (lane & 15)) << 4));
-                if constexpr (QT::SUMS) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sum[i] = TI::mma16(a[i], one, sum[i]);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const u32x4 v = QT::values(w[j][s], bl[j][b].off);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) t[i][j] = TI::mma16(a[i], v, t[i][j]);
-                }
-            }
+            for (int s = 0; s < 4; ++s) a[i][s] = *reinterpret_cast<const u32x4 *>(la + (4 * i + s) * 1024);
+        f32x4 sum[4][NBLK];
+        if constexpr (QT::SUMS)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int b = 0; b < NBLK; ++b) {
+                    sum[i][b] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int s = b * SUB; s < (b + 1) * SUB; ++s) sum[i][b] = TI::mma16(a[i][s], one, sum[i][b]);
+                }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const u32x4 w = exchange(*reinterpret_cast<const u32x4 *>(lq_ + 1024 * j));
+            const int row = wn * 64 + 16 * j + (lane & 15);
+            const Blocks<NBLK> blk = read_blocks<TI, NBLK, Z>(smem + OFF_S + 16 * row, smem + OFF_Z + 8 * row, bi);
+#pragma unroll
+            for (int b = 0; b < NBLK; ++b) {
+                f32x4 t[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int s = b * SUB; s < (b + 1) * SUB; ++s) {
+                    const u32x4 v = QT::values(w[s], blk.off[b]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) t[i] = TI::mma16(a[i][s], v, t[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float x = QT::SUMS ? __builtin_fmaf(-bl[j][b].off, sum[i][e], t[i][j][e]) : t[i][j][e];
-                        acc[i][j][e] = __builtin_fmaf(bl[j][b].s, x, acc[i][j][e]);
+                        const float x = QT::SUMS ? __builtin_fmaf(-blk.off[b], sum[i][b][e], t[i][e]) : t[i][e];
+                        acc[i][j][e] = __builtin_fmaf(blk.s[b], x, acc[i][j][e]);
                     }
+            }
         }
-        if (more) put((ch + 1) & 1);
+        if (more) stage(ch + 1);
         __syncthreads();
+        if (new_scales) {
+            // the last reader of the old scales is behind the barrier above
+            put_scales();
+            base = first_block(ch + 1);
+            __syncthreads();
+        }
     }
 
 #pragma unroll
@@ -435,28 +566,35 @@ __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
 
 // ---- entries -----------------------------------------------------------------------------------
 
-template <class TI, class TO, int G, int MT>
+template <class TI, class TO, int G, int MT, int CG>
 hipError_t launch_rows(const QuantParams &p, unsigned grid, hipStream_t s) {
-    hipLaunchKernelGGL((quant_rows<TI, TO, G, MT>), dim3(grid), dim3(WAVES * 64), 0, s, p);
+    if (p.zeros) hipLaunchKernelGGL((quant_rows<TI, TO, G, true, MT, CG>), dim3(grid), dim3(WAVES * 64), 0, s, p);
+    else hipLaunchKernelGGL((quant_rows<TI, TO, G, false, MT, CG>), dim3(grid), dim3(WAVES * 64), 0, s, p);
     return hipGetLastError();
 }
 template <class TI, class TO, int G>
 hipError_t launch_tile(const QuantParams &p, unsigned grid, hipStream_t s) {
-    hipLaunchKernelGGL((quant_tile<TI, TO, G>), dim3(grid), dim3(TNT), 0, s, p);
+    if (p.zeros) hipLaunchKernelGGL((quant_tile<TI, TO, G, true>), dim3(grid), dim3(TNT), 0, s, p);
+    else hipLaunchKernelGGL((quant_tile<TI, TO, G, false>), dim3(grid), dim3(TNT), 0, s, p);
     return hipGetLastError();
 }
 
 template <class TI, class TO, int G>
-const QuantEntry *rows_entry(int mt) {
-    static const QuantEntry e[3] = {{launch_rows<TI, TO, G, 1>, 16, NB, "quant_rows_m16"},
-                                    {launch_rows<TI, TO, G, 2>, 32, NB, "quant_rows_m32"},
-                                    {launch_rows<TI, TO, G, 4>, 64, NB, "quant_rows_m64"}};
-    return mt == 1 ? &e[0] : mt == 2 ? &e[1] : mt == 4 ? &e[2] : nullptr;
+const QuantEntry *rows_entry(int mt, int cg) {
+    static const QuantEntry e[6] = {{launch_rows<TI, TO, G, 1, 1>, 16, 16, "quant_rows_16x16"},
+                                    {launch_rows<TI, TO, G, 1, 4>, 16, 64, "quant_rows_16x64"},
+                                    {launch_rows<TI, TO, G, 2, 1>, 32, 16, "quant_rows_32x16"},
+                                    {launch_rows<TI, TO, G, 2, 2>, 32, 32, "quant_rows_32x32"},
+                                    {launch_rows<TI, TO, G, 4, 1>, 64, 16, "quant_rows_64x16"},
+                                    {launch_rows<TI, TO, G, 4, 2>, 64, 32, "quant_rows_64x32"}};
+    for (const QuantEntry &x : e)
+        if (x.bm == 16 * mt && x.bn == 16 * cg) return &x;
+    return nullptr;
 }
 template <class TI, class TO>
-const QuantEntry *lookup_rows(int block, int mt) {
-    return block == 32 ? rows_entry<TI, TO, 32>(mt) : block == 64 ? rows_entry<TI, TO, 64>(mt)
-           : block == 128 ? rows_entry<TI, TO, 128>(mt) : nullptr;
+const QuantEntry *lookup_rows(int block, int mt, int cg) {
+    return block == 32 ? rows_entry<TI, TO, 32>(mt, cg) : block == 64 ? rows_entry<TI, TO, 64>(mt, cg)
+           : block == 128 ? rows_entry<TI, TO, 128>(mt, cg) : nullptr;
 }
 template <class TI, class TO>
 const QuantEntry *lookup_tile(int block) {
@@ -469,16 +607,16 @@ const QuantEntry *lookup_tile(int block) {
 }  // namespace
 
 #if defined(TGE_PAIR_F16_F16)
-const QuantEntry *quant_rows_f16_f16(int b, int mt) { return lookup_rows<TF16, OF16>(b, mt); }
+const QuantEntry *quant_rows_f16_f16(int b, int mt, int cg) { return lookup_rows<TF16, OF16>(b, mt, cg); }
 const QuantEntry *quant_tile_f16_f16(int b) { return lookup_tile<TF16, OF16>(b); }
 #elif defined(TGE_PAIR_F16_F32)
-const QuantEntry *quant_rows_f16_f32(int b, int mt) { return lookup_rows<TF16, OF32>(b, mt); }
+const QuantEntry *quant_rows_f16_f32(int b, int mt, int cg) { return lookup_rows<TF16, OF32>(b, mt, cg); }
 const QuantEntry *quant_tile_f16_f32(int b) { return lookup_tile<TF16, OF32>(b); }
 #elif defined(TGE_PAIR_BF16_BF16)
-const QuantEntry *quant_rows_bf16_bf16(int b, int mt) { return lookup_rows<TBF16, OBF16>(b, mt); }
+const QuantEntry *quant_rows_bf16_bf16(int b, int mt, int cg) { return lookup_rows<TBF16, OBF16>(b, mt, cg); }
 const QuantEntry *quant_tile_bf16_bf16(int b) { return lookup_tile<TBF16, OBF16>(b); }
 #elif defined(TGE_PAIR_BF16_F32)
-const QuantEntry *quant_rows_bf16_f32(int b, int mt) { return lookup_rows<TBF16, OF32>(b, mt); }
+const QuantEntry *quant_rows_bf16_f32(int b, int mt, int cg) { return lookup_rows<TBF16, OF32>(b, mt, cg); }
 const QuantEntry *quant_tile_bf16_f32(int b) { return lookup_tile<TBF16, OF32>(b); }
 #else
 #error "define one TGE_PAIR_* macro of a 16-bit float type"

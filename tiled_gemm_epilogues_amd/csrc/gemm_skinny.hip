@@ -139,8 +139,8 @@ __global__ __launch_bounds__(NT, 1) void gemm_skinny(ParamsOf<GRP> p) {
         cb = lid - split * p.tiles_n;
     }
     const int n0 = cb * CB;
-    const uint8_t *A = static_cast<const uint8_t *>(p.A);
-    const uint8_t *B = static_cast<const uint8_t *>(p.B);
+    const uint8_t *A = dma_base<GRP>(p.A);
+    const uint8_t *B = dma_base<GRP>(p.B);
 
     // chunks [c0, c1) of this wave: the split's share of K, divided over the four waves
     const int nch_all = p.K / KCH;

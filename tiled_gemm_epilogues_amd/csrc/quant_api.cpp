@@ -25,7 +25,9 @@ struct gemm_quant_plan {
 
 namespace {
 
-using RowsFn = const QuantEntry *(*)(int, int);
+constexpr int64_t MAX_K = (int64_t)1 << 23;   // 2^16 chunks of 128 (see block_of in gemm_quant.hip)
+
+using RowsFn = const QuantEntry *(*)(int, int, int);
 using TileFn = const QuantEntry *(*)(int);
 
 RowsFn rows_table(int ab, int cd) {
@@ -75,7 +77,7 @@ gemm_status_t gemm_quant_plan_create(gemm_quant_plan_t *out, const gemm_quant_de
         return GEMM_STATUS_INVALID_VALUE;
     if (!rows_table(ab, cd) || !(d->block == 32 || d->block == 64 || d->block % 128 == 0))
         return GEMM_STATUS_NOT_SUPPORTED;
-    if (d->rows >= LIM31 || d->N >= LIM31 || d->K >= LIM31 / 2 || d->lda >= LIM31 || d->ldq >= LIM31 ||
+    if (d->rows >= LIM31 || d->N >= LIM31 || d->K >= MAX_K || d->lda >= LIM31 || d->ldq >= LIM31 ||
         d->lds >= LIM31 || d->ldc >= LIM31 || d->groups >= MAX_GROUPS)
         return GEMM_STATUS_NOT_SUPPORTED;
     const int64_t nb = d->K / d->block;
@@ -92,9 +94,15 @@ gemm_status_t gemm_quant_plan_create(gemm_quant_plan_t *out, const gemm_quant_de
     p.ab = ab; p.cd = cd; p.epi = epi; p.zeros = d->zeros != 0;
     const int g = d->block >= 128 ? 128 : (int)d->block;
     const int64_t avg = ceil_div(d->rows, d->groups);   // rows of an expert, on average
-    if (algo == GEMM_ALGO_SKINNY) p.kernel = rows_table(ab, cd)(g, tile ? tile / 16 : 1);
+    // rows kernels: the wide one where it still gives every CU a workgroup
+    const auto rows_kernel = [&](int mt) {
+        const QuantEntry *wide = rows_table(ab, cd)(g, mt, mt == 1 ? 4 : 2);
+        p.kernel = wide;
+        return grid_of(p, p.groups > 1) >= 256 ? wide : rows_table(ab, cd)(g, mt, 1);
+    };
+    if (algo == GEMM_ALGO_SKINNY) p.kernel = rows_kernel(tile ? tile / 16 : 1);
     else if (algo == GEMM_ALGO_FAST) p.kernel = tile_table(ab, cd)(g);
-    else if (avg <= 64) p.kernel = rows_table(ab, cd)(g, avg <= 16 ? 1 : avg <= 32 ? 2 : 4);
+    else if (avg <= 64) p.kernel = rows_kernel(avg <= 16 ? 1 : avg <= 32 ? 2 : 4);
     else p.kernel = tile_table(ab, cd)(g);
     if (grid_of(p, true) >= LIM31) return GEMM_STATUS_NOT_SUPPORTED;
     gemm_quant_plan *q = new (std::nothrow) gemm_quant_plan(p);
@@ -140,6 +148,7 @@ gemm_status_t gemm_quant_run(gemm_quant_plan_t p, const void *A, const void *Q, 
     prm.zeros = p->zeros ? static_cast<const uint8_t *>(zeros) : nullptr;
     prm.stride_q = p->stride_q; prm.stride_s = p->stride_s;
     prm.ldq = (int)p->ldq; prm.lds = (int)p->lds; prm.block = (int)p->block;
+    if (p->block >= 128) prm.block_rcp = (((uint64_t)1 << 32) + p->block / 128 - 1) / (p->block / 128);
     const unsigned grid = (unsigned)grid_of(*p, offsets != nullptr);
     return p->kernel->launch(prm, grid, static_cast<hipStream_t>(stream)) == hipSuccess ? GEMM_STATUS_SUCCESS
                                                                                        : GEMM_STATUS_HIP_ERROR;
