@@ -451,8 +451,8 @@ typedef struct gemm_quant_plan *gemm_quant_plan_t;
  * block: 32, 64 or a multiple of 128; K is a multiple of it.  lda, ldc in elements; ldq: bytes
  * between rows of codes (>= K / 2); lds: elements between rows of scales and of zeros (>= K /
  * block); stride_q (bytes), stride_s, stride_bias: from expert to expert.  zeros: 1 when the runs
- * pass zero points, 0 otherwise.  algo: AUTO, or SKINNY (tile 16, 32 or 64 rows: K split over the
- * waves of a workgroup, for few rows) or FAST (128 x 128 tiles) to pin a kernel.
+ * pass zero points, 0 otherwise.  algo: AUTO, or SKINNY (16 rows x 16 or 64 columns, by tile; K
+ * split over the waves of a workgroup, for few rows) or FAST (128 x 128 tiles) to pin a kernel.
  */
 typedef struct {
     int64_t rows, N, K, block, groups;

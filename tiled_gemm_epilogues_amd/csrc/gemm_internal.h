@@ -231,13 +231,12 @@ struct QuantEntry {
 };
 // block: 32, 64, or 128 for every multiple of 128 (K a multiple of the block).  No alignment
 // preconditions beyond the elements' own.
-//   rows:  16 * mt x 16 * cg tiles, K split over the waves of a workgroup; (mt, cg) = (1, 1), (1, 4),
-//          (2, 1), (2, 2), (4, 1) or (4, 2)
+//   rows:  16 x 16 * cg tiles (cg 1 or 4), K split over the waves of a workgroup
 //   tile:  128 x 128 tiles
-const QuantEntry *quant_rows_f16_f16(int block, int mt, int cg);
-const QuantEntry *quant_rows_f16_f32(int block, int mt, int cg);
-const QuantEntry *quant_rows_bf16_bf16(int block, int mt, int cg);
-const QuantEntry *quant_rows_bf16_f32(int block, int mt, int cg);
+const QuantEntry *quant_rows_f16_f16(int block, int cg);
+const QuantEntry *quant_rows_f16_f32(int block, int cg);
+const QuantEntry *quant_rows_bf16_bf16(int block, int cg);
+const QuantEntry *quant_rows_bf16_f32(int block, int cg);
 const QuantEntry *quant_tile_f16_f16(int block);
 const QuantEntry *quant_tile_f16_f32(int block);
 const QuantEntry *quant_tile_bf16_bf16(int block);

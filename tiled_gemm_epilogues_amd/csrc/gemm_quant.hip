@@ -93,14 +93,14 @@ struct Quant<TF16> {
         }
         return v;
     }
-    __device__ static constexpr uint32_t ones() { return 0x3c003c00u; }
+    __device__ static u32x4 ones() { return u32x4{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u}; }
 };
 template <>
 struct Quant<TBF16> {
     using T = __bf16;
     static constexpr bool SUMS = true;
     __device__ static u32x4 values(uint32_t w, float) { return codes16<TBF16>(w); }
-    __device__ static constexpr uint32_t ones() { return 0x3f803f80u; }
+    __device__ static u32x4 ones() { return u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}; }
 };
 
 // Scales and offsets 16 + z of a weight row's blocks in one chunk.
@@ -157,6 +157,16 @@ __device__ __forceinline__ Blocks<NBLK> read_blocks(const uint8_t *s, const uint
     return x;
 }
 
+// Adds one block's sum to the accumulator: the offset's part off, times the scale.
+template <class TI>
+__device__ __forceinline__ void add_block(f32x4 &acc, f32x4 t, f32x4 sum, float s, float off) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float x = Quant<TI>::SUMS ? __builtin_fmaf(-off, sum[e], t[e]) : t[e];
+        acc[e] = __builtin_fmaf(s, x, acc[e]);
+    }
+}
+
 // 16 rows x 64 bytes in LDS: 16-byte piece q of row r.  Global loads take 4 consecutive lanes per
 // row (lane / 4, lane % 4), so that the address unit sees whole 64-byte pieces (16 lanes on 16
 // different rows cost four times as many cache accesses, which bound the first version of this
@@ -210,45 +220,41 @@ __device__ __forceinline__ void store_one(const QuantParams &p, int m, int n, fl
 }
 
 // ---- few rows ----------------------------------------------------------------------------------
-// 16 * MT rows and 16 * CG columns per workgroup, K divided over its WAVES waves; each wave reads
-// its weights once, through registers (one chunk ahead) and a private LDS slot that only changes
-// the lane order.  A comes from L2: every workgroup reads it, CG column groups share one reading.
-// The waves' sums are added through LDS in wave order.
-#ifndef QW
-#define QW 8
-#endif
-constexpr int WAVES = QW;
+// 16 rows and 16 * CG columns per workgroup, K divided over its WAVES waves; each wave reads its
+// weights once, through registers (one chunk ahead) and a private LDS slot that only changes the
+// lane order.  A comes from L2: every workgroup reads it, CG column groups share one reading.  The
+// waves' sums are added through LDS in wave order.  Two workgroups fit a CU, so that one's loads
+// are in flight while the other starts or ends.
+constexpr int WAVES = 8;
 
-template <class TI, class TO, int G, bool Z, int MT, int CG>
-__global__ __launch_bounds__(WAVES * 64) void quant_rows(QuantParams p) {
+template <class TI, class TO, int G, bool Z, int CG>
+__global__ __launch_bounds__(WAVES * 64, 2) void quant_rows(QuantParams p) {
     using T = typename TO::T;
     using QT = Quant<TI>;
     constexpr int NBLK = G >= 128 ? 1 : CHUNK / G;           // blocks per chunk
     constexpr int SUB = 4 / NBLK;                            // matrix instructions per block
     constexpr int SC = SCALES / NBLK;                        // chunks per scale load
     constexpr int COLS = 16 * CG;
-    // a wave's slots: codes, one 16-row tile of A, scales and zero points
+    // a wave's slot: codes, A, scales and zero points
     constexpr int OFF_A = CG * 1024, OFF_S = OFF_A + 4096, OFF_Z = OFF_S + COLS * 16;
     constexpr int SLOT = OFF_Z + (Z ? COLS * 8 : 0);
-    constexpr int PART = MT * CG * 1024;                     // a wave's sums
-    __shared__ __attribute__((aligned(16))) uint8_t smem[WAVES * (SLOT > PART ? SLOT : PART)];
+    static_assert(SLOT >= CG * 1024, "the slots hold the waves' sums at the end");
+    __shared__ __attribute__((aligned(16))) uint8_t smem[WAVES * SLOT];
     struct Chunk {
-        u32x4 q[CG], a[MT][4];
+        u32x4 q[CG], a[4];
     };
 
     int tn;
-    if (!select_tile<(int)sizeof(T)>(p, 16 * MT, tn)) return;
+    if (!select_tile<(int)sizeof(T)>(p, 16, tn)) return;
     const int lane = threadIdx.x & 63, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane >> 2, lq = lane & 3;                 // load order: row, piece
     const int nch = (p.K + CHUNK - 1) / CHUNK, nblk = p.K / p.block;
     const int c0 = (int)((int64_t)nch * wave / WAVES), c1 = (int)((int64_t)nch * (wave + 1) / WAVES);
-    const uint8_t *qrow[CG], *arow[MT];
+    const uint8_t *qrow[CG];
 #pragma unroll
     for (int j = 0; j < CG; ++j) qrow[j] = p.Q + (int64_t)min(tn * COLS + 16 * j + lr, p.N - 1) * p.ldq;
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-        arow[t] = static_cast<const uint8_t *>(p.A) + (int64_t)min(16 * t + lr, p.M - 1) * p.lda * 2;
+    const uint8_t *arow = static_cast<const uint8_t *>(p.A) + (int64_t)min(lr, p.M - 1) * p.lda * 2;
     const int64_t srow = (int64_t)min(tn * COLS + lane, p.N - 1) * p.lds;
     uint8_t *const slot = smem + wave * SLOT;
     const int put = piece16(lr, lq), get = piece16(lane & 15, g);
@@ -261,149 +267,107 @@ __global__ __launch_bounds__(WAVES * 64) void quant_rows(QuantParams p) {
 #pragma unroll
         for (int j = 0; j < CG; ++j) c.q[j] = ldg16(qrow[j] + at);
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = k0 + 32 * i + 8 * lq;
-                c.a[t][i] = ldg16(arow[t] + 2 * (G >= 128 ? k : min(k, p.K - 8)));
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int k = k0 + 32 * i + 8 * lq;
+            c.a[i] = ldg16(arow + 2 * (G >= 128 ? k : min(k, p.K - 8)));
+        }
     };
     auto first_block = [&](int ch) { return G >= 128 ? block_of(p, ch) : ch * NBLK; };
 
-    f32x4 acc[MT][CG];
+    f32x4 acc[CG];
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int j = 0; j < CG; ++j) acc[t][j] = f32x4{0, 0, 0, 0};
-    // chunk ch in c, its scales from index bi of the slot on
-    auto compute = [&](const Chunk &c, int ch, int bi) {
-        const u32x4 one = u32x4{QT::ones(), QT::ones(), QT::ones(), QT::ones()};
-        u32x4 a[MT][4], w[CG];
-        Blocks<NBLK> blk[CG];
-        wave_order();
+    for (int j = 0; j < CG; ++j) acc[j] = f32x4{0, 0, 0, 0};
+    // chunk ch from registers to the slot, A in pair order
+    auto stage = [&](const Chunk &c, int ch) {
 #pragma unroll
         for (int j = 0; j < CG; ++j) *reinterpret_cast<u32x4 *>(slot + 1024 * j + put) = c.q[j];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4 *>(slot + OFF_A + 1024 * i + put) = c.a[t][i];
-            wave_order();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[t][i] = *reinterpret_cast<const u32x4 *>(slot + OFF_A + 1024 * i + get);
-            wave_order();
+        for (int i = 0; i < 4; ++i) {
+            u32x4 v = pair_order(c.a[i]);
+            if constexpr (G < 128) {   // an instruction's 32 k are inside K or past it
+                if (ch * CHUNK + 32 * i >= p.K) v = u32x4{0, 0, 0, 0};
+            }
+            *reinterpret_cast<u32x4 *>(slot + OFF_A + 1024 * i + put) = v;
         }
+    };
+    // the chunk in the slot, its scales from index bi on
+    auto compute = [&](int bi) {
+        u32x4 w[CG];
+        Blocks<NBLK> blk[CG];
 #pragma unroll
         for (int j = 0; j < CG; ++j) {
-            w[j] = *reinterpret_cast<const u32x4 *>(slot + 1024 * j + get);
             const int row = 16 * j + (lane & 15);
+            w[j] = exchange(*reinterpret_cast<const u32x4 *>(slot + 1024 * j + get));
             blk[j] = read_blocks<TI, NBLK, Z>(slot + OFF_S + 16 * row, slot + OFF_Z + 8 * row, bi);
         }
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+        for (int b = 0; b < NBLK; ++b) {
+            f32x4 t[CG], sum = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[t][i] = pair_order(a[t][i]);
-                if constexpr (G < 128) {   // an instruction's 32 k are inside K or past it
-                    if (ch * CHUNK + 32 * i >= p.K) a[t][i] = u32x4{0, 0, 0, 0};
-                }
+            for (int j = 0; j < CG; ++j) t[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = b * SUB; i < (b + 1) * SUB; ++i) {
+                const u32x4 a = *reinterpret_cast<const u32x4 *>(slot + OFF_A + 1024 * i + get);
+                if constexpr (QT::SUMS) sum = TI::mma16(a, QT::ones(), sum);
+#pragma unroll
+                for (int j = 0; j < CG; ++j) t[j] = TI::mma16(a, QT::values(w[j][i], blk[j].off[b]), t[j]);
             }
-        f32x4 sum[MT][NBLK];
-        if constexpr (QT::SUMS)
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int b = 0; b < NBLK; ++b) {
-                    sum[t][b] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int i = b * SUB; i < (b + 1) * SUB; ++i) sum[t][b] = TI::mma16(a[t][i], one, sum[t][b]);
-                }
-#pragma unroll
-        for (int j = 0; j < CG; ++j) {
-            const u32x4 x = exchange(w[j]);
-#pragma unroll
-            for (int b = 0; b < NBLK; ++b) {
-                f32x4 t[MT];
-#pragma unroll
-                for (int r = 0; r < MT; ++r) t[r] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int i = b * SUB; i < (b + 1) * SUB; ++i) {
-                    const u32x4 v = QT::values(x[i], blk[j].off[b]);
-#pragma unroll
-                    for (int r = 0; r < MT; ++r) t[r] = TI::mma16(a[r][i], v, t[r]);
-                }
-#pragma unroll
-                for (int r = 0; r < MT; ++r)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float y = QT::SUMS ? __builtin_fmaf(-blk[j].off[b], sum[r][b][e], t[r][e]) : t[r][e];
-                        acc[r][j][e] = __builtin_fmaf(blk[j].s[b], y, acc[r][j][e]);
-                    }
-            }
+            for (int j = 0; j < CG; ++j) add_block<TI>(acc[j], t[j], sum, blk[j].s[b], blk[j].off[b]);
         }
     };
 
     if (c0 < c1) {
         ScaleRegs<Z> sr;
-        Chunk x, y;
+        Chunk x;
         sr.load(p, srow, first_block(c0), nblk);
         load(x, c0);
-        int base = 0;                                        // block at index 0 of the slot
-        // every SC chunks: the scales loaded SC chunks ago go to the slot, the next ones are loaded
-        auto scales = [&](int ch) {
-            if ((ch - c0) % SC == 0) {
+        int base = 0, next = c0;                             // block at index 0 of the slot; chunk of new scales
+#pragma unroll 1
+        for (int ch = c0; ch < c1; ++ch) {
+            wave_order();                                    // the last chunk's reads come first
+            if (ch == next) {   // every SC chunks: scales loaded SC chunks ago to the slot
                 base = first_block(ch);
-                wave_order();
                 if (lane < COLS) {
                     *reinterpret_cast<u32x4 *>(slot + OFF_S + 16 * lane) = sr.s;
                     if constexpr (Z) *reinterpret_cast<uint2 *>(slot + OFF_Z + 8 * lane) = sr.z;
                 }
-                if (ch + SC < c1) sr.load(p, srow, first_block(ch + SC), nblk);
+                next += SC;
+                if (next < c1) sr.load(p, srow, first_block(next), nblk);
             }
-            return first_block(ch) - base;
-        };
-        int ch = c0;
-#pragma unroll 1
-        for (;;) {
-            const int bx = scales(ch);
-            if (ch + 1 < c1) load(y, ch + 1);
-            compute(x, ch, bx);
-            if (++ch >= c1) break;
-            const int by = scales(ch);
-            if (ch + 1 < c1) load(x, ch + 1);
-            compute(y, ch, by);
-            if (++ch >= c1) break;
+            stage(x, ch);
+            wave_order();
+            if (ch + 1 < c1) load(x, ch + 1);                // in flight while this chunk is computed
+            compute(first_block(ch) - base);
         }
     }
 
     __syncthreads();                                         // the slots become the sums
-    f32x4 *part = reinterpret_cast<f32x4 *>(smem);           // [wave][t][j][lane]
+    f32x4 *part = reinterpret_cast<f32x4 *>(smem);           // [wave][j][lane]
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int j = 0; j < CG; ++j) part[((wave * MT + t) * CG + j) * 64 + lane] = acc[t][j];
+    for (int j = 0; j < CG; ++j) part[(wave * CG + j) * 64 + lane] = acc[j];
     __syncthreads();
-    // wave w finishes tiles w, w + WAVES, ...: lane holds rows 4 * (lane / 16) + r of one column
-    for (int tile = wave; tile < MT * CG; tile += WAVES) {
-        const int t = tile / CG, j = tile % CG;
-        f32x4 sum = part[tile * 64 + lane];
+    // wave j finishes column group j: lane holds rows 4 * (lane / 16) + r of one column
+    if (wave >= CG) return;
+    f32x4 sum = part[wave * 64 + lane];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) sum += part[(w * MT * CG + tile) * 64 + lane];
-        const int n = tn * COLS + 16 * j + (lane & 15);
-        if (n >= p.N) continue;
-        const float bias = p.has_bias ? static_cast<const float *>(p.bias)[n] : 0.0f;
+    for (int w = 1; w < WAVES; ++w) sum += part[(w * CG + wave) * 64 + lane];
+    const int n = tn * COLS + 16 * wave + (lane & 15);
+    if (n >= p.N) return;
+    const float bias = p.has_bias ? static_cast<const float *>(p.bias)[n] : 0.0f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int m = 16 * t + 4 * g + r;
-            if (m < p.M) store_one<T>(p, m, n, sum[r], bias);
-        }
+    for (int r = 0; r < 4; ++r) {
+        const int m = 4 * g + r;
+        if (m < p.M) store_one<T>(p, m, n, sum[r], bias);
     }
 }
 
 // ---- many rows ---------------------------------------------------------------------------------
 // 128 x 128 output tile, 4 waves of 64 x 64.  Per chunk of 128 k, A (in pair order: permuted on
-// the way from registers to LDS) and the codes are staged in LDS once per workgroup, two stages,
-// the next chunk's loads in flight during the current one; each wave turns the codes of its 64
-// columns into fragments in registers, one group of 16 at a time.
+// the way from registers to LDS) and the codes are staged in LDS once per workgroup, the next
+// chunk's loads in flight in registers during the current one; each wave turns the codes of its
+// 64 columns into fragments in registers, one group of 16 at a time.  One stage, so that two
+// workgroups fit a CU and one computes while the other is between its barriers.
 constexpr int TM = 128, TN = 128, TNT = 256;
 
 template <class TI, class TO, int G, bool Z>
@@ -413,10 +377,9 @@ __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
     constexpr int NBLK = G >= 128 ? 1 : CHUNK / G;
     constexpr int SUB = 4 / NBLK;
     constexpr int SC = SCALES / NBLK;
-    // a stage: A in 8 groups of 16 rows x 4 pieces of 32 k, codes in 8 groups of 16 columns; scales
-    // and zero points once (replaced every SC chunks, between two barriers)
-    constexpr int A_BYTES = TM * CHUNK * 2, STAGE = A_BYTES + TN * CHUNK / 2;
-    constexpr int OFF_S = 2 * STAGE, OFF_Z = OFF_S + TN * 16;
+    // A in 8 groups of 16 rows x 4 pieces of 32 k, codes in 8 groups of 16 columns; scales and zero
+    // points (replaced every SC chunks)
+    constexpr int OFF_Q = TM * CHUNK * 2, OFF_S = OFF_Q + TN * CHUNK / 2, OFF_Z = OFF_S + TN * 16;
     __shared__ __attribute__((aligned(16))) uint8_t smem[OFF_Z + (Z ? TN * 8 : 0)];
 
     int tn;
@@ -452,17 +415,16 @@ __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
         }
     };
     auto stage = [&](int ch) {
-        uint8_t *d = smem + (ch & 1) * STAGE;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            *reinterpret_cast<u32x4 *>(d + A_BYTES + 1024 * (2 * wave + i) + put) = sq[i];
+            *reinterpret_cast<u32x4 *>(smem + OFF_Q + 1024 * (2 * wave + i) + put) = sq[i];
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 u32x4 v = pair_order(st[i][s]);
                 if constexpr (G < 128) {
                     if (ch * CHUNK + 32 * s >= p.K) v = u32x4{0, 0, 0, 0};
                 }
-                *reinterpret_cast<u32x4 *>(d + (4 * (2 * wave + i) + s) * 1024 + put) = v;
+                *reinterpret_cast<u32x4 *>(smem + (4 * (2 * wave + i) + s) * 1024 + put) = v;
             }
         }
     };
@@ -475,78 +437,62 @@ __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
     ScaleRegs<Z> sr;
-    auto put_scales = [&]() {
-        if (tid < TN) {
-            *reinterpret_cast<u32x4 *>(smem + OFF_S + 16 * tid) = sr.s;
-            if constexpr (Z) *reinterpret_cast<uint2 *>(smem + OFF_Z + 8 * tid) = sr.z;
-        }
-    };
-    int base = 0;
+    int base = 0, next = 0;                                  // block at index 0 of the scales; chunk of new ones
     if (nch > 0) {
         sr.load(p, srow, 0, nblk);
         fetch(0);
-        put_scales();
-        stage(0);
     }
-    __syncthreads();
-    const u32x4 one = u32x4{QT::ones(), QT::ones(), QT::ones(), QT::ones()};
+    const uint8_t *const la = smem + wm * 16384 + get;
+    const uint8_t *const lc = smem + OFF_Q + wn * 4096 + get;
 #pragma unroll 1
     for (int ch = 0; ch < nch; ++ch) {
-        const bool more = ch + 1 < nch;
-        const bool new_scales = more && (ch + 1) % SC == 0;
-        if (more) fetch(ch + 1);
-        if (new_scales) sr.load(p, srow, first_block(ch + 1), nblk);
-        const uint8_t *la = smem + (ch & 1) * STAGE + wm * 16384 + get;
-        const uint8_t *lq_ = smem + (ch & 1) * STAGE + A_BYTES + wn * 4096 + get;
+        if (ch == next) {
+            base = first_block(ch);
+            if (tid < TN) {
+                *reinterpret_cast<u32x4 *>(smem + OFF_S + 16 * tid) = sr.s;
+                if constexpr (Z) *reinterpret_cast<uint2 *>(smem + OFF_Z + 8 * tid) = sr.z;
+            }
+            next += SC;
+            if (next < nch) sr.load(p, srow, first_block(next), nblk);
+        }
+        stage(ch);
+        __syncthreads();
+        if (ch + 1 < nch) fetch(ch + 1);
         const int bi = first_block(ch) - base;
-        u32x4 a[4][4];
+        u32x4 w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j) w[j] = exchange(*reinterpret_cast<const u32x4 *>(lc + 1024 * j));
 #pragma unroll
-            for (int s = 0; s < 4; ++s) a[i][s] = *reinterpret_cast<const u32x4 *>(la + (4 * i + s) * 1024);
-        f32x4 sum[4][NBLK];
-        if constexpr (QT::SUMS)
+        for (int b = 0; b < NBLK; ++b) {
+            u32x4 a[4][SUB];
+            f32x4 sum[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                sum[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int b = 0; b < NBLK; ++b) {
-                    sum[i][b] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int s = b * SUB; s < (b + 1) * SUB; ++s) sum[i][b] = TI::mma16(a[i][s], one, sum[i][b]);
+                for (int s = 0; s < SUB; ++s) {
+                    a[i][s] = *reinterpret_cast<const u32x4 *>(la + (4 * i + b * SUB + s) * 1024);
+                    if constexpr (QT::SUMS) sum[i] = TI::mma16(a[i][s], QT::ones(), sum[i]);
                 }
+            }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const u32x4 w = exchange(*reinterpret_cast<const u32x4 *>(lq_ + 1024 * j));
-            const int row = wn * 64 + 16 * j + (lane & 15);
-            const Blocks<NBLK> blk = read_blocks<TI, NBLK, Z>(smem + OFF_S + 16 * row, smem + OFF_Z + 8 * row, bi);
-#pragma unroll
-            for (int b = 0; b < NBLK; ++b) {
+            for (int j = 0; j < 4; ++j) {
+                const int row = wn * 64 + 16 * j + (lane & 15);
+                const Blocks<1> blk = read_blocks<TI, 1, Z>(smem + OFF_S + 16 * row, smem + OFF_Z + 8 * row, bi + b);
                 f32x4 t[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) t[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int s = b * SUB; s < (b + 1) * SUB; ++s) {
-                    const u32x4 v = QT::values(w[s], blk.off[b]);
+                for (int s = 0; s < SUB; ++s) {
+                    const u32x4 v = QT::values(w[j][b * SUB + s], blk.off[0]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) t[i] = TI::mma16(a[i][s], v, t[i]);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x = QT::SUMS ? __builtin_fmaf(-blk.off[b], sum[i][b][e], t[i][e]) : t[i][e];
-                        acc[i][j][e] = __builtin_fmaf(blk.s[b], x, acc[i][j][e]);
-                    }
+                for (int i = 0; i < 4; ++i) add_block<TI>(acc[i][j], t[i], sum[i], blk.s[0], blk.off[0]);
             }
         }
-        if (more) stage(ch + 1);
         __syncthreads();
-        if (new_scales) {
-            // the last reader of the old scales is behind the barrier above
-            put_scales();
-            base = first_block(ch + 1);
-            __syncthreads();
-        }
     }
 
 #pragma unroll
@@ -566,10 +512,10 @@ __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
 
 // ---- entries -----------------------------------------------------------------------------------
 
-template <class TI, class TO, int G, int MT, int CG>
+template <class TI, class TO, int G, int CG>
 hipError_t launch_rows(const QuantParams &p, unsigned grid, hipStream_t s) {
-    if (p.zeros) hipLaunchKernelGGL((quant_rows<TI, TO, G, true, MT, CG>), dim3(grid), dim3(WAVES * 64), 0, s, p);
-    else hipLaunchKernelGGL((quant_rows<TI, TO, G, false, MT, CG>), dim3(grid), dim3(WAVES * 64), 0, s, p);
+    if (p.zeros) hipLaunchKernelGGL((quant_rows<TI, TO, G, true, CG>), dim3(grid), dim3(WAVES * 64), 0, s, p);
+    else hipLaunchKernelGGL((quant_rows<TI, TO, G, false, CG>), dim3(grid), dim3(WAVES * 64), 0, s, p);
     return hipGetLastError();
 }
 template <class TI, class TO, int G>
@@ -579,22 +525,16 @@ hipError_t launch_tile(const QuantParams &p, unsigned grid, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <class TI, class TO, int G>
-const QuantEntry *rows_entry(int mt, int cg) {
-    static const QuantEntry e[6] = {{launch_rows<TI, TO, G, 1, 1>, 16, 16, "quant_rows_16x16"},
-                                    {launch_rows<TI, TO, G, 1, 4>, 16, 64, "quant_rows_16x64"},
-                                    {launch_rows<TI, TO, G, 2, 1>, 32, 16, "quant_rows_32x16"},
-                                    {launch_rows<TI, TO, G, 2, 2>, 32, 32, "quant_rows_32x32"},
-                                    {launch_rows<TI, TO, G, 4, 1>, 64, 16, "quant_rows_64x16"},
-                                    {launch_rows<TI, TO, G, 4, 2>, 64, 32, "quant_rows_64x32"}};
-    for (const QuantEntry &x : e)
-        if (x.bm == 16 * mt && x.bn == 16 * cg) return &x;
-    return nullptr;
-}
 template <class TI, class TO>
-const QuantEntry *lookup_rows(int block, int mt, int cg) {
-    return block == 32 ? rows_entry<TI, TO, 32>(mt, cg) : block == 64 ? rows_entry<TI, TO, 64>(mt, cg)
-           : block == 128 ? rows_entry<TI, TO, 128>(mt, cg) : nullptr;
+const QuantEntry *lookup_rows(int block, int cg) {
+    static const QuantEntry e[6] = {{launch_rows<TI, TO, 32, 1>, 16, 16, "quant_rows_16x16"},
+                                    {launch_rows<TI, TO, 32, 4>, 16, 64, "quant_rows_16x64"},
+                                    {launch_rows<TI, TO, 64, 1>, 16, 16, "quant_rows_16x16"},
+                                    {launch_rows<TI, TO, 64, 4>, 16, 64, "quant_rows_16x64"},
+                                    {launch_rows<TI, TO, 128, 1>, 16, 16, "quant_rows_16x16"},
+                                    {launch_rows<TI, TO, 128, 4>, 16, 64, "quant_rows_16x64"}};
+    if ((cg != 1 && cg != 4) || (block != 32 && block != 64 && block != 128)) return nullptr;
+    return &e[(block == 32 ? 0 : block == 64 ? 2 : 4) + (cg == 4)];
 }
 template <class TI, class TO>
 const QuantEntry *lookup_tile(int block) {
@@ -607,16 +547,16 @@ const QuantEntry *lookup_tile(int block) {
 }  // namespace
 
 #if defined(TGE_PAIR_F16_F16)
-const QuantEntry *quant_rows_f16_f16(int b, int mt, int cg) { return lookup_rows<TF16, OF16>(b, mt, cg); }
+const QuantEntry *quant_rows_f16_f16(int b, int cg) { return lookup_rows<TF16, OF16>(b, cg); }
 const QuantEntry *quant_tile_f16_f16(int b) { return lookup_tile<TF16, OF16>(b); }
 #elif defined(TGE_PAIR_F16_F32)
-const QuantEntry *quant_rows_f16_f32(int b, int mt, int cg) { return lookup_rows<TF16, OF32>(b, mt, cg); }
+const QuantEntry *quant_rows_f16_f32(int b, int cg) { return lookup_rows<TF16, OF32>(b, cg); }
 const QuantEntry *quant_tile_f16_f32(int b) { return lookup_tile<TF16, OF32>(b); }
 #elif defined(TGE_PAIR_BF16_BF16)
-const QuantEntry *quant_rows_bf16_bf16(int b, int mt, int cg) { return lookup_rows<TBF16, OBF16>(b, mt, cg); }
+const QuantEntry *quant_rows_bf16_bf16(int b, int cg) { return lookup_rows<TBF16, OBF16>(b, cg); }
 const QuantEntry *quant_tile_bf16_bf16(int b) { return lookup_tile<TBF16, OBF16>(b); }
 #elif defined(TGE_PAIR_BF16_F32)
-const QuantEntry *quant_rows_bf16_f32(int b, int mt, int cg) { return lookup_rows<TBF16, OF32>(b, mt, cg); }
+const QuantEntry *quant_rows_bf16_f32(int b, int cg) { return lookup_rows<TBF16, OF32>(b, cg); }
 const QuantEntry *quant_tile_bf16_f32(int b) { return lookup_tile<TBF16, OF32>(b); }
 #else
 #error "define one TGE_PAIR_* macro of a 16-bit float type"

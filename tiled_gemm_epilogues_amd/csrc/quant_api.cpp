@@ -27,7 +27,7 @@ namespace {
 
 constexpr int64_t MAX_K = (int64_t)1 << 23;   // 2^16 chunks of 128 (see block_of in gemm_quant.hip)
 
-using RowsFn = const QuantEntry *(*)(int, int, int);
+using RowsFn = const QuantEntry *(*)(int, int);
 using TileFn = const QuantEntry *(*)(int);
 
 RowsFn rows_table(int ab, int cd) {
@@ -52,6 +52,20 @@ int64_t grid_of(const gemm_quant_plan &p, bool by_expert) {
     return tm * ceil_div(p.N, p.kernel->bn);
 }
 
+// Whether the 128 x 128 tiles beat the kernel for few rows (16 x 64).  Both take a time in
+// proportion to K; at K = 4096 a round of tiles takes 68 us however few there are and 0.195 us per
+// tile from two per CU on, the other kernel 0.0205 us per workgroup.  Measured (bf16, blocks of 128;
+// few rows -> tiles): 512 x 4096 x 4096 47 vs 69 us, 1024 x 4096 x 4096 87 -> 69, 2048 x 4096 x 4096
+// 169 -> 100, 2048 x 1024 x 4096 46 vs 68, 256 x 16384 x 2048 51 -> 41, 512 x 8192 x 8192 162 -> 127.
+// Experts' ranges end inside a tile: half a tile each is counted for them.
+bool tiles_pay(const gemm_quant_plan &p) {
+    const double ragged = p.groups > 1 ? 0.5 * (double)(p.rows < p.groups ? p.rows : p.groups) : 0.0;
+    const double few = ((double)p.rows / 16 + ragged) * (double)ceil_div(p.N, 64);
+    const double tiles = ((double)p.rows / 128 + ragged) * (double)ceil_div(p.N, 128);
+    const double t = 0.195 * tiles;
+    return 0.0205 * few > (t > 68.0 ? t : 68.0);
+}
+
 }  // namespace
 
 extern "C" {
@@ -69,7 +83,7 @@ gemm_status_t gemm_quant_plan_create(gemm_quant_plan_t *out, const gemm_quant_de
     case GEMM_ALGO_AUTO: if (tile != 0) return GEMM_STATUS_INVALID_VALUE; break;
     case GEMM_ALGO_FAST: if (tile != 0 && tile != 128) return GEMM_STATUS_INVALID_VALUE; break;
     case GEMM_ALGO_SKINNY:
-        if (tile != 0 && tile != 16 && tile != 32 && tile != 64) return GEMM_STATUS_INVALID_VALUE;
+        if (tile != 0 && tile != 16 && tile != 64) return GEMM_STATUS_INVALID_VALUE;
         break;
     default: return GEMM_STATUS_INVALID_VALUE;
     }
@@ -93,17 +107,14 @@ gemm_status_t gemm_quant_plan_create(gemm_quant_plan_t *out, const gemm_quant_de
     p.stride_q = d->stride_q; p.stride_s = d->stride_s; p.stride_bias = d->stride_bias;
     p.ab = ab; p.cd = cd; p.epi = epi; p.zeros = d->zeros != 0;
     const int g = d->block >= 128 ? 128 : (int)d->block;
-    const int64_t avg = ceil_div(d->rows, d->groups);   // rows of an expert, on average
     // rows kernels: the wide one where it still gives every CU a workgroup
-    const auto rows_kernel = [&](int mt) {
-        const QuantEntry *wide = rows_table(ab, cd)(g, mt, mt == 1 ? 4 : 2);
-        p.kernel = wide;
-        return grid_of(p, p.groups > 1) >= 256 ? wide : rows_table(ab, cd)(g, mt, 1);
+    const auto rows_kernel = [&]() {
+        p.kernel = rows_table(ab, cd)(g, 4);
+        return grid_of(p, p.groups > 1) >= 256 ? p.kernel : rows_table(ab, cd)(g, 1);
     };
-    if (algo == GEMM_ALGO_SKINNY) p.kernel = rows_kernel(tile ? tile / 16 : 1);
+    if (algo == GEMM_ALGO_SKINNY) p.kernel = tile ? rows_table(ab, cd)(g, tile / 16) : rows_kernel();
     else if (algo == GEMM_ALGO_FAST) p.kernel = tile_table(ab, cd)(g);
-    else if (avg <= 64) p.kernel = rows_kernel(avg <= 16 ? 1 : avg <= 32 ? 2 : 4);
-    else p.kernel = tile_table(ab, cd)(g);
+    else p.kernel = tiles_pay(p) ? tile_table(ab, cd)(g) : rows_kernel();
     if (grid_of(p, true) >= LIM31) return GEMM_STATUS_NOT_SUPPORTED;
     gemm_quant_plan *q = new (std::nothrow) gemm_quant_plan(p);
     if (!q) return GEMM_STATUS_ALLOC_FAILED;
