@@ -359,7 +359,7 @@ gemm_status_t gemm_plan_describe(gemm_plan_t plan, char *buf, size_t len);
  *
  * Types: F32 -> F32, F16 -> F16 | F32, BF16 -> BF16 | F32, accumulated in fp32; bias and bias_grad
  * are fp32.  Any leading dimension and alignment is allowed (the element's own alignment is
- * required); the fast kernels need 16-byte aligned A and B, leading dimensions and strides.  A
+ * required); 16-byte aligned A and B, leading dimensions and strides take the faster load paths.  A
  * plan holds no device memory: it may be shared between host threads, streams and graphs.
  */
 typedef struct gemm_grouped_plan *gemm_grouped_plan_t;
@@ -367,9 +367,10 @@ typedef struct gemm_grouped_plan *gemm_grouped_plan_t;
 /*
  * Description of a rows plan.  rows: rows of A, C and D; B_e is K x N (op_b N; ldb >= N) or stored
  * N x K (op_b T; ldb >= K) at B + e * stride_b, bias_e at bias + e * stride_bias (a zero stride
- * shares it).  algo: AUTO, or FAST (with tile 256 or 128; 0: the plan's choice), GENERAL (tile 128
- * or 64) or SKINNY (tile 16, 32, 48 or 64: rows per workgroup) to pin a kernel, which falls back
- * to the general one where its preconditions do not hold.
+ * shares it).  algo: AUTO, or FAST (with tile 256 or 128; 0: 128), FAST_STAGED (the 128-wide
+ * tiles on operands of any alignment), GENERAL (tile 128 or 64) or SKINNY (for few rows per
+ * expert: 16 rows and, by tile, 64 or with B transposed 16 columns per workgroup) to pin a kernel,
+ * which falls back to the general one where its preconditions do not hold.
  */
 typedef struct {
     int64_t rows, N, K, groups;

@@ -506,17 +506,25 @@ class _GroupedBase:
         """Device pointer of tensor t after checking it; raw ints and None pass as is."""
         if t is None or isinstance(t, int):
             return t
+        # one expression for a tensor that fits (a small product takes about as long as the checks)
+        dtype, need, row_len = self._spec[what]
+        if (t.dtype is dtype and t.get_device() == device and t.is_contiguous() and t.numel() >= need
+                and (row_len is None or t.dim() < 2 or t.size(-1) == row_len)):
+            return t.data_ptr()
         if t.get_device() != device:
             raise ValueError(f"{what} is on {t.device}, the current device is cuda:{device}"
                              if t.is_cuda else f"{what} must be a device tensor")
         self.check(what, t)
         return t.data_ptr()
 
-    @staticmethod
-    def _stream(stream, device):
+    def _start(self, entry):
+        """What every run needs: the C entry point, and torch."""
         import torch
+        self._torch, self._entry = torch, entry
+
+    def _stream(self, stream, device):
         if stream is None:
-            return torch.cuda.current_stream(device).cuda_stream
+            return self._torch._C._cuda_getCurrentRawStream(device)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -543,6 +551,7 @@ class GroupedPlan(_GroupedBase):
         if st != STATUS_SUCCESS:
             raise GemmError(st, "gemm_grouped_plan_create")
         self._h = h
+        self._start(lib().gemm_grouped_run)
         tab, tcd = _torch_dtype(ab), _torch_dtype(cd)
         b = _span(b_rows, b_cols, self.ldb)
         cdn = _span(rows, N, self.ldc)
@@ -560,10 +569,9 @@ class GroupedPlan(_GroupedBase):
         C is read when beta != 0 or the epilogue is "gate".  Rows of D outside the ranges are left
         as they are.  Raises ValueError / TypeError before anything is enqueued when a tensor does
         not fit the plan."""
-        import torch
-        dev = torch.cuda.current_device()
+        dev = self._torch.cuda.current_device()
         ptr = self._ptr
-        st = lib().gemm_grouped_run(
+        st = self._entry(
             self._h, ptr("A", A, dev), ptr("B", B, dev),
             ptr("C", C, dev) if beta != 0 or self._gate else None, ptr("D", D, dev),
             ptr("bias", bias, dev) if self._has_bias else None, ptr("offsets", offsets, dev),
@@ -592,6 +600,7 @@ class GroupedGradPlan(_GroupedBase):
         if st != STATUS_SUCCESS:
             raise GemmError(st, "gemm_grouped_grad_plan_create")
         self._h = h
+        self._start(lib().gemm_grouped_grad_run)
         tab, tcd = _torch_dtype(ab), _torch_dtype(cd)
         c = _span(M, N, self.ldc)
         cdn = (groups - 1) * self.stride_c + c if c else 0
@@ -605,10 +614,9 @@ class GroupedGradPlan(_GroupedBase):
     def run(self, A, B, C, D, offsets, bias_grad=None, alpha=1.0, beta=0.0, stream=None):
         """Enqueue on `stream` (as Plan.run).  C is read when beta != 0 (C == D adds into the
         gradients); bias_grad (groups x N, fp32) is overwritten, None leaves it out."""
-        import torch
-        dev = torch.cuda.current_device()
+        dev = self._torch.cuda.current_device()
         ptr = self._ptr
-        st = lib().gemm_grouped_grad_run(
+        st = self._entry(
             self._h, ptr("A", A, dev), ptr("B", B, dev), ptr("C", C, dev) if beta != 0 else None,
             ptr("D", D, dev), ptr("bias_grad", bias_grad, dev), ptr("offsets", offsets, dev),
             float(alpha), float(beta), self._stream(stream, dev))
@@ -645,6 +653,7 @@ class QuantPlan(_GroupedBase):
         if st != STATUS_SUCCESS:
             raise GemmError(st, "gemm_quant_plan_create")
         self._h = h
+        self._start(lib().gemm_quant_run)
         tab, tcd = _torch_dtype(ab), _torch_dtype(cd)
         cdn = _span(rows, N, self.ldc)
         more = groups - 1
@@ -664,10 +673,9 @@ class QuantPlan(_GroupedBase):
         """Enqueue on `stream` (as Plan.run).  zeros: None for a plan without them; offsets: as in
         GroupedPlan.run, None with one weight matrix for all rows; C is read when beta != 0.  Raises
         ValueError / TypeError before anything is enqueued when a tensor does not fit the plan."""
-        import torch
-        dev = torch.cuda.current_device()
+        dev = self._torch.cuda.current_device()
         ptr = self._ptr
-        st = lib().gemm_quant_run(
+        st = self._entry(
             self._h, ptr("A", A, dev), ptr("Q", Q, dev), ptr("scales", scales, dev),
             ptr("zeros", zeros, dev) if self.zeros else None, ptr("C", C, dev) if beta != 0 else None,
             ptr("D", D, dev), ptr("bias", bias, dev) if self._has_bias else None,

@@ -48,12 +48,12 @@ def steps():
         for pair in pairs:
             add(name + ".hip", f"{name}_{pair.lower()}", f"-DTGE_PAIR_{pair}")
     # the same kernels on products grouped by expert (float types)
-    for name, pairs in (("gemm_kernels", GROUPED_PAIRS + ["F32_F32"]), ("gemm_fast", GROUPED_PAIRS),
-                        ("gemm_skinny", GROUPED_PAIRS)):
+    for name, pairs in (("gemm_kernels", GROUPED_PAIRS + ["F32_F32"]), ("gemm_fast", GROUPED_PAIRS)):
         for pair in pairs:
             add(name + ".hip", f"grouped_{name}_{pair.lower()}", f"-DTGE_PAIR_{pair}", "-DTGE_GROUPED")
     for pair in GROUPED_PAIRS:
-        add("gemm_quant.hip", f"gemm_quant_{pair.lower()}", f"-DTGE_PAIR_{pair}")
+        for name in ("gemm_rows16", "gemm_quant"):
+            add(name + ".hip", f"{name}_{pair.lower()}", f"-DTGE_PAIR_{pair}")
     for name in ("gemm_complex", "gemm_diag", "gemm_repack"):
         add(name + ".hip", name)
     for name in ("gemm_api", "grouped_api", "quant_api"):

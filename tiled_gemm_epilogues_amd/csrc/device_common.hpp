@@ -120,6 +120,23 @@ __device__ __forceinline__ u32x4 ldg16_partial(const uint8_t *p, int nvalid) {
     return v;
 }
 
+// Elements k .. k+7 of a row of K >= 8 two-byte elements, zero past its end: a whole load that ends
+// with the row at the latest, moved down.
+__device__ __forceinline__ u32x4 ldg16_row_end(const uint8_t *row, int k, int K) {
+    const int at = min(k, K - 8), past = k - at;
+    u32x4 v = ldg16(row + 2 * (int64_t)at);
+    uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+    if (past >= 4) {
+        lo = hi;
+        hi = 0;
+    }
+    const int n = 16 * (past & 3);
+    lo = (lo >> n) | (n ? hi << (64 - n) : 0);
+    hi >>= n;
+    if (past >= 8) lo = 0;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
 // Transpose a VE x VE block of E-byte elements held as VE rows of 16 bytes.
 template <int E>
 __device__ __forceinline__ void transpose_block(const u32x4 *in, u32x4 *out);

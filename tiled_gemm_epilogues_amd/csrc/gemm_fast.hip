@@ -547,7 +547,7 @@ struct Sched {
 template <class TI, class TO, bool AK, bool BK, int MF, bool XF, bool RS = false, int TL = 256,
           int GRP = GROUP_NONE>
 __global__ __launch_bounds__(NT, TL == 256 ? 1 : 2) void gemm_fast(ParamsOf<GRP> p) {
-    static_assert(TL == 256 || (TL == 128 && MF == 16 && !XF && !RS), "tile variants");
+    static_assert(TL == 256 || (TL == 128 && MF == 16 && !XF), "tile variants");
     using acc_t = typename TI::acc_t;
     using accv_t = typename std::conditional<MF == 32, typename TI::accv_t, typename TI::accv16_t>::type;
     using SH = Shape<MF, TL>;
@@ -884,27 +884,31 @@ const KernelEntry *lookup_fast128(int op_a, int op_b) {
 
 // ---- grouped instances -------------------------------------------------------------------------
 
-template <class TI, class TO, int TL, bool AT, bool BT, int GRP>
+template <class TI, class TO, int TL, bool AT, bool BT, int GRP, bool RS = false>
 hipError_t launch_grouped(const GroupedParams &p, unsigned grid, hipStream_t s) {
     constexpr int MF = TL == 256 ? fast_mf<AT, BT>() : 16;
-    hipLaunchKernelGGL((gemm_fast<TI, TO, !AT, BT, MF, false, false, TL, GRP>), dim3(grid), dim3(NT), 0, s, p);
+    hipLaunchKernelGGL((gemm_fast<TI, TO, !AT, BT, MF, false, RS, TL, GRP>), dim3(grid), dim3(NT), 0, s, p);
     return hipGetLastError();
 }
 
 template <class TI, class TO>
-const GroupedEntry *lookup_grouped(int mode, int op_b, int tile) {
-    if (tile != 256 && tile != 128) return nullptr;
+const GroupedEntry *lookup_grouped(int mode, int op_b, int tile, int rs) {
+    if ((tile != 256 && tile != 128) || (rs && tile != 128)) return nullptr;
     const int i = tile == 256 ? 0 : 1;
     static const GroupedEntry rows[4] = {
         {launch_grouped<TI, TO, 256, false, false, GROUP_ROWS>, 256, 256, "gemm_fast_256x256"},
         {launch_grouped<TI, TO, 128, false, false, GROUP_ROWS>, 128, 128, "gemm_fast_128x128"},
         {launch_grouped<TI, TO, 256, false, true, GROUP_ROWS>, 256, 256, "gemm_fast_256x256"},
         {launch_grouped<TI, TO, 128, false, true, GROUP_ROWS>, 128, 128, "gemm_fast_128x128"}};
+    static const GroupedEntry staged[3] = {
+        {launch_grouped<TI, TO, 128, false, false, GROUP_ROWS, true>, 128, 128, "gemm_fast_128x128_rs"},
+        {launch_grouped<TI, TO, 128, false, true, GROUP_ROWS, true>, 128, 128, "gemm_fast_128x128_rs"},
+        {launch_grouped<TI, TO, 128, true, false, GROUP_K, true>, 128, 128, "gemm_fast_128x128_rs"}};
     static const GroupedEntry k[2] = {
         {launch_grouped<TI, TO, 256, true, false, GROUP_K>, 256, 256, "gemm_fast_256x256"},
         {launch_grouped<TI, TO, 128, true, false, GROUP_K>, 128, 128, "gemm_fast_128x128"}};
-    if (mode == GROUP_ROWS && (op_b == 0 || op_b == 1)) return &rows[2 * op_b + i];
-    if (mode == GROUP_K && op_b == 0) return &k[i];
+    if (mode == GROUP_ROWS && (op_b == 0 || op_b == 1)) return rs ? &staged[op_b] : &rows[2 * op_b + i];
+    if (mode == GROUP_K && op_b == 0) return rs ? &staged[2] : &k[i];
     return nullptr;
 }
 
@@ -913,13 +917,13 @@ const GroupedEntry *lookup_grouped(int mode, int op_b, int tile) {
 #if defined(TGE_GROUPED)
 // the grouped instances are a build of their own (one object per type pair)
 #if defined(TGE_PAIR_F16_F16)
-const GroupedEntry *grouped_fast_f16_f16(int m, int b, int t) { return lookup_grouped<TF16, OF16>(m, b, t); }
+const GroupedEntry *grouped_fast_f16_f16(int m, int b, int t, int rs) { return lookup_grouped<TF16, OF16>(m, b, t, rs); }
 #elif defined(TGE_PAIR_F16_F32)
-const GroupedEntry *grouped_fast_f16_f32(int m, int b, int t) { return lookup_grouped<TF16, OF32>(m, b, t); }
+const GroupedEntry *grouped_fast_f16_f32(int m, int b, int t, int rs) { return lookup_grouped<TF16, OF32>(m, b, t, rs); }
 #elif defined(TGE_PAIR_BF16_BF16)
-const GroupedEntry *grouped_fast_bf16_bf16(int m, int b, int t) { return lookup_grouped<TBF16, OBF16>(m, b, t); }
+const GroupedEntry *grouped_fast_bf16_bf16(int m, int b, int t, int rs) { return lookup_grouped<TBF16, OBF16>(m, b, t, rs); }
 #elif defined(TGE_PAIR_BF16_F32)
-const GroupedEntry *grouped_fast_bf16_f32(int m, int b, int t) { return lookup_grouped<TBF16, OF32>(m, b, t); }
+const GroupedEntry *grouped_fast_bf16_f32(int m, int b, int t, int rs) { return lookup_grouped<TBF16, OF32>(m, b, t, rs); }
 #else
 #error "define one TGE_PAIR_* macro of a 16-bit float type"
 #endif

@@ -196,21 +196,24 @@ hipError_t finish_i8_i32(const GemmParams &p, hipStream_t s);
 // op_b: 0 = N, 1 = T (GROUP_K: 0).  Preconditions as for the kernels above, for every range:
 //   any    the general kernel, tile CFG_128 or CFG_64: none
 //   fast   tile 256 or 128, direct loads: 16-byte aligned pointers, leading dimensions and strides;
-//          GROUP_ROWS: K >= 64, N % 8 == 0 when op_b is N; GROUP_K: M % 8 == 0 and N % 8 == 0
-//   skinny GROUP_ROWS, 16 * mt rows per workgroup: fast's, and K % 32 == 0
+//          GROUP_ROWS: K >= 64, N % 8 == 0 when op_b is N; GROUP_K: M % 8 == 0 and N % 8 == 0.
+//          rs = 1 (tile 128): register-staged loads; at least 8 elements (one chunk) along M and N,
+//          nothing else
+//   rows16 GROUP_ROWS, 16 rows and 16 * cg columns per workgroup (cg 4; 1 too when op_b is T):
+//          K >= 8, N >= 8 when op_b is N
 const GroupedEntry *grouped_any_f32_f32(int mode, int op_b, int cfg);
 const GroupedEntry *grouped_any_f16_f16(int mode, int op_b, int cfg);
 const GroupedEntry *grouped_any_f16_f32(int mode, int op_b, int cfg);
 const GroupedEntry *grouped_any_bf16_bf16(int mode, int op_b, int cfg);
 const GroupedEntry *grouped_any_bf16_f32(int mode, int op_b, int cfg);
-const GroupedEntry *grouped_fast_f16_f16(int mode, int op_b, int tile);
-const GroupedEntry *grouped_fast_f16_f32(int mode, int op_b, int tile);
-const GroupedEntry *grouped_fast_bf16_bf16(int mode, int op_b, int tile);
-const GroupedEntry *grouped_fast_bf16_f32(int mode, int op_b, int tile);
-const GroupedEntry *grouped_skinny_f16_f16(int op_b, int mt);
-const GroupedEntry *grouped_skinny_f16_f32(int op_b, int mt);
-const GroupedEntry *grouped_skinny_bf16_bf16(int op_b, int mt);
-const GroupedEntry *grouped_skinny_bf16_f32(int op_b, int mt);
+const GroupedEntry *grouped_fast_f16_f16(int mode, int op_b, int tile, int rs);
+const GroupedEntry *grouped_fast_f16_f32(int mode, int op_b, int tile, int rs);
+const GroupedEntry *grouped_fast_bf16_bf16(int mode, int op_b, int tile, int rs);
+const GroupedEntry *grouped_fast_bf16_f32(int mode, int op_b, int tile, int rs);
+const GroupedEntry *grouped_rows16_f16_f16(int op_b, int cg);
+const GroupedEntry *grouped_rows16_f16_f32(int op_b, int cg);
+const GroupedEntry *grouped_rows16_bf16_bf16(int op_b, int cg);
+const GroupedEntry *grouped_rows16_bf16_f32(int op_b, int cg);
 
 // Products with 4-bit weights (gemm_quant.hip): W_e[n][k] = scale * (code - zero), codes packed
 // two per byte along k (low half: even k), one scale (of A's type) and zero point (uint8; nullptr:

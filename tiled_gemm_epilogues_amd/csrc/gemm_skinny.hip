@@ -103,9 +103,8 @@ __device__ __forceinline__ void wait_vm_atmost(int n) {
 // columns per workgroup (64, or 16 with B transposed).
 // Grid: (k split, column block) pairs of every product: p.tiles_m holds the number of k splits
 // S, p.tiles_n the number of CB-column blocks.
-// GRP = GROUP_ROWS: 16 * MT rows of one expert per workgroup, no k split.
-template <class TI, class TO, int MT, bool BT, int CB, int GRP = GROUP_NONE>
-__global__ __launch_bounds__(NT, 1) void gemm_skinny(ParamsOf<GRP> p) {
+template <class TI, class TO, int MT, bool BT, int CB>
+__global__ __launch_bounds__(NT, 1) void gemm_skinny(GemmParams p) {
     static_assert(CB == NB || (CB == NB_NARROW && BT), "narrow blocks need rows of B along K");
     static_assert(TI::E == 2 || BT, "int8: B transposed only (no transposing byte reads here)");
     constexpr int ES = TI::E;                           // input element bytes
@@ -127,20 +126,14 @@ __global__ __launch_bounds__(NT, 1) void gemm_skinny(ParamsOf<GRP> p) {
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int prod = 0, S = 1, split = 0, cb = 0;
-    if constexpr (GRP == GROUP_ROWS) {
-        if (!select_rows<ES, (int)sizeof(typename TO::T)>(p, blockIdx.x, 16 * MT, cb)) return;
-    } else {
-        const int per = p.tiles_m * p.tiles_n;
-        prod = blockIdx.x / per;                        // product of the batch
-        const int lid = select_batch<ES, (int)sizeof(typename TO::T)>(p, blockIdx.x, per);
-        S = p.tiles_m;
-        split = lid / p.tiles_n;
-        cb = lid - split * p.tiles_n;
-    }
+    const int per = p.tiles_m * p.tiles_n;
+    const int prod = blockIdx.x / per;                  // product of the batch
+    const int lid = select_batch<ES, (int)sizeof(typename TO::T)>(p, blockIdx.x, per);
+    const int S = p.tiles_m;
+    const int split = lid / p.tiles_n, cb = lid - split * p.tiles_n;
     const int n0 = cb * CB;
-    const uint8_t *A = dma_base<GRP>(p.A);
-    const uint8_t *B = dma_base<GRP>(p.B);
+    const uint8_t *A = static_cast<const uint8_t *>(p.A);
+    const uint8_t *B = static_cast<const uint8_t *>(p.B);
 
     // chunks [c0, c1) of this wave: the split's share of K, divided over the four waves
     const int nch_all = p.K / KCH;
@@ -323,12 +316,7 @@ __global__ __launch_bounds__(NT, 1) void gemm_skinny(ParamsOf<GRP> p) {
             if (m >= p.M) continue;
             const int64_t idx = (int64_t)m * p.ldc + n;
             float x = p.alpha * sum[t][r];
-            if constexpr (GRP == GROUP_ROWS) {
-                if (p.gate) x = (float)C[idx] > 0.0f ? x : 0.0f;
-                else if (p.has_beta) x += p.beta * (float)C[idx];
-            } else {
-                if (p.has_beta) x += p.beta * c_in_f(C[idx], p.xform_c);
-            }
+            if (p.has_beta) x += p.beta * c_in_f(C[idx], p.xform_c);
             x += bv;
             if (p.relu) x = x > 0.0f ? x : 0.0f;
             D[idx] = (T)x;
@@ -439,49 +427,9 @@ const KernelEntry *lookup_skinny(int op_b, int mt, int narrow) {
     }
 }
 
-// ---- grouped instances -------------------------------------------------------------------------
-
-template <class TI, class TO, int MT, bool BT>
-hipError_t launch_grouped(const GroupedParams &p, unsigned grid, hipStream_t s) {
-    hipLaunchKernelGGL((gemm_skinny<TI, TO, MT, BT, NB, GROUP_ROWS>), dim3(grid), dim3(NT), 0, s, p);
-    return hipGetLastError();
-}
-
-template <class TI, class TO>
-const GroupedEntry *lookup_grouped(int op_b, int mt) {
-    if (op_b < 0 || op_b > 1 || mt < 1 || mt > 4) return nullptr;
-    if constexpr (TI::E == 1) {
-        return nullptr;
-    } else {
-        static const GroupedEntry t[8] = {
-            {launch_grouped<TI, TO, 1, false>, 16, NB, "gemm_skinny_m16"},
-            {launch_grouped<TI, TO, 2, false>, 32, NB, "gemm_skinny_m32"},
-            {launch_grouped<TI, TO, 3, false>, 48, NB, "gemm_skinny_m48"},
-            {launch_grouped<TI, TO, 4, false>, 64, NB, "gemm_skinny_m64"},
-            {launch_grouped<TI, TO, 1, true>, 16, NB, "gemm_skinny_m16"},
-            {launch_grouped<TI, TO, 2, true>, 32, NB, "gemm_skinny_m32"},
-            {launch_grouped<TI, TO, 3, true>, 48, NB, "gemm_skinny_m48"},
-            {launch_grouped<TI, TO, 4, true>, 64, NB, "gemm_skinny_m64"}};
-        return &t[4 * op_b + mt - 1];
-    }
-}
-
 }  // namespace
 
-#if defined(TGE_GROUPED)
-// the grouped instances are a build of their own (one object per type pair)
 #if defined(TGE_PAIR_F16_F16)
-const GroupedEntry *grouped_skinny_f16_f16(int b, int mt) { return lookup_grouped<TF16, OF16>(b, mt); }
-#elif defined(TGE_PAIR_F16_F32)
-const GroupedEntry *grouped_skinny_f16_f32(int b, int mt) { return lookup_grouped<TF16, OF32>(b, mt); }
-#elif defined(TGE_PAIR_BF16_BF16)
-const GroupedEntry *grouped_skinny_bf16_bf16(int b, int mt) { return lookup_grouped<TBF16, OBF16>(b, mt); }
-#elif defined(TGE_PAIR_BF16_F32)
-const GroupedEntry *grouped_skinny_bf16_f32(int b, int mt) { return lookup_grouped<TBF16, OF32>(b, mt); }
-#else
-#error "define one TGE_PAIR_* macro of a 16-bit float type"
-#endif
-#elif defined(TGE_PAIR_F16_F16)
 const KernelEntry *skinny_f16_f16(int b, int mt, int nw) { return lookup_skinny<TF16, OF16>(b, mt, nw); }
 hipError_t finish_f16_f16(const GemmParams &p, hipStream_t s) { return launch_finish<OF16>(p, s); }
 #elif defined(TGE_PAIR_F16_F32)

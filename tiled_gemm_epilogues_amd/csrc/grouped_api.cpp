@@ -30,7 +30,8 @@ namespace {
 constexpr int64_t FAST_MIN_K = 64;         // one slab of the fast kernel (16-bit inputs)
 
 using TableFn = const GroupedEntry *(*)(int, int, int);
-using SkinnyFn = const GroupedEntry *(*)(int, int);
+using FastFn = const GroupedEntry *(*)(int, int, int, int);
+using RowsFn = const GroupedEntry *(*)(int, int);
 
 TableFn any_table(int ab, int cd) {
     if (ab == GEMM_F32 && cd == GEMM_F32) return tge::grouped_any_f32_f32;
@@ -41,15 +42,9 @@ TableFn any_table(int ab, int cd) {
     return nullptr;
 }
 
-TableFn fast_table(int ab, int cd) {
+FastFn fast_table(int ab, int cd) {
     if (ab == GEMM_F16) return cd == GEMM_F16 ? tge::grouped_fast_f16_f16 : tge::grouped_fast_f16_f32;
     if (ab == GEMM_BF16) return cd == GEMM_BF16 ? tge::grouped_fast_bf16_bf16 : tge::grouped_fast_bf16_f32;
-    return nullptr;
-}
-
-SkinnyFn skinny_table(int ab, int cd) {
-    if (ab == GEMM_F16) return cd == GEMM_F16 ? tge::grouped_skinny_f16_f16 : tge::grouped_skinny_f16_f32;
-    if (ab == GEMM_BF16) return cd == GEMM_BF16 ? tge::grouped_skinny_bf16_bf16 : tge::grouped_skinny_bf16_f32;
     return nullptr;
 }
 
@@ -98,6 +93,13 @@ gemm_status_t launch(const gemm_grouped_plan &p, const void *A, const void *B, c
                                                                                 : GEMM_STATUS_HIP_ERROR;
 }
 
+// Whether the kernel for few rows (16 rows per workgroup) beats the 128-wide tiles, which waste most
+// of a tile but move the weights at full rate once there are enough of them: up to 64 rows per
+// expert where the tiles do not fill the chip, and only up to 6 where they do.  Measured (bf16, N
+// 2048, K 4096; few rows -> tiles): 8 experts: 128 rows 28 vs 54 us, 256 31 vs 56, 512 47 vs 55; 64
+// experts: 64 rows 106 vs 146 us, 512 186 vs 176, 2048 249 vs 181, 4096 365 vs 232.
+bool few_rows_pay(int64_t avg, double tiles) { return avg <= (tiles >= 384 ? 6 : 64); }
+
 // Hands a finished plan out, with its description.
 gemm_status_t finish_plan(gemm_grouped_plan_t *out, const gemm_grouped_plan &p, const char *what) {
     const GroupedEntry *k = p.fast ? p.fast : p.any;
@@ -109,6 +111,12 @@ gemm_status_t finish_plan(gemm_grouped_plan_t *out, const gemm_grouped_plan &p, 
              (long long)grid_of(p, *k, false));
     *out = q;
     return GEMM_STATUS_SUCCESS;
+}
+
+RowsFn rows16_table(int ab, int cd) {
+    if (ab == GEMM_F16) return cd == GEMM_F16 ? tge::grouped_rows16_f16_f16 : tge::grouped_rows16_f16_f32;
+    if (ab == GEMM_BF16) return cd == GEMM_BF16 ? tge::grouped_rows16_bf16_bf16 : tge::grouped_rows16_bf16_f32;
+    return nullptr;
 }
 
 }  // namespace
@@ -127,9 +135,10 @@ gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grou
     switch (algo) {
     case GEMM_ALGO_AUTO: if (tile != 0) return GEMM_STATUS_INVALID_VALUE; break;
     case GEMM_ALGO_FAST: if (tile != 0 && tile != 256 && tile != 128) return GEMM_STATUS_INVALID_VALUE; break;
+    case GEMM_ALGO_FAST_STAGED: if (tile != 0 && tile != 128) return GEMM_STATUS_INVALID_VALUE; break;
     case GEMM_ALGO_GENERAL: if (tile != 0 && tile != 128 && tile != 64) return GEMM_STATUS_INVALID_VALUE; break;
     case GEMM_ALGO_SKINNY:
-        if (tile != 0 && tile != 16 && tile != 32 && tile != 48 && tile != 64) return GEMM_STATUS_INVALID_VALUE;
+        if (tile != 0 && tile != 64 && !(tile == 16 && op_b == GEMM_OP_T)) return GEMM_STATUS_INVALID_VALUE;
         break;
     default: return GEMM_STATUS_INVALID_VALUE;
     }
@@ -151,21 +160,51 @@ gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grou
     p.rows = d->rows; p.N = d->N; p.K = d->K; p.groups = d->groups;
     p.lda = d->lda; p.ldb = d->ldb; p.ldc = d->ldc; p.stride_b = d->stride_b; p.stride_bias = d->stride_bias;
     p.ab = ab; p.cd = cd; p.epi = epi;
-    const int64_t avg = ceil_div(d->rows, d->groups);   // rows of an expert, on average
+    // Kernels: `any` runs whatever the pointers' alignment is, `fast` on aligned ones.
+    const TableFn general = any_table(ab, cd);
+    const bool t = op_b == GEMM_OP_T;
+    const int64_t avg = ceil_div(d->rows, d->groups);                      // rows of an expert, on average
+    const int64_t n = d->rows < d->groups ? d->rows : d->groups;           // experts with rows, at most
+    const double tiles = ((double)d->rows / 128 + 0.5 * (double)n) * (double)ceil_div(d->N, 128);
     const bool small = algo == GEMM_ALGO_GENERAL && tile ? tile == 64 : avg < 128 || d->N < 128;
-    p.any = any_table(ab, cd)(tge::GROUP_ROWS, op_b, small ? tge::CFG_64 : tge::CFG_128);
-    // direct loads: whole 16-byte chunks, and 32-bit offsets within a tile's rows
+    p.any = general(tge::GROUP_ROWS, op_b, small ? tge::CFG_64 : tge::CFG_128);
+    const bool offsets_ok = d->lda * eab * 256 < LIM31;                    // 32-bit offsets within a tile's rows
+    const bool staged_ok = eab == 2 && d->N >= 8 && d->K > 0 && offsets_ok;
+    const bool rows16_ok = eab == 2 && d->K >= 8 && (t || d->N >= 8);
+    // direct loads: whole 16-byte chunks
     const bool fast_ok = eab == 2 && d->K >= FAST_MIN_K && d->lda % 8 == 0 && d->ldb % 8 == 0 &&
-                         d->stride_b % 8 == 0 && (op_b == GEMM_OP_T || (d->N % 8 == 0 && d->N > 0)) &&
-                         d->lda * eab * 256 < LIM31;
-    const bool skinny_ok = fast_ok && d->K % 32 == 0;
-    if (algo == GEMM_ALGO_SKINNY) {
-        if (skinny_ok) p.fast = skinny_table(ab, cd)(op_b, tile ? tile / 16 : 1);
-    } else if (algo == GEMM_ALGO_FAST) {
-        if (fast_ok) p.fast = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, tile ? tile : 128);
-    } else if (algo == GEMM_ALGO_AUTO && fast_ok) {
-        if (skinny_ok && avg <= 32) p.fast = skinny_table(ab, cd)(op_b, avg <= 8 ? 1 : avg <= 16 ? 2 : 4);
-        else p.fast = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, avg >= 1024 ? 256 : 128);
+                         d->stride_b % 8 == 0 && (t || (d->N % 8 == 0 && d->N > 0)) && offsets_ok;
+    // 16 x 64 tiles where they give every CU a workgroup, else 16 x 16 (B transposed): 4097 x 4097, one
+    // row, 18.2 -> 13.4 us; 8 rows over 16 experts, 1024 x 2048, even; but 200 rows over 8 experts,
+    // 1001 x 1001, 15.2 us with 16 x 64 tiles and 24.0 with 16 x 16
+    const auto rows16 = [&]() {
+        p.any = rows16_table(ab, cd)(op_b, 4);
+        if (t && grid_of(p, *p.any, false) < 256) p.any = rows16_table(ab, cd)(op_b, 1);
+    };
+    switch (algo) {
+    case GEMM_ALGO_SKINNY:
+        if (rows16_ok && tile) p.any = rows16_table(ab, cd)(op_b, tile / 16);
+        else if (rows16_ok) rows16();
+        break;
+    case GEMM_ALGO_FAST:
+        if (fast_ok) p.fast = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, tile ? tile : 128, 0);
+        break;
+    case GEMM_ALGO_FAST_STAGED:
+        if (staged_ok) p.any = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, 128, 1);
+        break;
+    case GEMM_ALGO_AUTO:
+        if (rows16_ok && few_rows_pay(avg, tiles)) {
+            rows16();
+        } else {
+            if (fast_ok) p.fast = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, avg >= 1024 ? 256 : 128, 0);
+            // the general kernel's 64-wide tiles keep up while 128-wide ones leave CUs idle, but only
+            // with B transposed (else it transposes through registers): 3001 x 777 x 1001 over 7
+            // experts 88 (T: 26) -> 28 us (27); 390 x 1968 x 2581, T, 40 vs 43
+            if (staged_ok && (!t || tiles >= 192)) p.any = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, 128, 1);
+            else if (t && tiles < 192) p.any = general(tge::GROUP_ROWS, op_b, tge::CFG_64);
+        }
+        break;
+    default: break;
     }
     char what[16];
     snprintf(what, sizeof what, "rows N%c", op_b == GEMM_OP_N ? 'N' : 'T');
@@ -181,6 +220,7 @@ gemm_status_t gemm_grouped_grad_plan_create(gemm_grouped_plan_t *out, const gemm
     switch (algo) {
     case GEMM_ALGO_AUTO: if (tile != 0) return GEMM_STATUS_INVALID_VALUE; break;
     case GEMM_ALGO_FAST: if (tile != 0 && tile != 256 && tile != 128) return GEMM_STATUS_INVALID_VALUE; break;
+    case GEMM_ALGO_FAST_STAGED: if (tile != 0 && tile != 128) return GEMM_STATUS_INVALID_VALUE; break;
     case GEMM_ALGO_GENERAL: if (tile != 0 && tile != 128 && tile != 64) return GEMM_STATUS_INVALID_VALUE; break;
     default: return GEMM_STATUS_INVALID_VALUE;
     }
@@ -200,10 +240,14 @@ gemm_status_t gemm_grouped_grad_plan_create(gemm_grouped_plan_t *out, const gemm
     const int eab = elem_bytes(ab);
     const bool small = algo == GEMM_ALGO_GENERAL && tile ? tile == 64 : d->M < 128 || d->N < 128;
     p.any = any_table(ab, cd)(tge::GROUP_K, 0, small ? tge::CFG_64 : tge::CFG_128);
+    const bool staged_ok = eab == 2 && d->M >= 8 && d->N >= 8 && d->lda * eab * 256 < LIM31 &&
+                           d->ldb * eab * 256 < LIM31;
+    if (staged_ok && (algo == GEMM_ALGO_FAST_STAGED || algo == GEMM_ALGO_AUTO || algo == GEMM_ALGO_FAST))
+        p.any = fast_table(ab, cd)(tge::GROUP_K, 0, 128, 1);
     const bool fast_ok = eab == 2 && d->M % 8 == 0 && d->N % 8 == 0 && d->M > 0 && d->N > 0 && d->lda % 8 == 0 &&
                          d->ldb % 8 == 0 && d->lda * eab * 256 < LIM31 && d->ldb * eab * 256 < LIM31;
-    if (fast_ok && algo == GEMM_ALGO_FAST) p.fast = fast_table(ab, cd)(tge::GROUP_K, 0, tile ? tile : 128);
-    else if (fast_ok && algo == GEMM_ALGO_AUTO) p.fast = fast_table(ab, cd)(tge::GROUP_K, 0, 128);
+    if (fast_ok && algo == GEMM_ALGO_FAST) p.fast = fast_table(ab, cd)(tge::GROUP_K, 0, tile ? tile : 128, 0);
+    else if (fast_ok && algo == GEMM_ALGO_AUTO) p.fast = fast_table(ab, cd)(tge::GROUP_K, 0, 128, 0);
     return finish_plan(out, p, "gradient TN");
 }
 
