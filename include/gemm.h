@@ -399,7 +399,7 @@ typedef struct {
  * Host-only, like gemm_plan_create.  Return INVALID_VALUE for a NULL argument, a negative size,
  * groups < 1, a leading dimension or stride below its minimum, or an enum or tile out of range;
  * NOT_SUPPORTED for a type pair outside the table, a size or leading dimension of 2^31 or more, 2^20
- * groups or more, one expert's B spanning 2^31 bytes or more, or a grid of 2^31
+ * groups or more, one expert's B spanning 2^31 bytes or more, or a grid of 2^23
  * workgroups; ALLOC_FAILED without host memory.
  */
 gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grouped_desc_t *desc);
@@ -470,7 +470,7 @@ typedef struct {
  * < 1, K not a multiple of block, a leading dimension below its minimum, or an enum, flag or tile
  * out of range (GATE included); NOT_SUPPORTED for another type pair or block, or a size beyond
  * the limits (rows, N and leading dimensions below 2^31, K below 2^23, groups below 2^20, a grid
- * below 2^31 workgroups); ALLOC_FAILED without host memory.
+ * below 2^23 workgroups); ALLOC_FAILED without host memory.
  */
 gemm_status_t gemm_quant_plan_create(gemm_quant_plan_t *out, const gemm_quant_desc_t *desc);
 

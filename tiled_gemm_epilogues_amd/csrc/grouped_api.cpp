@@ -48,10 +48,13 @@ FastFn fast_table(int ab, int cd) {
     return nullptr;
 }
 
+// Workgroups of a launch, at most MAX_GRID.
 int64_t grid_of(const gemm_grouped_plan &p, const GroupedEntry &k, bool colsum) {
     const int64_t tn = ceil_div(p.N, k.bn);
-    if (p.mode == tge::GROUP_ROWS) return row_tiles(p.rows, p.groups, k.bm) * tn;
-    return p.groups * (ceil_div(p.M, k.bm) * tn + (colsum ? ceil_div(p.N, 128) : 0));
+    const __int128 g = p.mode == tge::GROUP_ROWS
+                           ? (__int128)row_tiles(p.rows, p.groups, k.bm) * tn
+                           : (__int128)p.groups * (ceil_div(p.M, k.bm) * tn + (colsum ? ceil_div(p.N, 128) : 0));
+    return g < MAX_GRID ? (int64_t)g : MAX_GRID;
 }
 
 // What both descriptions have in common: ranges, types, algorithm.  SUCCESS when they hold.
@@ -100,10 +103,19 @@ gemm_status_t launch(const gemm_grouped_plan &p, const void *A, const void *B, c
 // experts: 64 rows 106 vs 146 us, 512 186 vs 176, 2048 249 vs 181, 4096 365 vs 232.
 bool few_rows_pay(int64_t avg, double tiles) { return avg <= (tiles >= 384 ? 6 : 64); }
 
+// Whether the 256-wide tiles (one workgroup per CU) beat the 128-wide ones (two): with rows enough
+// to fill them and a few rounds of them.  Measured (bf16, B not transposed; 128 -> 256): 8192 x 4096
+// x 4096 over 8 experts 310 -> 275 us, 4096 x 14336 x 4096 over 8 562 -> 490, 16384 x 8192 x 2048
+// over 16 592 -> 475, 32768 x 2048 x 1024 over 64 189 -> 182; but 8192 x 2048 x 4096 over 16 even
+// and 2048 x 8192 x 2048 over 2 75 -> 87.
+bool wide_tiles_pay(int64_t rows, int64_t n, int64_t avg, int64_t N) {
+    return avg >= 512 && ((double)rows / 256 + 0.5 * (double)n) * (double)ceil_div(N, 256) >= 384;
+}
+
 // Hands a finished plan out, with its description.
 gemm_status_t finish_plan(gemm_grouped_plan_t *out, const gemm_grouped_plan &p, const char *what) {
     const GroupedEntry *k = p.fast ? p.fast : p.any;
-    if (grid_of(p, *p.any, true) >= LIM31 || grid_of(p, *k, true) >= LIM31) return GEMM_STATUS_NOT_SUPPORTED;
+    if (grid_of(p, *p.any, true) >= MAX_GRID || grid_of(p, *k, true) >= MAX_GRID) return GEMM_STATUS_NOT_SUPPORTED;
     gemm_grouped_plan *q = new (std::nothrow) gemm_grouped_plan(p);
     if (!q) return GEMM_STATUS_ALLOC_FAILED;
     snprintf(q->desc, sizeof q->desc, "grouped %s %s %s->%s tile %dx%d groups %lld grid %lld", what, k->name,
@@ -152,7 +164,7 @@ gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grou
     // 32-bit offsets inside one expert's weights, 63-bit ones between them
     const int64_t b_rows = op_b == GEMM_OP_N ? d->K : d->N;
     const int64_t big = ((int64_t)1 << 62) / 8 / d->groups;
-    if ((b_rows > 0 && ((b_rows - 1) * d->ldb + min_ldb) * eab >= LIM31) || d->stride_b > big || d->stride_bias > big)
+    if ((b_rows > 0 && (b_rows - 1) * d->ldb + min_ldb >= LIM31 / eab) || d->stride_b > big || d->stride_bias > big)
         return GEMM_STATUS_NOT_SUPPORTED;
 
     gemm_grouped_plan p = {};
@@ -196,7 +208,7 @@ gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grou
         if (rows16_ok && few_rows_pay(avg, tiles)) {
             rows16();
         } else {
-            if (fast_ok) p.fast = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, avg >= 1024 ? 256 : 128, 0);
+            if (fast_ok) p.fast = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, wide_tiles_pay(d->rows, n, avg, d->N) ? 256 : 128, 0);
             // the general kernel's 64-wide tiles keep up while 128-wide ones leave CUs idle, but only
             // with B transposed (else it transposes through registers): 3001 x 777 x 1001 over 7
             // experts 88 (T: 26) -> 28 us (27); 390 x 1968 x 2581, T, 40 vs 43
@@ -226,10 +238,10 @@ gemm_status_t gemm_grouped_grad_plan_create(gemm_grouped_plan_t *out, const gemm
     }
     const gemm_status_t st = check_common(d->rows, d->N, d->M, d->groups, d->lda, d->ldb, d->ldc, ab, cd);
     if (st != GEMM_STATUS_SUCCESS) return st;
-    const int64_t span = d->M > 0 && d->N > 0 ? (d->M - 1) * d->ldc + d->N : 0;
-    if (d->lda < (d->M > 1 ? d->M : 1) || d->ldb < (d->N > 1 ? d->N : 1) || d->ldc < (d->N > 1 ? d->N : 1) ||
-        d->stride_c < 0 || (d->groups > 1 && d->stride_c < span))
+    if (d->lda < (d->M > 1 ? d->M : 1) || d->ldb < (d->N > 1 ? d->N : 1) || d->ldc < (d->N > 1 ? d->N : 1))
         return GEMM_STATUS_INVALID_VALUE;
+    const int64_t span = d->M > 0 && d->N > 0 ? (d->M - 1) * d->ldc + d->N : 0;
+    if (d->stride_c < 0 || (d->groups > 1 && d->stride_c < span)) return GEMM_STATUS_INVALID_VALUE;
     if (d->stride_c > ((int64_t)1 << 62) / 8 / d->groups) return GEMM_STATUS_NOT_SUPPORTED;
 
     gemm_grouped_plan p = {};

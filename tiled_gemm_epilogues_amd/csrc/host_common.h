@@ -10,6 +10,7 @@ namespace host {
 
 constexpr int64_t LIM31 = (int64_t)1 << 31;
 constexpr int64_t MAX_GROUPS = (int64_t)1 << 20;
+constexpr int64_t MAX_GRID = (int64_t)1 << 23;   // workgroups of up to 512 threads, 2^32 threads in all
 constexpr int GROUP_M = 8;                 // tile rows per raster group, as in plain plans
 
 // The integer held by an enum field (C callers may store any int).

@@ -115,7 +115,7 @@ gemm_status_t gemm_quant_plan_create(gemm_quant_plan_t *out, const gemm_quant_de
     if (algo == GEMM_ALGO_SKINNY) p.kernel = tile ? rows_table(ab, cd)(g, tile / 16) : rows_kernel();
     else if (algo == GEMM_ALGO_FAST) p.kernel = tile_table(ab, cd)(g);
     else p.kernel = tiles_pay(p) ? tile_table(ab, cd)(g) : rows_kernel();
-    if (grid_of(p, true) >= LIM31) return GEMM_STATUS_NOT_SUPPORTED;
+    if (grid_of(p, true) >= MAX_GRID) return GEMM_STATUS_NOT_SUPPORTED;
     gemm_quant_plan *q = new (std::nothrow) gemm_quant_plan(p);
     if (!q) return GEMM_STATUS_ALLOC_FAILED;
     snprintf(q->desc, sizeof q->desc, "%s %s->%s block %lld%s tile %dx%d groups %lld grid %lld", p.kernel->name,
