@@ -259,7 +259,14 @@ gemm_status_t gemm_grouped_grad_plan_create(gemm_grouped_plan_t *out, const gemm
     const bool fast_ok = eab == 2 && d->M % 8 == 0 && d->N % 8 == 0 && d->M > 0 && d->N > 0 && d->lda % 8 == 0 &&
                          d->ldb % 8 == 0 && d->lda * eab * 256 < LIM31 && d->ldb * eab * 256 < LIM31;
     if (fast_ok && algo == GEMM_ALGO_FAST) p.fast = fast_table(ab, cd)(tge::GROUP_K, 0, tile ? tile : 128, 0);
-    else if (fast_ok && algo == GEMM_ALGO_AUTO) p.fast = fast_table(ab, cd)(tge::GROUP_K, 0, 128, 0);
+    else if (fast_ok && algo == GEMM_ALGO_AUTO) {
+        // The 256-wide tiles (one workgroup per CU, so that each tile's start and store are not
+        // hidden) pay for long sums only.  Measured (bf16 -> fp32; 128 -> 256): 32768 rows, 4 experts
+        // of 4096 x 4096, 986 -> 821 us; 16384 rows, 8 of 8192 x 4096, even; 16384 rows, 16 of 4096
+        // x 2048, 356 -> 416; 32768 rows, 8 of 1024 x 1024 (128 wide tiles) 114 -> 138.
+        const bool wide = d->rows / d->groups >= 4096 && d->groups * ceil_div(d->M, 256) * ceil_div(d->N, 256) >= 512;
+        p.fast = fast_table(ab, cd)(tge::GROUP_K, 0, wide ? 256 : 128, 0);
+    }
     return finish_plan(out, p, "gradient TN");
 }
 
