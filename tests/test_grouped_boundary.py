@@ -46,7 +46,7 @@ def quant_plan(**kw):
     dict(rows=-1), dict(N=-1), dict(K=-1), dict(groups=0), dict(groups=-3), dict(lda=63), dict(ldb=63),
     dict(op_b="T", ldb=63), dict(ldc=63), dict(stride_b=-1), dict(stride_bias=-1), dict(op_b=2),
     dict(ab_type=9), dict(cd_type=-1), dict(epilogue=5), dict(epilogue=-1), dict(algo=8), dict(algo="split"),
-    dict(algo="nosplit"), dict(algo="kmajor"), dict(tile=128), dict(algo="fast", tile=64),
+    dict(algo="nosplit"), dict(algo="kmajor"), dict(tile=128), dict(algo="fast", tile=32),
     dict(algo="staged", tile=256), dict(algo="general", tile=256), dict(algo="skinny", tile=32),
     dict(algo="skinny", tile=16), dict(K=0, lda=0)])
 def test_rows_invalid(kw):
@@ -175,9 +175,15 @@ def test_kernel_choice():
     assert _kernel(G(2048, 2048, 4096, 64, "T")) == "gemm_fast_128x128"
     assert _kernel(G(32768, 4096, 4096, 8, "T")) == "gemm_fast_256x256"
     assert _kernel(G(30000, 4095, 4096, 8, "N")) == "gemm_fast_128x128_rs"
+    assert _kernel(G(3001, 777, 1001, 7, "N", cd="f32")) == "gemm_fast_64x64_rs"
+    assert _kernel(G(1000, 1000, 1000, 4, "N")) == "gemm_fast_64x64"
     assert _kernel(G(3000, 777, 1001, 7, "T", ab="f32", cd="f32")).startswith("gemm_mfma")
     assert _kernel(W(16384, 4096, 2048, 16)) == "gemm_fast_128x128"
     assert _kernel(W(16384, 4095, 2048, 16)) == "gemm_fast_128x128_rs"
+    assert _kernel(W(3000, 1001, 777, 7)) == "gemm_fast_64x64_rs"
+    assert _kernel(W(40, 1955, 7260, 4)) == "gemm_fast_128x128_rs"
+    assert _kernel(W(1003, 1024, 704, 8)) == "gemm_fast_64x64"
+    assert _kernel(W(32768, 4096, 4096, 4)) == "gemm_fast_256x256"
     assert _kernel(W(16384, 4, 2048, 16)).startswith("gemm_mfma")
     # a pinned kernel whose preconditions do not hold: the general one
     assert _kernel(G(64, 7, 64, 2, "N", algo="skinny")).startswith("gemm_mfma")

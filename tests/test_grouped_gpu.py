@@ -66,9 +66,9 @@ def rows_case(counts, N, K, op_b="N", ab="f16", cd="f16", epilogue="none", alpha
 
 
 RAGGED = [5, 0, 130, 1, 64, 0, 0, 300, 17]
-KERNELS = [("fast", 256), ("fast", 128), ("staged", 128), ("skinny", 0), ("skinny", 64),
+KERNELS = [("fast", 256), ("fast", 128), ("fast", 64), ("staged", 128), ("staged", 64), ("skinny", 0), ("skinny", 64),
            ("general", 128), ("general", 64)]
-NAMES = {"fast": "gemm_fast", "staged": "gemm_fast_128x128_rs", "skinny": "gemm_rows16",
+NAMES = {"fast": "gemm_fast", "staged": "_rs", "skinny": "gemm_rows16",
          "general": "gemm_mfma"}
 
 
@@ -82,15 +82,16 @@ def test_rows_every_kernel(algo, tile, op_b):
 
 @pytest.mark.parametrize("ab,cd", [("f16", "f16"), ("f16", "f32"), ("bf16", "bf16"), ("bf16", "f32"),
                                    ("f32", "f32")])
-@pytest.mark.parametrize("algo,tile", [("fast", 256), ("fast", 128), ("staged", 128), ("skinny", 0), ("skinny", 64),
-                                       ("general", 64)])
+@pytest.mark.parametrize("algo,tile", [("fast", 256), ("fast", 128), ("fast", 64), ("staged", 128), ("staged", 64),
+                                       ("skinny", 0), ("skinny", 64), ("general", 64)])
 def test_rows_types(ab, cd, algo, tile):
     rows_case([40, 3, 0, 257], 136, 192, "T", ab, cd, "gate", start=1, behind=2, algo=algo,
               tile=tile, seed=1)
 
 
 @pytest.mark.parametrize("epilogue", ["none", "relu", "bias", "bias_relu", "gate"])
-@pytest.mark.parametrize("algo,tile", [("fast", 256), ("fast", 128), ("staged", 128), ("skinny", 64), ("general", 128)])
+@pytest.mark.parametrize("algo,tile", [("fast", 256), ("fast", 128), ("fast", 64), ("staged", 128), ("staged", 64),
+                                       ("skinny", 64), ("general", 128)])
 def test_rows_epilogues(epilogue, algo, tile):
     beta = 0.0 if epilogue == "gate" else 2.0
     rows_case([33, 200, 0, 90], 264, 128, "N", "bf16", "f32", epilogue, alpha=-1.0, beta=beta,
@@ -103,7 +104,7 @@ def test_rows_epilogues(epilogue, algo, tile):
     ([1], 0, 0), ([0], 0, 1), ([0, 0, 0], 2, 0), ([0, 1], 0, 0), ([1] * 130, 0, 0),
     ([0] * 64 + [1], 0, 5), ([3, 0] * 100, 1, 1), ([700], 0, 0), ([0] * 299 + [129], 7, 0),
     ([2] * 64, 0, 0), ([128, 256, 64], 0, 0)])
-@pytest.mark.parametrize("algo,tile", [("auto", 0), ("fast", 128), ("staged", 128), ("skinny", 0), ("skinny", 64),
+@pytest.mark.parametrize("algo,tile", [("auto", 0), ("fast", 128), ("fast", 64), ("staged", 128), ("staged", 64), ("skinny", 0), ("skinny", 64),
                                        ("general", 64)])
 def test_rows_ranges(counts, start, behind, algo, tile):
     rows_case(counts, 72, 64, "T", start=start, behind=behind, algo=algo, tile=tile, seed=4)
@@ -117,7 +118,7 @@ def test_rows_odd_sizes(N, K, op_b):
         rows_case([5, 0, 40, 1, 150], N, K, op_b, ab, cd, "bias", start=1, behind=1, seed=5)
 
 
-@pytest.mark.parametrize("algo,tile", [("staged", 128), ("skinny", 0), ("skinny", 64), ("general", 64)])
+@pytest.mark.parametrize("algo,tile", [("staged", 128), ("staged", 64), ("skinny", 0), ("skinny", 64), ("general", 64)])
 @pytest.mark.parametrize("op_b", ["N", "T"])
 @pytest.mark.parametrize("N,K", [(8, 8), (9, 15), (63, 63), (65, 64), (71, 65), (127, 129), (129, 200),
                                  (64, 128), (72, 513), (1001, 1001)])
@@ -147,7 +148,7 @@ def test_rows_unaligned_pointers():
     assert D[0].item() == SENTINEL
 
 
-@pytest.mark.parametrize("algo,tile", [("fast", 128), ("staged", 128), ("skinny", 0), ("general", 64)])
+@pytest.mark.parametrize("algo,tile", [("fast", 128), ("fast", 64), ("staged", 64), ("skinny", 0), ("general", 64)])
 def test_rows_unordered_offsets_stay_inside(algo, tile):
     # undefined results, but nothing outside D's rows is written
     T, N, K = 100, 64, 64
@@ -170,7 +171,8 @@ def test_rows_beyond_32_bit_offsets():
     A[T - tail:] = ints(g, (tail, K), -1, 1, torch.float16).to(DEV)
     B = ints(g, (3, N, K), -1, 1, torch.float16)
     offs = offsets_of([100, 300, 290], T - tail)
-    for algo, tile in (("fast", 256), ("fast", 128), ("staged", 128), ("skinny", 64), ("skinny", 16), ("general", 128)):
+    for algo, tile in (("fast", 256), ("fast", 128), ("fast", 64), ("staged", 128), ("staged", 64), ("skinny", 64), ("skinny", 16),
+                       ("general", 128)):
         D[T - tail:] = SENTINEL
         tge.GroupedPlan(T, N, K, 3, "T", cd="f32", algo=algo, tile=tile).run(
             A, B.to(DEV), None, D, torch.from_numpy(offs).to(DEV))
@@ -214,7 +216,7 @@ def grad_case(counts, M, N, ab="f16", cd="f32", alpha=1.0, beta=0.0, start=0, be
     same(sums.cpu(), want_sums.float() if bias else torch.full((E, N), SENTINEL), "bias_grad")
 
 
-GRAD_KERNELS = [("fast", 256), ("fast", 128), ("staged", 128), ("general", 128), ("general", 64)]
+GRAD_KERNELS = [("fast", 256), ("fast", 128), ("fast", 64), ("staged", 128), ("staged", 64), ("general", 128), ("general", 64)]
 
 
 @pytest.mark.parametrize("ab,cd", [("f16", "f16"), ("f16", "f32"), ("bf16", "bf16"), ("bf16", "f32"),
@@ -236,7 +238,8 @@ def test_grad_scalars_and_in_place(algo, tile):
 @pytest.mark.parametrize("counts,start,behind", [
     ([1], 0, 0), ([0], 0, 3), ([0, 0], 0, 0), ([64], 0, 0), ([63, 64, 65, 128, 127, 129], 0, 1),
     ([1] * 70, 3, 0), ([2000, 0, 1], 0, 0)])
-@pytest.mark.parametrize("algo,tile", [("fast", 256), ("fast", 128), ("staged", 128), ("general", 64)])
+@pytest.mark.parametrize("algo,tile", [("fast", 256), ("fast", 128), ("fast", 64), ("staged", 128), ("staged", 64),
+                                       ("general", 64)])
 def test_grad_ranges(counts, start, behind, algo, tile):
     grad_case(counts, 64, 72, start=start, behind=behind, algo=algo, tile=tile, seed=14)
 
@@ -263,7 +266,7 @@ def test_grad_beyond_32_bit_offsets():
     B[T - tail:] = ints(g, (tail, N), -2, 2, torch.float16).to(DEV)
     offs = offsets_of([100, 0, 190], T - tail)
     want, sums = grad_reference(A[T - tail:].cpu(), B[T - tail:].cpu(), None, offs - (T - tail), 1.0, 0.0)
-    for algo, tile in (("fast", 128), ("fast", 256), ("staged", 128), ("general", 128)):
+    for algo, tile in (("fast", 128), ("fast", 256), ("fast", 64), ("staged", 128), ("staged", 64), ("general", 128)):
         D = torch.full((3, M, N), SENTINEL, device=DEV)
         s = torch.full((3, N), SENTINEL, device=DEV)
         tge.GroupedGradPlan(T, M, N, 3, algo=algo, tile=tile).run(

@@ -108,6 +108,11 @@ __device__ __forceinline__ int swz_mc(int k) {
         // second transposing read, the k-slice offset).
         static_assert(MF == 16, "16x16 shape");
         return ((k >> 1) & 3) ^ (((k >> 5) & 1) << 2);
+    } else if constexpr (E == 2 && TL == 64) {
+        // 16-bit rows of 128 B (8 chunks; rows k and k+2 in the same half of the banks): the 16 lanes
+        // of a k group read 4 rows at 2 adjacent chunks, the group served with it 16 rows on
+        static_assert(MF == 16, "16x16 shape");
+        return (((k >> 1) & 1) << 1) | (((k >> 4) & 1) << 2);
     } else if constexpr (E == 2) {
         const int q = k & 3;
         return (4 * q + 2 * (q >> 1)) ^ (MF == 16 ? ((k >> 4) & 1) << 1 : 0);
@@ -529,12 +534,14 @@ __device__ __forceinline__ void epilogue(const ParamsOf<GRP> &p, int mbase, int 
 template <int MF, int TL = 256>
 struct Sched {
     static constexpr int NLD = 2 * Geo<TL>::NL;          // loads per slab and wave
-    static constexpr int BAR_AT = MF == 32 ? 4 : 8;
-    static constexpr int DS = MF == 32 || TL == 128 ? 2 : 4;
+    static constexpr int BAR_AT = MF == 32 ? 4 : TL == 64 ? 2 : 8;
+    static constexpr int DS = TL == 64 ? 1 : MF == 32 || TL == 128 ? 2 : 4;
+    static constexpr int RD = TL == 64 ? 1 : 2;          // register-staged: MFMA slots per chunk
     static constexpr int REM = Shape<MF, TL>::NMS - BAR_AT;   // MFMA slots after the barrier
     static constexpr int N3 = (REM + DS - 1) / DS;       // loads of slab s+2 in them
     static_assert(N3 <= NLD, "loads after the barrier");
     // every load of a slab finds a slot: N3 after the barrier, the rest in the first k-slices
+    static_assert(((Shape<MF, TL>::NS - 1) * Shape<MF, TL>::NMS + RD - 1) / RD >= NLD, "staging slots");
     static_assert(N3 + ((Shape<MF, TL>::NS - 1) * Shape<MF, TL>::NMS + DS - 1) / DS >= NLD, "load slots");
 };
 
@@ -546,8 +553,8 @@ struct Sched {
 // loads, no load transforms).  GRP: GroupMode of the launch (products grouped by expert).
 template <class TI, class TO, bool AK, bool BK, int MF, bool XF, bool RS = false, int TL = 256,
           int GRP = GROUP_NONE>
-__global__ __launch_bounds__(NT, TL == 256 ? 1 : 2) void gemm_fast(ParamsOf<GRP> p) {
-    static_assert(TL == 256 || (TL == 128 && MF == 16 && !XF), "tile variants");
+__global__ __launch_bounds__(NT, TL == 256 ? 1 : TL == 128 ? 2 : 4) void gemm_fast(ParamsOf<GRP> p) {
+    static_assert(TL == 256 || ((TL == 128 || TL == 64) && MF == 16 && !XF), "tile variants");
     using acc_t = typename TI::acc_t;
     using accv_t = typename std::conditional<MF == 32, typename TI::accv_t, typename TI::accv16_t>::type;
     using SH = Shape<MF, TL>;
@@ -697,9 +704,9 @@ __global__ __launch_bounds__(NT, TL == 256 ? 1 : 2) void gemm_fast(ParamsOf<GRP>
                 rd_slot(X, j + 1, (j + 1) & 1, t, NMS);
                 const int q = NMS * j + t;                       // load slot in the slab
                 if constexpr (RS) {
-                    if (q % 2 == 0 && q / 2 < SC::NLD) {
-                        if (has_next) rs_put(Y, q / 2);
-                        if (dma_next2) rs_fetch(s + 2, q / 2);
+                    if (q % SC::RD == 0 && q / SC::RD < SC::NLD) {
+                        if (has_next) rs_put(Y, q / SC::RD);
+                        if (dma_next2) rs_fetch(s + 2, q / SC::RD);
                     }
                 } else if (dma_next) {
                     if (q % SC::DS == 0 && SC::N3 + q / SC::DS < SC::NLD) dma(na, nb, Y, SC::N3 + q / SC::DS);
@@ -757,7 +764,8 @@ __global__ __launch_bounds__(NT, TL == 256 ? 1 : 2) void gemm_fast(ParamsOf<GRP>
             // slab 0 landed, slab 1 (its 2 NL loads) may still fly
             if (nfull > 1) {
                 if constexpr (NL == 8) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
-                else asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+                else if constexpr (NL == 4) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+                else asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
             } else {
                 wait_vmcnt0();
             }
@@ -893,23 +901,28 @@ hipError_t launch_grouped(const GroupedParams &p, unsigned grid, hipStream_t s) 
 
 template <class TI, class TO>
 const GroupedEntry *lookup_grouped(int mode, int op_b, int tile, int rs) {
-    if ((tile != 256 && tile != 128) || (rs && tile != 128)) return nullptr;
-    const int i = tile == 256 ? 0 : 1;
-    static const GroupedEntry rows[4] = {
-        {launch_grouped<TI, TO, 256, false, false, GROUP_ROWS>, 256, 256, "gemm_fast_256x256"},
-        {launch_grouped<TI, TO, 128, false, false, GROUP_ROWS>, 128, 128, "gemm_fast_128x128"},
-        {launch_grouped<TI, TO, 256, false, true, GROUP_ROWS>, 256, 256, "gemm_fast_256x256"},
-        {launch_grouped<TI, TO, 128, false, true, GROUP_ROWS>, 128, 128, "gemm_fast_128x128"}};
-    static const GroupedEntry staged[3] = {
-        {launch_grouped<TI, TO, 128, false, false, GROUP_ROWS, true>, 128, 128, "gemm_fast_128x128_rs"},
-        {launch_grouped<TI, TO, 128, false, true, GROUP_ROWS, true>, 128, 128, "gemm_fast_128x128_rs"},
-        {launch_grouped<TI, TO, 128, true, false, GROUP_K, true>, 128, 128, "gemm_fast_128x128_rs"}};
-    static const GroupedEntry k[2] = {
-        {launch_grouped<TI, TO, 256, true, false, GROUP_K>, 256, 256, "gemm_fast_256x256"},
-        {launch_grouped<TI, TO, 128, true, false, GROUP_K>, 128, 128, "gemm_fast_128x128"}};
-    if (mode == GROUP_ROWS && (op_b == 0 || op_b == 1)) return rs ? &staged[op_b] : &rows[2 * op_b + i];
-    if (mode == GROUP_K && op_b == 0) return rs ? &staged[2] : &k[i];
-    return nullptr;
+    // [layout: rows N, rows T, gradient][tile 256, 128, 64]; register-staged [layout][128, 64]
+    static const GroupedEntry direct[3][3] = {
+        {{launch_grouped<TI, TO, 256, false, false, GROUP_ROWS>, 256, 256, "gemm_fast_256x256"},
+         {launch_grouped<TI, TO, 128, false, false, GROUP_ROWS>, 128, 128, "gemm_fast_128x128"},
+         {launch_grouped<TI, TO, 64, false, false, GROUP_ROWS>, 64, 64, "gemm_fast_64x64"}},
+        {{launch_grouped<TI, TO, 256, false, true, GROUP_ROWS>, 256, 256, "gemm_fast_256x256"},
+         {launch_grouped<TI, TO, 128, false, true, GROUP_ROWS>, 128, 128, "gemm_fast_128x128"},
+         {launch_grouped<TI, TO, 64, false, true, GROUP_ROWS>, 64, 64, "gemm_fast_64x64"}},
+        {{launch_grouped<TI, TO, 256, true, false, GROUP_K>, 256, 256, "gemm_fast_256x256"},
+         {launch_grouped<TI, TO, 128, true, false, GROUP_K>, 128, 128, "gemm_fast_128x128"},
+         {launch_grouped<TI, TO, 64, true, false, GROUP_K>, 64, 64, "gemm_fast_64x64"}}};
+    static const GroupedEntry staged[3][2] = {
+        {{launch_grouped<TI, TO, 128, false, false, GROUP_ROWS, true>, 128, 128, "gemm_fast_128x128_rs"},
+         {launch_grouped<TI, TO, 64, false, false, GROUP_ROWS, true>, 64, 64, "gemm_fast_64x64_rs"}},
+        {{launch_grouped<TI, TO, 128, false, true, GROUP_ROWS, true>, 128, 128, "gemm_fast_128x128_rs"},
+         {launch_grouped<TI, TO, 64, false, true, GROUP_ROWS, true>, 64, 64, "gemm_fast_64x64_rs"}},
+        {{launch_grouped<TI, TO, 128, true, false, GROUP_K, true>, 128, 128, "gemm_fast_128x128_rs"},
+         {launch_grouped<TI, TO, 64, true, false, GROUP_K, true>, 64, 64, "gemm_fast_64x64_rs"}}};
+    if ((mode != GROUP_ROWS && mode != GROUP_K) || op_b < 0 || op_b > (mode == GROUP_ROWS ? 1 : 0)) return nullptr;
+    const int layout = mode == GROUP_K ? 2 : op_b;
+    if (rs) return tile == 128 ? &staged[layout][0] : tile == 64 ? &staged[layout][1] : nullptr;
+    return tile == 256 ? &direct[layout][0] : tile == 128 ? &direct[layout][1] : tile == 64 ? &direct[layout][2] : nullptr;
 }
 
 }  // namespace

@@ -195,9 +195,9 @@ hipError_t finish_i8_i32(const GemmParams &p, hipStream_t s);
 // Grouped products (the same kernels with the group selection compiled in).  mode: GroupMode;
 // op_b: 0 = N, 1 = T (GROUP_K: 0).  Preconditions as for the kernels above, for every range:
 //   any    the general kernel, tile CFG_128 or CFG_64: none
-//   fast   tile 256 or 128, direct loads: 16-byte aligned pointers, leading dimensions and strides;
+//   fast   tile 256, 128 or 64, direct loads: 16-byte aligned pointers, leading dimensions and strides;
 //          GROUP_ROWS: K >= 64, N % 8 == 0 when op_b is N; GROUP_K: M % 8 == 0 and N % 8 == 0.
-//          rs = 1 (tile 128): register-staged loads; at least 8 elements (one chunk) along M and N,
+//          rs = 1 (tile 128 or 64): register-staged loads; at least 8 elements (one chunk) along M and N,
 //          nothing else
 //   rows16 GROUP_ROWS, 16 rows and 16 * cg columns per workgroup (cg 4; 1 too when op_b is T):
 //          K >= 8, N >= 8 when op_b is N

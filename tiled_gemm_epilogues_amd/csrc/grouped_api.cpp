@@ -96,12 +96,13 @@ gemm_status_t launch(const gemm_grouped_plan &p, const void *A, const void *B, c
                                                                                 : GEMM_STATUS_HIP_ERROR;
 }
 
-// Whether the kernel for few rows (16 rows per workgroup) beats the 128-wide tiles, which waste most
-// of a tile but move the weights at full rate once there are enough of them: up to 64 rows per
-// expert where the tiles do not fill the chip, and only up to 6 where they do.  Measured (bf16, N
-// 2048, K 4096; few rows -> tiles): 8 experts: 128 rows 28 vs 54 us, 256 31 vs 56, 512 47 vs 55; 64
-// experts: 64 rows 106 vs 146 us, 512 186 vs 176, 2048 249 vs 181, 4096 365 vs 232.
-bool few_rows_pay(int64_t avg, double tiles) { return avg <= (tiles >= 384 ? 6 : 64); }
+// Whether the kernel for few rows (16 rows per workgroup, K split over its waves) beats the tiles,
+// which waste most of a tile but move more weights per workgroup: for a few rows per expert, and as
+// long as its 16 x 64 workgroups (`few`) are about one round.  Measured (bf16, B not transposed, N 2048,
+// K 4096; few rows -> best tile): 1 row per expert, 64 experts, 107 vs 146 us; 1 expert, 128 rows (272
+// workgroups) 13 vs 30; 8 experts, 256 rows (640) 35 vs 44, 512 (1152) 49 vs 46, 1024 (2176) 81 vs 50;
+// 64 experts, 512 rows (2048) 196 vs 193, 2048 (5120) 254 vs 200.
+bool few_rows_pay(int64_t avg, double few) { return avg <= 6 || few <= 700; }
 
 // Whether the 256-wide tiles (one workgroup per CU) beat the 128-wide ones (two): with rows enough
 // to fill them and a few rounds of them.  Measured (bf16, B not transposed; 128 -> 256): 8192 x 4096
@@ -146,8 +147,8 @@ gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grou
         return GEMM_STATUS_INVALID_VALUE;
     switch (algo) {
     case GEMM_ALGO_AUTO: if (tile != 0) return GEMM_STATUS_INVALID_VALUE; break;
-    case GEMM_ALGO_FAST: if (tile != 0 && tile != 256 && tile != 128) return GEMM_STATUS_INVALID_VALUE; break;
-    case GEMM_ALGO_FAST_STAGED: if (tile != 0 && tile != 128) return GEMM_STATUS_INVALID_VALUE; break;
+    case GEMM_ALGO_FAST: if (tile != 0 && tile != 256 && tile != 128 && tile != 64) return GEMM_STATUS_INVALID_VALUE; break;
+    case GEMM_ALGO_FAST_STAGED: if (tile != 0 && tile != 128 && tile != 64) return GEMM_STATUS_INVALID_VALUE; break;
     case GEMM_ALGO_GENERAL: if (tile != 0 && tile != 128 && tile != 64) return GEMM_STATUS_INVALID_VALUE; break;
     case GEMM_ALGO_SKINNY:
         if (tile != 0 && tile != 64 && !(tile == 16 && op_b == GEMM_OP_T)) return GEMM_STATUS_INVALID_VALUE;
@@ -178,6 +179,7 @@ gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grou
     const int64_t avg = ceil_div(d->rows, d->groups);                      // rows of an expert, on average
     const int64_t n = d->rows < d->groups ? d->rows : d->groups;           // experts with rows, at most
     const double tiles = ((double)d->rows / 128 + 0.5 * (double)n) * (double)ceil_div(d->N, 128);
+    const double few = ((double)d->rows / 16 + 0.5 * (double)n) * (double)ceil_div(d->N, 64);
     const bool small = algo == GEMM_ALGO_GENERAL && tile ? tile == 64 : avg < 128 || d->N < 128;
     p.any = general(tge::GROUP_ROWS, op_b, small ? tge::CFG_64 : tge::CFG_128);
     const bool offsets_ok = d->lda * eab * 256 < LIM31;                    // 32-bit offsets within a tile's rows
@@ -202,18 +204,24 @@ gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grou
         if (fast_ok) p.fast = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, tile ? tile : 128, 0);
         break;
     case GEMM_ALGO_FAST_STAGED:
-        if (staged_ok) p.any = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, 128, 1);
+        if (staged_ok) p.any = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, tile ? tile : 128, 1);
         break;
     case GEMM_ALGO_AUTO:
-        if (rows16_ok && few_rows_pay(avg, tiles)) {
+        if (rows16_ok && few_rows_pay(avg, few)) {
             rows16();
         } else {
-            if (fast_ok) p.fast = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, wide_tiles_pay(d->rows, n, avg, d->N) ? 256 : 128, 0);
-            // the general kernel's 64-wide tiles keep up while 128-wide ones leave CUs idle, but only
-            // with B transposed (else it transposes through registers): 3001 x 777 x 1001 over 7
-            // experts 88 (T: 26) -> 28 us (27); 390 x 1968 x 2581, T, 40 vs 43
-            if (staged_ok && (!t || tiles >= 192)) p.any = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, 128, 1);
-            else if (t && tiles < 192) p.any = general(tge::GROUP_ROWS, op_b, tge::CFG_64);
+            // 64-wide tiles where 128-wide ones are too few to fill the chip: 390 x 1968 x 2584 (56
+            // of them) 33 -> 22 us, 1000 x 1000 x 1000 over 4 experts (78) 17 -> 12, 3000 x 776 x
+            // 1000 over 7 (189) 18.2 -> 17.1; but 1000 x 4096 x 512 over 2 (281) 11.5 -> 13.4 and
+            // 2100 x 1408 x 2048 over 32 (356) 46 -> 62
+            if (fast_ok) {
+                const int tl = wide_tiles_pay(d->rows, n, avg, d->N) ? 256 : tiles < 200 ? 64 : 128;
+                p.fast = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, tl, 0);
+            }
+            // register-staged: 390 x 1968 x 2581 41 -> 23 us, 3001 x 777 x 1001 over 7 experts 28 -> 24, 700
+            // x 4097 x 127 over 3 (231) 12 -> 10; but 20000 x 2049 x 4097 over 8 596 -> 984 (the
+            // general kernel 1530, 87 for the second)
+            if (staged_ok) p.any = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, tiles < 400 ? 64 : 128, 1);
         }
         break;
     default: break;
@@ -231,8 +239,8 @@ gemm_status_t gemm_grouped_grad_plan_create(gemm_grouped_plan_t *out, const gemm
     if (!in(ab, GEMM_F32, GEMM_DF32) || !in(cd, GEMM_F32, GEMM_DF32)) return GEMM_STATUS_INVALID_VALUE;
     switch (algo) {
     case GEMM_ALGO_AUTO: if (tile != 0) return GEMM_STATUS_INVALID_VALUE; break;
-    case GEMM_ALGO_FAST: if (tile != 0 && tile != 256 && tile != 128) return GEMM_STATUS_INVALID_VALUE; break;
-    case GEMM_ALGO_FAST_STAGED: if (tile != 0 && tile != 128) return GEMM_STATUS_INVALID_VALUE; break;
+    case GEMM_ALGO_FAST: if (tile != 0 && tile != 256 && tile != 128 && tile != 64) return GEMM_STATUS_INVALID_VALUE; break;
+    case GEMM_ALGO_FAST_STAGED: if (tile != 0 && tile != 128 && tile != 64) return GEMM_STATUS_INVALID_VALUE; break;
     case GEMM_ALGO_GENERAL: if (tile != 0 && tile != 128 && tile != 64) return GEMM_STATUS_INVALID_VALUE; break;
     default: return GEMM_STATUS_INVALID_VALUE;
     }
@@ -254,8 +262,14 @@ gemm_status_t gemm_grouped_grad_plan_create(gemm_grouped_plan_t *out, const gemm
     p.any = any_table(ab, cd)(tge::GROUP_K, 0, small ? tge::CFG_64 : tge::CFG_128);
     const bool staged_ok = eab == 2 && d->M >= 8 && d->N >= 8 && d->lda * eab * 256 < LIM31 &&
                            d->ldb * eab * 256 < LIM31;
-    if (staged_ok && (algo == GEMM_ALGO_FAST_STAGED || algo == GEMM_ALGO_AUTO || algo == GEMM_ALGO_FAST))
-        p.any = fast_table(ab, cd)(tge::GROUP_K, 0, 128, 1);
+    const int64_t avg = d->rows / d->groups;
+    const int64_t tiles = d->groups * ceil_div(d->M, 128) * ceil_div(d->N, 128);
+    // Register-staged: 64-wide tiles while the 128-wide ones do not fill the chip (3000 rows, 7 experts of
+    // 1001 x 777, 26 -> 23 us, 300 rows, 16 of 333 x 1001, 11.1 -> 10.7; 16000 rows, 8 of 2049 x 2049,
+    // 253 -> 381, 40 rows, 4 of 1955 x 7260, 84 -> 107; the general kernel 101 and 995 for the first
+    // and third).
+    if (staged_ok && algo != GEMM_ALGO_GENERAL)
+        p.any = fast_table(ab, cd)(tge::GROUP_K, 0, algo == GEMM_ALGO_FAST_STAGED && tile ? tile : tiles < 400 ? 64 : 128, 1);
     const bool fast_ok = eab == 2 && d->M % 8 == 0 && d->N % 8 == 0 && d->M > 0 && d->N > 0 && d->lda % 8 == 0 &&
                          d->ldb % 8 == 0 && d->lda * eab * 256 < LIM31 && d->ldb * eab * 256 < LIM31;
     if (fast_ok && algo == GEMM_ALGO_FAST) p.fast = fast_table(ab, cd)(tge::GROUP_K, 0, tile ? tile : 128, 0);
@@ -264,8 +278,11 @@ gemm_status_t gemm_grouped_grad_plan_create(gemm_grouped_plan_t *out, const gemm
         // hidden) pay for long sums only.  Measured (bf16 -> fp32; 128 -> 256): 32768 rows, 4 experts
         // of 4096 x 4096, 986 -> 821 us; 16384 rows, 8 of 8192 x 4096, even; 16384 rows, 16 of 4096
         // x 2048, 356 -> 416; 32768 rows, 8 of 1024 x 1024 (128 wide tiles) 114 -> 138.
-        const bool wide = d->rows / d->groups >= 4096 && d->groups * ceil_div(d->M, 256) * ceil_div(d->N, 256) >= 512;
-        p.fast = fast_table(ab, cd)(tge::GROUP_K, 0, wide ? 256 : 128, 0);
+        const bool wide = avg >= 4096 && d->groups * ceil_div(d->M, 256) * ceil_div(d->N, 256) >= 512;
+        // 64-wide tiles where the 128-wide ones do not fill the chip or the sums are short: 1003
+        // rows, 8 experts of 1024 x 704 (384 128-wide tiles), 12.1 -> 9.6 us, 2000 rows, 2 of 72 x
+        // 3504, 17 -> 12, 40 rows, 4 of 1952 x 7264, 46 -> 42; 16000 rows, 8 of 2048 x 2048, 144 -> 192.
+        p.fast = fast_table(ab, cd)(tge::GROUP_K, 0, wide ? 256 : tiles < 400 || avg < 64 ? 64 : 128, 0);
     }
     return finish_plan(out, p, "gradient TN");
 }
