@@ -45,8 +45,9 @@ const GroupedEntry *any(int mode, int op_b, int cfg) {
     return cfg == CFG_128 ? entry<128, 128>("any128") : cfg == CFG_64 ? entry<64, 64>("any64") : nullptr;
 }
 const GroupedEntry *fast(int mode, int op_b, int tile, int rs) {
-    if ((mode != GROUP_ROWS && mode != GROUP_K) || (mode == GROUP_K && op_b) || (rs && tile != 128)) return nullptr;
-    return tile == 256 ? entry<256, 256>("fast256") : tile == 128 ? entry<128, 128>(rs ? "rs" : "fast128") : nullptr;
+    if ((mode != GROUP_ROWS && mode != GROUP_K) || (mode == GROUP_K && op_b) || (rs && tile == 256)) return nullptr;
+    return tile == 256 ? entry<256, 256>("fast256") : tile == 128 ? entry<128, 128>(rs ? "rs" : "fast128")
+           : tile == 64 ? entry<64, 64>(rs ? "rs64" : "fast64") : nullptr;
 }
 const GroupedEntry *rows16(int op_b, int cg) {
     return cg == 4 ? entry<16, 64>("rows16") : cg == 1 && op_b == 1 ? entry<16, 16>("rows16") : nullptr;
