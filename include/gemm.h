@@ -369,7 +369,7 @@ typedef struct gemm_grouped_plan *gemm_grouped_plan_t;
  * N x K (op_b T; ldb >= K) at B + e * stride_b, bias_e at bias + e * stride_bias (a zero stride
  * shares it).  algo: AUTO, or FAST (with tile 256, 128 or 64; 0: 128), FAST_STAGED (its tiles
  * of 128 or 64 on operands of any alignment), GENERAL (tile 128 or 64) or SKINNY (for few rows per
- * expert: 16 rows and, by tile, 64 or with B transposed 16 columns per workgroup) to pin a kernel,
+ * expert: 16 rows and, by tile, 64 or 32 columns per workgroup, with B transposed 64 or 16) to pin a kernel,
  * which falls back to the general one where its preconditions do not hold.
  */
 typedef struct {

@@ -50,7 +50,8 @@ const GroupedEntry *fast(int mode, int op_b, int tile, int rs) {
            : tile == 64 ? entry<64, 64>(rs ? "rs64" : "fast64") : nullptr;
 }
 const GroupedEntry *rows16(int op_b, int cg) {
-    return cg == 4 ? entry<16, 64>("rows16") : cg == 1 && op_b == 1 ? entry<16, 16>("rows16") : nullptr;
+    return cg == 4 ? entry<16, 64>("rows16") : cg == 1 && op_b == 1 ? entry<16, 16>("rows16")
+           : cg == 2 && op_b == 0 ? entry<16, 32>("rows16") : nullptr;
 }
 const QuantEntry *qrows(int block, int cg) {
     static const QuantEntry e[2] = {{launch_quant, 16, 16, "qrows"}, {launch_quant, 16, 64, "qrows"}};

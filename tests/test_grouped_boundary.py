@@ -47,8 +47,8 @@ def quant_plan(**kw):
     dict(op_b="T", ldb=63), dict(ldc=63), dict(stride_b=-1), dict(stride_bias=-1), dict(op_b=2),
     dict(ab_type=9), dict(cd_type=-1), dict(epilogue=5), dict(epilogue=-1), dict(algo=8), dict(algo="split"),
     dict(algo="nosplit"), dict(algo="kmajor"), dict(tile=128), dict(algo="fast", tile=32),
-    dict(algo="staged", tile=256), dict(algo="general", tile=256), dict(algo="skinny", tile=32),
-    dict(algo="skinny", tile=16), dict(K=0, lda=0)])
+    dict(algo="staged", tile=256), dict(algo="general", tile=256), dict(algo="skinny", tile=48),
+    dict(algo="skinny", tile=16), dict(op_b="T", algo="skinny", tile=32), dict(K=0, lda=0)])
 def test_rows_invalid(kw):
     assert rows_plan(**kw)[0] == INVALID
 
@@ -172,6 +172,7 @@ def test_kernel_choice():
     assert _kernel(G(8, 1024, 2048, 16, "T")) == "gemm_rows16_16x16"
     assert _kernel(G(64, 2048, 4096, 64, "T")) == "gemm_rows16_16x64"
     assert _kernel(G(64, 2048, 4096, 64, "N")) == "gemm_rows16_16x64"
+    assert _kernel(G(1, 2048, 4096, 1, "N")) == "gemm_rows16_16x32"
     assert _kernel(G(2048, 2048, 4096, 64, "T")) == "gemm_fast_128x128"
     assert _kernel(G(32768, 4096, 4096, 8, "T")) == "gemm_fast_256x256"
     assert _kernel(G(30000, 4095, 4096, 8, "N")) == "gemm_fast_128x128_rs"

@@ -199,8 +199,8 @@ hipError_t finish_i8_i32(const GemmParams &p, hipStream_t s);
 //          GROUP_ROWS: K >= 64, N % 8 == 0 when op_b is N; GROUP_K: M % 8 == 0 and N % 8 == 0.
 //          rs = 1 (tile 128 or 64): register-staged loads; at least 8 elements (one chunk) along M and N,
 //          nothing else
-//   rows16 GROUP_ROWS, 16 rows and 16 * cg columns per workgroup (cg 4; 1 too when op_b is T):
-//          K >= 8, N >= 8 when op_b is N
+//   rows16 GROUP_ROWS, 16 rows and 16 * cg columns per workgroup (cg 4, or 1 when op_b is T, 2
+//          when it is N): K >= 8, N >= 8 when op_b is N
 const GroupedEntry *grouped_any_f32_f32(int mode, int op_b, int cfg);
 const GroupedEntry *grouped_any_f16_f16(int mode, int op_b, int cfg);
 const GroupedEntry *grouped_any_f16_f32(int mode, int op_b, int cfg);

@@ -9,8 +9,9 @@
 //
 //  * an operand whose rows lie along K (A, a transposed B) is loaded 4 lanes per row (whole
 //    64-byte pieces) and read as fragments, row lane % 16, 8 k of piece lane / 16;
-//  * a B stored K x N is loaded 8 lanes per row of 64 columns and read with the transposing read
-//    ds_read_b64_tr_b16 (the lane maps and swizzles of gemm_skinny.hip).
+//  * a B stored K x N is loaded 8 lanes per row of 64 columns (4 per row of 32: a workgroup streams
+//    some 60 GB/s, so few columns take narrower workgroups) and read with the transposing read
+//    ds_read_b64_tr_b16 (the lane map of gemm_skinny.hip).
 //
 // The direct-to-LDS loads of gemm_skinny.hip need 16-byte alignment and a whole number of 64-byte
 // pieces in K; ordinary loads do not.  Loads that would cross the end of K are moved back and their
@@ -48,9 +49,10 @@ __device__ __forceinline__ void wave_order() {
 template <class TI, class TO, bool BT, int CG, int KC>
 __global__ __launch_bounds__(WAVES * 64, 2) void gemm_rows16(GroupedParams p) {
     using T = typename TO::T;
-    static_assert(BT || (CG == 4 && KC == 64), "rows of 64 columns, 8 rows per load");
+    static_assert(BT || ((CG == 4 || CG == 2) && KC == 64), "rows of 64 or 32 columns");
     constexpr int NI = KC / 32;                              // 16x16x32 instructions per chunk and group
-    constexpr int NL = BT ? CG * NI : KC / 8;                // 1 KiB loads of B per chunk
+    constexpr int LPR = 2 * CG, RPL = 64 / LPR;              // K x N: lanes per row, rows per load
+    constexpr int NL = BT ? CG * NI : KC / RPL;              // 1 KiB loads of B per chunk
     constexpr int COLS = 16 * CG;
     constexpr int OFF_A = NL * 1024, SLOT = OFF_A + NI * 1024;
     static_assert(SLOT >= CG * 1024, "the slots hold the waves' sums at the end");
@@ -68,15 +70,15 @@ __global__ __launch_bounds__(WAVES * 64, 2) void gemm_rows16(GroupedParams p) {
     const int put = piece16(lr, lq), get = piece16(lane & 15, g);
 
     const uint8_t *arow = static_cast<const uint8_t *>(p.A) + (int64_t)min(lr, p.M - 1) * p.lda * 2 + 16 * lq;
-    // BT: row n0 + 16 j + lr of B.  Else: row lane / 8 of the chunk, 8 columns from n0 + 8 * (lane % 8)
+    // BT: row n0 + 16 j + lr of B.  Else: row lane / LPR of the load, 8 columns from n0 + 8 * (lane % LPR)
     const uint8_t *brow[BT ? CG : 1];
-    const int bc = n0 + 8 * (lane & 7), bcol = min(bc, p.N - 1);
+    const int br = lane / LPR, bq = lane % LPR, bc = n0 + 8 * bq, bcol = min(bc, p.N - 1);
     if constexpr (BT) {
 #pragma unroll
         for (int j = 0; j < CG; ++j)
             brow[j] = static_cast<const uint8_t *>(p.B) + (int64_t)min(n0 + 16 * j + lr, p.N - 1) * p.ldb * 2 + 16 * lq;
     } else {
-        brow[0] = static_cast<const uint8_t *>(p.B) + ((int64_t)(lane >> 3) * p.ldb + bcol) * 2;
+        brow[0] = static_cast<const uint8_t *>(p.B) + ((int64_t)br * p.ldb + bcol) * 2;
     }
     // (uniform) a chunk whose loads need no care: inside K; with columns past N also a row after it
     const int last = p.K - KC - (!BT && n0 + COLS > p.N ? 1 : 0);
@@ -94,7 +96,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void gemm_rows16(GroupedParams p) {
                     for (int i = 0; i < NI; ++i) c.b[j * NI + i] = ldg16(brow[j] + 2 * (k0 + 32 * i));
             } else {
 #pragma unroll
-                for (int i = 0; i < NL; ++i) c.b[i] = ldg16(brow[0] + (int64_t)(k0 + 8 * i) * p.ldb * 2);
+                for (int i = 0; i < NL; ++i) c.b[i] = ldg16(brow[0] + (int64_t)(k0 + RPL * i) * p.ldb * 2);
             }
 #pragma unroll
             for (int i = 0; i < NI; ++i) c.a[i] = ldg16(arow + 2 * (k0 + 32 * i));
@@ -108,7 +110,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void gemm_rows16(GroupedParams p) {
             } else {
 #pragma unroll
                 for (int i = 0; i < NL; ++i) {
-                    const int k = k0 + 8 * i + (lane >> 3);
+                    const int k = k0 + RPL * i + br;
                     c.b[i] = ldg16_row_end(static_cast<const uint8_t *>(p.B) + (int64_t)min(k, p.K - 1) * p.ldb * 2, bc, p.N);
                     if (k >= p.K) c.b[i] = u32x4{0, 0, 0, 0};
                 }
@@ -119,9 +121,10 @@ __global__ __launch_bounds__(WAVES * 64, 2) void gemm_rows16(GroupedParams p) {
         }
     };
 
-    // B stored K x N in the slot: row r of 128 bytes keeps 16-byte piece q at q ^ sw(r); the
-    // transposing read's lane a of each 16 takes row a / 4 + 8 g (and + 4), columns 4 (a % 4) .. +3
-    auto sw = [](int r) { return (((r >> 1) & 1) << 1) | (((r >> 3) & 1) << 2); };
+    // B stored K x N in the slot: row r of 128 (64) bytes keeps 16-byte piece q at q ^ sw(r); the
+    // transposing read's lane a of each 16 takes row a / 4 + 8 g (and + 4), columns 4 (a % 4) .. +3,
+    // and two groups g are served together: their rows' pieces stand in different banks
+    auto sw = [](int r) { return CG == 4 ? (((r >> 1) & 1) << 1) | (((r >> 3) & 1) << 2) : ((r >> 3) & 1) << 1; };
     const int rb = 8 * g + ((lane & 15) >> 2);
 
     f32x4 acc[CG];
@@ -130,7 +133,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void gemm_rows16(GroupedParams p) {
     auto stage = [&](const Chunk &c) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            const int at = BT ? put : (lane >> 3) * 128 + (((lane & 7) ^ sw(8 * i + (lane >> 3))) << 4);
+            const int at = BT ? put : br * 16 * LPR + ((bq ^ sw(RPL * i + br)) << 4);
             *reinterpret_cast<u32x4 *>(slot + 1024 * i + at) = c.b[i];
         }
 #pragma unroll
@@ -146,9 +149,9 @@ __global__ __launch_bounds__(WAVES * 64, 2) void gemm_rows16(GroupedParams p) {
                 if constexpr (BT) {
                     b = *reinterpret_cast<const u32x4 *>(slot + 1024 * (j * NI + i) + get);
                 } else {
-                    const uint8_t *q = slot + 4096 * i + rb * 128 + (((2 * j + ((lane & 3) >> 1)) ^ sw(rb)) << 4) + (lane & 1) * 8;
+                    const uint8_t *q = slot + (32 * i + rb) * 16 * LPR + (((2 * j + ((lane & 3) >> 1)) ^ sw(rb)) << 4) + (lane & 1) * 8;
                     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)q);
-                    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(q + 4 * 128));
+                    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(q + 4 * 16 * LPR));
                     b = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
                 }
                 acc[j] = TI::mma16(a, b, acc[j]);
@@ -206,10 +209,11 @@ hipError_t launch(const GroupedParams &p, unsigned grid, hipStream_t s) {
 
 template <class TI, class TO>
 const GroupedEntry *lookup(int op_b, int cg) {
-    static const GroupedEntry n = {launch<TI, TO, false, 4, 64>, 16, 64, "gemm_rows16_16x64"};
+    static const GroupedEntry n[2] = {{launch<TI, TO, false, 2, 64>, 16, 32, "gemm_rows16_16x32"},
+                                      {launch<TI, TO, false, 4, 64>, 16, 64, "gemm_rows16_16x64"}};
     static const GroupedEntry t[2] = {{launch<TI, TO, true, 1, 128>, 16, 16, "gemm_rows16_16x16"},
                                       {launch<TI, TO, true, 4, 64>, 16, 64, "gemm_rows16_16x64"}};
-    if (op_b == 0) return cg == 4 ? &n : nullptr;
+    if (op_b == 0) return cg == 2 ? &n[0] : cg == 4 ? &n[1] : nullptr;
     return op_b == 1 ? (cg == 1 ? &t[0] : cg == 4 ? &t[1] : nullptr) : nullptr;
 }
 

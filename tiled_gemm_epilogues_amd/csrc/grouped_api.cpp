@@ -151,7 +151,7 @@ gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grou
     case GEMM_ALGO_FAST_STAGED: if (tile != 0 && tile != 128 && tile != 64) return GEMM_STATUS_INVALID_VALUE; break;
     case GEMM_ALGO_GENERAL: if (tile != 0 && tile != 128 && tile != 64) return GEMM_STATUS_INVALID_VALUE; break;
     case GEMM_ALGO_SKINNY:
-        if (tile != 0 && tile != 64 && !(tile == 16 && op_b == GEMM_OP_T)) return GEMM_STATUS_INVALID_VALUE;
+        if (tile != 0 && tile != 64 && tile != (op_b == GEMM_OP_T ? 16 : 32)) return GEMM_STATUS_INVALID_VALUE;
         break;
     default: return GEMM_STATUS_INVALID_VALUE;
     }
@@ -188,12 +188,13 @@ gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grou
     // direct loads: whole 16-byte chunks
     const bool fast_ok = eab == 2 && d->K >= FAST_MIN_K && d->lda % 8 == 0 && d->ldb % 8 == 0 &&
                          d->stride_b % 8 == 0 && (t || (d->N % 8 == 0 && d->N > 0)) && offsets_ok;
-    // 16 x 64 tiles where they give every CU a workgroup, else 16 x 16 (B transposed): 4097 x 4097, one
-    // row, 18.2 -> 13.4 us; 8 rows over 16 experts, 1024 x 2048, even; but 200 rows over 8 experts,
-    // 1001 x 1001, 15.2 us with 16 x 64 tiles and 24.0 with 16 x 16
+    // 16 x 64 tiles where they give every CU a workgroup, else narrower ones: B transposed 16 x 16 (4097
+    // x 4097, one row, 16.5 -> 11.8 us, 2048 x 4096 10.1 -> 6.0; 200 rows over 8 experts, 1001 x 1001,
+    // 8.7 vs 11.3), else 16 x 32 (2048 x 4096, one row, 11.0 -> 9.2 us, 4097 x 4097 16.6 -> 12.8; 200 rows over
+    // 8 experts, 1001 x 1001, 8.2 vs 9.2)
     const auto rows16 = [&]() {
         p.any = rows16_table(ab, cd)(op_b, 4);
-        if (t && grid_of(p, *p.any, false) < 256) p.any = rows16_table(ab, cd)(op_b, 1);
+        if (grid_of(p, *p.any, false) < 256) p.any = rows16_table(ab, cd)(op_b, t ? 1 : 2);
     };
     switch (algo) {
     case GEMM_ALGO_SKINNY:
