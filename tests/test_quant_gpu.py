@@ -140,6 +140,23 @@ def test_strides_and_unaligned_pointers(algo, tile):
                algo=algo, tile=tile, seed=6)
 
 
+@pytest.mark.parametrize("algo,tile", KERNELS)
+def test_rows_far_apart(algo, tile):
+    # rows of A 2^24 bytes and more apart: 128 of them span 2^31
+    g = np.random.default_rng(8)
+    rows, N, K, block, lda = 40, 40, 320, 64, (1 << 23) + 8
+    A = ints(g, (rows, K), -3, 3, torch.float16)
+    Q = torch.from_numpy(g.integers(0, 256, (1, N, K // 2)).astype(np.uint8))
+    scales = torch.from_numpy(2.0 ** g.integers(-1, 2, (1, N, K // block))).to(torch.float16)
+    dA = torch.empty(rows, lda, dtype=torch.float16, device=DEV)
+    dA[:, :K] = A.to(DEV)
+    D = torch.empty(rows, N, dtype=torch.float32, device=DEV)
+    tge.QuantPlan(rows, N, K, block, 1, False, lda, ab="f16", cd="f32", algo=algo, tile=tile).run(
+        dA, Q.to(DEV), scales.to(DEV), None, None, D)
+    want = A.double() @ dequantised(Q, scales, None, block)[0].t()
+    assert (D.cpu().double() == want).all()
+
+
 @pytest.mark.parametrize("counts,start,behind", [([0], 0, 2), ([1] * 130, 1, 0), ([0, 0, 9], 0, 0),
                                                 ([200], 3, 3), ([16, 32, 64, 128], 0, 0)])
 @pytest.mark.parametrize("algo,tile", [("auto", 0), *KERNELS])

@@ -219,6 +219,41 @@ __device__ __forceinline__ void store_one(const QuantParams &p, int m, int n, fl
     static_cast<T *>(p.D)[idx] = (T)x;
 }
 
+// Eight columns of a row, nv of them inside N.
+template <class T>
+__device__ __forceinline__ void store_row(const QuantParams &p, int m, int n, int nv, const float (&sum)[8], const float (&bias)[8]) {
+    const int64_t idx = (int64_t)m * p.ldc + n;
+    const T *C = static_cast<const T *>(p.C) + idx;
+    T *D = static_cast<T *>(p.D) + idx;
+    T c[8], d[8];
+    if (p.has_beta) {
+        if (nv == 8) {
+            __builtin_memcpy(c, C, sizeof c);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) c[e] = C[min(e, nv - 1)];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float x = p.alpha * sum[e];
+        if (p.has_beta) x += p.beta * (float)c[e];
+        x += bias[e];
+        if (p.relu) x = x > 0.0f ? x : 0.0f;
+        d[e] = (T)x;
+    }
+    if (nv == 8) {
+        __builtin_memcpy(D, d, sizeof d);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < nv) D[e] = d[e];
+    }
+}
+
+// Waits for this wave's loads, the direct ones (which the compiler does not count) too.
+__device__ __forceinline__ void wait_all_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 // ---- few rows ----------------------------------------------------------------------------------
 // 16 rows and 16 * CG columns per workgroup, K divided over its WAVES waves; each wave reads its
 // weights once, through registers (one chunk ahead) and a private LDS slot that only changes the
@@ -363,12 +398,35 @@ __global__ __launch_bounds__(WAVES * 64, 2) void quant_rows(QuantParams p) {
 }
 
 // ---- many rows ---------------------------------------------------------------------------------
-// 128 x 128 output tile, 4 waves of 64 x 64.  Per chunk of 128 k, A (in pair order: permuted on
-// the way from registers to LDS) and the codes are staged in LDS once per workgroup, the next
-// chunk's loads in flight in registers during the current one; each wave turns the codes of its
-// 64 columns into fragments in registers, one group of 16 at a time.  One stage, so that two
-// workgroups fit a CU and one computes while the other is between its barriers.
+// 128 x 128 output tile, 4 waves of 64 x 64, two workgroups per CU.  Chunks of 128 k of A go to LDS
+// directly, the next one while this one is multiplied (two buffers, one barrier per chunk); each wave
+// loads the codes of its own 64 columns in fragment order (4 loads, which share cache lines badly, but
+// need no LDS) and brings its scales through a private slot.  A stays in its order, so the code
+// pairs are brought into A's: permuting A instead would take it through registers, and all 256
+// are in use.
+//
+// Bound by issue: of a chunk's instructions per wave (bf16, block 128) 80 are matrix ones (1280
+// cycles) and some 330 vector ones (1320: 11 per word of codes, 2 per sum and block), shared by two
+// waves per SIMD.  2048 x 4096 x 4096, block 128 with zero points, bf16 99 us (0.69 PFLOP/s), fp16 96;
+// block 32 137.  Without its loads it takes 20 us less, without the conversion and scaling 20.
+// Earlier form, everything staged through registers and two barriers per chunk: 104 us.
 constexpr int TM = 128, TN = 128, TNT = 256;
+
+// 8 values of a word in the order of A: (0,1) (2,3) (4,5) (6,7)
+__device__ __forceinline__ u32x4 row_order(u32x4 v) {
+    return u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x05040100u), __builtin_amdgcn_perm(v[3], v[2], 0x05040100u),
+                 __builtin_amdgcn_perm(v[1], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u)};
+}
+
+__device__ __forceinline__ uint32_t lds_addr(const uint8_t *p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)p;
+}
+
+// direct-to-LDS 16-byte load per lane (LDS destination lds + 16 * lane), see gemm_fast.hip
+__device__ __forceinline__ void dma16(const void *sbase, uint32_t voff, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0"
+                 :: "s"(sbase), "v"(voff), "s"(lds) : "memory", "m0");
+}
 
 template <class TI, class TO, int G, bool Z>
 __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
@@ -377,10 +435,10 @@ __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
     constexpr int NBLK = G >= 128 ? 1 : CHUNK / G;
     constexpr int SUB = 4 / NBLK;
     constexpr int SC = SCALES / NBLK;
-    // A in 8 groups of 16 rows x 4 pieces of 32 k, codes in 8 groups of 16 columns; scales and zero
-    // points (replaced every SC chunks)
-    constexpr int OFF_Q = TM * CHUNK * 2, OFF_S = OFF_Q + TN * CHUNK / 2, OFF_Z = OFF_S + TN * 16;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[OFF_Z + (Z ? TN * 8 : 0)];
+    // two buffers of A (8 groups of 16 rows x 4 pieces of 32 k); each wave's slot: codes of 32
+    // columns, scales and zero points of 64 (replaced every SC chunks)
+    constexpr int BUF = TM * CHUNK * 2, OFF_Z = 1024, SLOT = OFF_Z + (Z ? 512 : 0);
+    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * BUF + 4 * SLOT];
 
     int tn;
     if (!select_tile<(int)sizeof(T)>(p, TM, tn)) return;
@@ -389,45 +447,51 @@ __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
     const int wm = wave >> 1, wn = wave & 1;
     const int nch = (p.K + CHUNK - 1) / CHUNK, nblk = p.K / p.block;
     const int lr = lane >> 2, lq = lane & 3;
+    const int put = piece16(lr, lq), get = piece16(lane & 15, g);
+    uint8_t *const slot = smem + 2 * BUF + wave * SLOT;
 
-    // this wave loads A's row groups 2w, 2w+1 (4 pieces each) and the codes' column groups 2w, 2w+1
-    const uint8_t *arow[2], *qrow[2];
+    // A: this wave brings row groups 2w, 2w+1.  A direct load's lane writes position lane % 4 of row
+    // lane / 4, where piece16 keeps piece lq ^ (row / 4) % 4.
+    const uint8_t *const abase = dma_base<GROUP_ROWS>(p.A);
+    const bool direct = ((reinterpret_cast<uintptr_t>(abase) | (uintptr_t)p.lda * 2) & 15) == 0 && p.lda < (1 << 23);
+    int ar[2];
+    uint32_t voff[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int r = 16 * (2 * wave + i) + lr;
-        arow[i] = static_cast<const uint8_t *>(p.A) + (int64_t)min(r, p.M - 1) * p.lda * 2;
-        qrow[i] = p.Q + (int64_t)min(tn * TN + r, p.N - 1) * p.ldq;
+        ar[i] = min(16 * (2 * wave + i) + lr, p.M - 1);
+        voff[i] = (uint32_t)ar[i] * (uint32_t)p.lda * 2u + 16u * (uint32_t)(lq ^ ((lr >> 2) & 3));
     }
-    const int64_t srow = (int64_t)min(tn * TN + tid, p.N - 1) * p.lds;
-    const int put = piece16(lr, lq), get = piece16(lane & 15, g);
-    u32x4 st[2][4], sq[2];
-    auto fetch = [&](int ch) {
-        const int k0 = ch * CHUNK;
-        const int at = G >= 128 ? k0 / 2 + 16 * lq : min(k0 / 2 + 16 * lq, p.K / 2 - 16);
+    auto bring = [&](int ch) {
+        const int k0 = ch * CHUNK, buf = (ch & 1) * BUF + 8192 * wave;
+        if (direct && k0 + CHUNK <= p.K) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            sq[i] = ldg16(qrow[i] + at);
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int k = k0 + 32 * s + 8 * lq;
-                st[i][s] = ldg16(arow[i] + 2 * (G >= 128 ? k : min(k, p.K - 8)));
-            }
-        }
-    };
-    auto stage = [&](int ch) {
+                for (int s = 0; s < 4; ++s)
+                    dma16(abase + 2 * (int64_t)(k0 + 32 * s), voff[i], lds_addr(smem) + buf + (4 * i + s) * 1024);
+        } else {   // unaligned rows, or a chunk that ends inside K (after whole blocks): zeros past it
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            *reinterpret_cast<u32x4 *>(smem + OFF_Q + 1024 * (2 * wave + i) + put) = sq[i];
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                u32x4 v = pair_order(st[i][s]);
-                if constexpr (G < 128) {
-                    if (ch * CHUNK + 32 * s >= p.K) v = u32x4{0, 0, 0, 0};
+                for (int s = 0; s < 4; ++s) {
+                    const int k = k0 + 32 * s;
+                    u32x4 v = u32x4{0, 0, 0, 0};
+                    if (k < p.K) v = ldg16(static_cast<const uint8_t *>(p.A) + ((int64_t)ar[i] * p.lda + k + 8 * lq) * 2);
+                    *reinterpret_cast<u32x4 *>(smem + buf + (4 * i + s) * 1024 + put) = v;
                 }
-                *reinterpret_cast<u32x4 *>(smem + (4 * (2 * wave + i) + s) * 1024 + put) = v;
-            }
         }
     };
+    // codes of this wave's 64 columns, 16 rows of 64 bytes each
+    const uint8_t *qrow[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) qrow[j] = p.Q + (int64_t)min(tn * TN + wn * 64 + 16 * j + (lane & 15), p.N - 1) * p.ldq;
+    u32x4 sq[4];
+    auto fetch = [&](int ch) {
+        const int at = ch * (CHUNK / 2) + 16 * g;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sq[j] = ldg16(qrow[j] + (G >= 128 ? at : min(at, p.K / 2 - 16)));
+    };
+    const int64_t srow = (int64_t)min(tn * TN + wn * 64 + lane, p.N - 1) * p.lds;
     auto first_block = [&](int ch) { return G >= 128 ? block_of(p, ch) : ch * NBLK; };
 
     f32x4 acc[4][4];
@@ -436,77 +500,119 @@ __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-    ScaleRegs<Z> sr;
     int base = 0, next = 0;                                  // block at index 0 of the scales; chunk of new ones
     if (nch > 0) {
-        sr.load(p, srow, 0, nblk);
         fetch(0);
+        bring(0);
     }
-    const uint8_t *const la = smem + wm * 16384 + get;
-    const uint8_t *const lc = smem + OFF_Q + wn * 4096 + get;
 #pragma unroll 1
     for (int ch = 0; ch < nch; ++ch) {
-        if (ch == next) {
-            base = first_block(ch);
-            if (tid < TN) {
-                *reinterpret_cast<u32x4 *>(smem + OFF_S + 16 * tid) = sr.s;
-                if constexpr (Z) *reinterpret_cast<uint2 *>(smem + OFF_Z + 8 * tid) = sr.z;
-            }
-            next += SC;
-            if (next < nch) sr.load(p, srow, first_block(next), nblk);
-        }
-        stage(ch);
-        __syncthreads();
-        if (ch + 1 < nch) fetch(ch + 1);
-        const int bi = first_block(ch) - base;
+        wait_all_loads();                                    // this chunk's A, for every wave after the barrier
         u32x4 w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = exchange(*reinterpret_cast<const u32x4 *>(lc + 1024 * j));
+        for (int j = 0; j < 4; ++j) w[j] = exchange(sq[j]);
+        __syncthreads();                                     // (and the other buffer's reads are done)
+        if (ch + 1 < nch) bring(ch + 1);
+        if (ch == next) {
+            base = first_block(ch);
+            // loaded here and not ahead: the registers to hold them are not there (spilled 105 us, 99 so)
+            ScaleRegs<Z> sr;
+            sr.load(p, srow, base, nblk);
+            wave_order();
+            *reinterpret_cast<u32x4 *>(slot + 16 * lane) = sr.s;
+            if constexpr (Z) *reinterpret_cast<uint2 *>(slot + OFF_Z + 8 * lane) = sr.z;
+            next += SC;
+        }
+        const int bi = first_block(ch) - base;
+        Blocks<NBLK> blk[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = 16 * j + (lane & 15);
+            blk[j] = read_blocks<TI, NBLK, Z>(slot + 16 * row, slot + OFF_Z + 8 * row, bi);
+        }
+        const uint8_t *const la = smem + (ch & 1) * BUF + wm * 16384 + get;
+        // Steps of 4 matrix instructions (one word of codes against 4 row groups).  Beside them run the
+        // conversion of the next step's word and the scaling of the column group before.
+        u32x4 v = row_order(QT::values(w[0][0], blk[0].off[0]));
+        f32x4 tp[4], sump[4];
 #pragma unroll
         for (int b = 0; b < NBLK; ++b) {
             u32x4 a[4][SUB];
             f32x4 sum[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sum[i] = f32x4{0, 0, 0, 0};
+            for (int i = 0; i < 4; ++i) sum[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int s = 0; s < SUB; ++s) {
-                    a[i][s] = *reinterpret_cast<const u32x4 *>(la + (4 * i + b * SUB + s) * 1024);
-                    if constexpr (QT::SUMS) sum[i] = TI::mma16(a[i][s], QT::ones(), sum[i]);
-                }
+            for (int s = 0; s < SUB; ++s) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i][s] = *reinterpret_cast<const u32x4 *>(la + (4 * i + b * SUB + s) * 1024);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int row = wn * 64 + 16 * j + (lane & 15);
-                const Blocks<1> blk = read_blocks<TI, 1, Z>(smem + OFF_S + 16 * row, smem + OFF_Z + 8 * row, bi + b);
                 f32x4 t[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) t[i] = f32x4{0, 0, 0, 0};
+                if (b == NBLK - 1 && j == 2) fetch(min(ch + 1, nch - 1));   // (no branch: the last again)
 #pragma unroll
                 for (int s = 0; s < SUB; ++s) {
-                    const u32x4 v = QT::values(w[j][b * SUB + s], blk.off[0]);
+                    // next word: (s + 1, j), (0, j + 1) or the next block's first
+                    const int nj = s + 1 < SUB ? j : (j + 1) & 3, ns = s + 1 < SUB ? s + 1 : 0;
+                    const int nb = s + 1 < SUB || j < 3 ? b : b + 1;
+                    u32x4 nv = v;
+                    if (nb < NBLK) nv = row_order(QT::values(w[nj][nb * SUB + ns], blk[nj].off[nb]));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) t[i] = TI::mma16(a[i][s], v, t[i]);
+                    for (int i = 0; i < 4; ++i) {
+                        t[i] = TI::mma16(a[i][s], v, s ? t[i] : f32x4{0, 0, 0, 0});
+                        if (QT::SUMS && j == 0) sum[i] = TI::mma16(a[i][s], QT::ones(), sum[i]);
+                    }
+                    if (j > 0 || b > 0) {
+                        const int pj = (j + 3) & 3, pb = j > 0 ? b : b - 1;
+#pragma unroll
+                        for (int i = s * 4 / SUB; i < (s + 1) * 4 / SUB; ++i)
+                            add_block<TI>(acc[i][pj], tp[i], sump[i], blk[pj].s[pb], blk[pj].off[pb]);
+                    }
+                    v = nv;
+                    // one matrix instruction (two with the sums), then the vector ones that fit beside it
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (QT::SUMS && j == 0) __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
+                        else __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x2, SUB == 4 ? 5 : SUB == 2 ? 7 : 11, 0);
+                    }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) add_block<TI>(acc[i][j], t[i], sum[i], blk.s[0], blk.off[0]);
+                for (int i = 0; i < 4; ++i) {
+                    tp[i] = t[i];
+                    sump[i] = sum[i];
+                }
             }
         }
-        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) add_block<TI>(acc[i][3], tp[i], sump[i], blk[3].s[NBLK - 1], blk[3].off[NBLK - 1]);
     }
 
+    // The sums go through LDS, so that a store covers whole rows of 64 columns (8 lanes of 8 columns);
+    // 2-byte stores by the accumulators' layout took 3 us more (2048 x 4096 x 4096).
+    __syncthreads();
+    constexpr int STR = 68;                                  // floats between rows: no bank is met twice
+    float *const st = reinterpret_cast<float *>(smem) + wave * 16 * STR;
+    const int er = lane >> 3, ec = 8 * (lane & 7), n = tn * TN + wn * 64 + ec;
+    const int nv = min(p.N - n, 8);                          // columns of this lane
+    float bias[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int n = tn * TN + wn * 64 + 16 * j + (lane & 15);
-        if (n >= p.N) continue;
-        const float bias = p.has_bias ? static_cast<const float *>(p.bias)[n] : 0.0f;
+    for (int e = 0; e < 8; ++e) bias[e] = p.has_bias && nv > 0 ? static_cast<const float *>(p.bias)[n + min(e, nv - 1)] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+        wave_order();
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int m = wm * 64 + 16 * i + 4 * g + r;
-                if (m < p.M) store_one<T>(p, m, n, acc[i][j][r], bias);
-            }
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) st[(4 * g + r) * STR + 16 * j + (lane & 15)] = acc[i][j][r];
+        wave_order();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float x[8];
+            __builtin_memcpy(x, __builtin_assume_aligned(st + (8 * h + er) * STR + ec, 16), sizeof x);
+            const int m = wm * 64 + 16 * i + 8 * h + er;
+            if (m < p.M && nv > 0) store_row<T>(p, m, n, nv, x, bias);
+        }
     }
 }
 
