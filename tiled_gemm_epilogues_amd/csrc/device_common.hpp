@@ -403,16 +403,18 @@ __device__ __forceinline__ void select_k(GroupedParams &p, int id, int &tm, int 
 }
 
 // GROUP_K: the column sums of B over one range (the gradient of a bias added to its rows), as
-// extra workgroups of 256 threads in front of the products': COLSUM_COLS columns of one range,
-// 16 rows at a time, the 16 partial sums of a column added through `part` (256 x 8 floats of LDS).
-// Sums are in fp32 and in a fixed order.  These workgroups read B once more (a part of what the
-// products' workgroups read, N / M-th of A's bytes per tile row) beside the MFMA-bound ones.
-constexpr int COLSUM_COLS = 128;
+// extra workgroups of 256 threads in front of the products': COLSUM_COLS columns of one range, 32
+// rows at a time, eight times in flight; the 32 partial sums of a column are added through `part`
+// (256 x 8 floats of LDS).  Sums are in fp32 and in a fixed order.  They read B once more, hidden
+// beside the products: 16384 rows, 16 experts of 4096 x 2048, 316 us with and without them; 32768
+// rows, one expert of 4096 x 4096 (two full rounds of tiles), 987 -> 1067 (128 columns, 16 rows four
+// times in flight: 1223).
 template <class T>
 __device__ __forceinline__ void colsum_block(const GroupedParams &p, int id, float *part) {
+    constexpr int LPR = COLSUM_COLS / 8, ROWS = 256 / LPR;   // threads per row, rows at a time
     const int nb = (p.N + COLSUM_COLS - 1) / COLSUM_COLS;
     const int e = id / nb, tid = threadIdx.x;
-    const int n = (id - e * nb) * COLSUM_COLS + (tid & 15) * 8;
+    const int n = (id - e * nb) * COLSUM_COLS + (tid % LPR) * 8;
     int lo, hi;
     group_range(p, e, lo, hi);
     float s[8];
@@ -420,18 +422,18 @@ __device__ __forceinline__ void colsum_block(const GroupedParams &p, int id, flo
     for (int i = 0; i < 8; ++i) s[i] = 0.0f;
     const T *B = static_cast<const T *>(p.B);
     if (n + 8 <= p.N) {
-#pragma unroll 4
-        for (int r = lo + (tid >> 4); r < hi; r += 16) {
+#pragma unroll 8
+        for (int r = lo + tid / LPR; r < hi; r += ROWS) {
             T v[8];
             __builtin_memcpy(v, B + (int64_t)r * p.ldb + n, sizeof(v));
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[i] += (float)v[i];
         }
-    } else if (n < p.N) {
-        for (int r = lo + (tid >> 4); r < hi; r += 16)
+    } else if (n < p.N) {   // columns past N read the last one; they are not stored
+#pragma unroll 2
+        for (int r = lo + tid / LPR; r < hi; r += ROWS)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (n + i < p.N) s[i] += (float)B[(int64_t)r * p.ldb + n + i];
+            for (int i = 0; i < 8; ++i) s[i] += (float)B[(int64_t)r * p.ldb + min(n + i, p.N - 1)];
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) part[tid * 8 + i] = s[i];
@@ -440,7 +442,7 @@ __device__ __forceinline__ void colsum_block(const GroupedParams &p, int id, flo
         const int col = (id - e * nb) * COLSUM_COLS + tid;
         float t = 0.0f;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) t += part[(r * 16 + (tid >> 3)) * 8 + (tid & 7)];
+        for (int r = 0; r < ROWS; ++r) t += part[(r * LPR + (tid >> 3)) * 8 + (tid & 7)];
         if (col < p.N) p.colsum[(int64_t)e * p.N + col] = t;
     }
 }

@@ -42,6 +42,7 @@ using LaunchFn = hipError_t (*)(const GemmParams &, unsigned grid, hipStream_t);
 //               per workgroup
 // A range is clamped to [0, rows], so that no offset makes a kernel leave the operands.
 enum GroupMode { GROUP_NONE = 0, GROUP_ROWS = 1, GROUP_K = 2 };
+constexpr int COLSUM_COLS = 64;   // columns of a workgroup that sums B (gradient plans)
 struct GroupedParams : GemmParams {
     const int32_t *offs;
     int groups, rows;

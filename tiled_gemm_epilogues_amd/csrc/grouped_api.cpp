@@ -53,7 +53,7 @@ int64_t grid_of(const gemm_grouped_plan &p, const GroupedEntry &k, bool colsum) 
     const int64_t tn = ceil_div(p.N, k.bn);
     const __int128 g = p.mode == tge::GROUP_ROWS
                            ? (__int128)row_tiles(p.rows, p.groups, k.bm) * tn
-                           : (__int128)p.groups * (ceil_div(p.M, k.bm) * tn + (colsum ? ceil_div(p.N, 128) : 0));
+                           : (__int128)p.groups * (ceil_div(p.M, k.bm) * tn + (colsum ? ceil_div(p.N, tge::COLSUM_COLS) : 0));
     return g < MAX_GRID ? (int64_t)g : MAX_GRID;
 }
 
