@@ -175,6 +175,8 @@ def test_kernel_choice():
     assert _kernel(G(1, 2048, 4096, 1, "N")) == "gemm_rows16_16x32"
     assert _kernel(G(2048, 2048, 4096, 64, "T")) == "gemm_fast_128x128"
     assert _kernel(G(32768, 4096, 4096, 8, "T")) == "gemm_fast_256x256"
+    assert _kernel(G(4096, 4096, 4096, 1, "T")) == "gemm_fast_256x256"
+    assert _kernel(G(5120, 4096, 4096, 1, "T")) == "gemm_fast_128x128"
     assert _kernel(G(30000, 4095, 4096, 8, "N")) == "gemm_fast_128x128_rs"
     assert _kernel(G(3001, 777, 1001, 7, "N", cd="f32")) == "gemm_fast_64x64_rs"
     assert _kernel(G(1000, 1000, 1000, 4, "N")) == "gemm_fast_64x64"
@@ -185,6 +187,8 @@ def test_kernel_choice():
     assert _kernel(W(40, 1955, 7260, 4)) == "gemm_fast_128x128_rs"
     assert _kernel(W(1003, 1024, 704, 8)) == "gemm_fast_64x64"
     assert _kernel(W(32768, 4096, 4096, 4)) == "gemm_fast_256x256"
+    assert _kernel(W(32768, 4096, 4096, 1)) == "gemm_fast_256x256"
+    assert _kernel(W(8192, 5120, 4096, 1)) == "gemm_fast_128x128"
     assert _kernel(W(16384, 4, 2048, 16)).startswith("gemm_mfma")
     # a pinned kernel whose preconditions do not hold: the general one
     assert _kernel(G(64, 7, 64, 2, "N", algo="skinny")).startswith("gemm_mfma")

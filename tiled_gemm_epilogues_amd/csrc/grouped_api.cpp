@@ -109,8 +109,14 @@ bool few_rows_pay(int64_t avg, double few) { return avg <= 6 || few <= 700; }
 // x 4096 over 8 experts 310 -> 275 us, 4096 x 14336 x 4096 over 8 562 -> 490, 16384 x 8192 x 2048
 // over 16 592 -> 475, 32768 x 2048 x 1024 over 64 189 -> 182; but 8192 x 2048 x 4096 over 16 even
 // and 2048 x 8192 x 2048 over 2 75 -> 87.
-bool wide_tiles_pay(int64_t rows, int64_t n, int64_t avg, int64_t N) {
-    return avg >= 512 && ((double)rows / 256 + 0.5 * (double)n) * (double)ceil_div(N, 256) >= 384;
+// With one expert the number of tiles is known, and what counts is that the last round is nearly
+// full: 4096 x 4096 x 4096 (256 tiles) 111 -> 96, 6144 x 2048 x 4096 (192) 97 -> 83, 7168 x 4096 x
+// 4096 (448) 203 -> 171; but 5120 x 4096 x 4096 (320) 148 -> 158.
+bool rounds_full(int64_t wide_tiles) { return wide_tiles > 0 && 4 * wide_tiles >= 3 * 256 * ceil_div(wide_tiles, 256); }
+bool wide_tiles_pay(int64_t rows, int64_t groups, int64_t n, int64_t avg, int64_t N) {
+    if (avg < 512) return false;
+    if (groups == 1) return rounds_full(ceil_div(rows, 256) * ceil_div(N, 256));
+    return ((double)rows / 256 + 0.5 * (double)n) * (double)ceil_div(N, 256) >= 384;
 }
 
 // Hands a finished plan out, with its description.
@@ -216,7 +222,7 @@ gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grou
             // 1000 over 7 (189) 18.2 -> 17.1; but 1000 x 4096 x 512 over 2 (281) 11.5 -> 13.4 and
             // 2100 x 1408 x 2048 over 32 (356) 46 -> 62
             if (fast_ok) {
-                const int tl = wide_tiles_pay(d->rows, n, avg, d->N) ? 256 : tiles < 200 ? 64 : 128;
+                const int tl = wide_tiles_pay(d->rows, d->groups, n, avg, d->N) ? 256 : tiles < 200 ? 64 : 128;
                 p.fast = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, tl, 0);
             }
             // register-staged: 390 x 1968 x 2581 41 -> 23 us, 3001 x 777 x 1001 over 7 experts 28 -> 24, 700
@@ -276,10 +282,11 @@ gemm_status_t gemm_grouped_grad_plan_create(gemm_grouped_plan_t *out, const gemm
     if (fast_ok && algo == GEMM_ALGO_FAST) p.fast = fast_table(ab, cd)(tge::GROUP_K, 0, tile ? tile : 128, 0);
     else if (fast_ok && algo == GEMM_ALGO_AUTO) {
         // The 256-wide tiles (one workgroup per CU, so that each tile's start and store are not
-        // hidden) pay for long sums only.  Measured (bf16 -> fp32; 128 -> 256): 32768 rows, 4 experts
-        // of 4096 x 4096, 986 -> 821 us; 16384 rows, 8 of 8192 x 4096, even; 16384 rows, 16 of 4096
-        // x 2048, 356 -> 416; 32768 rows, 8 of 1024 x 1024 (128 wide tiles) 114 -> 138.
-        const bool wide = avg >= 4096 && d->groups * ceil_div(d->M, 256) * ceil_div(d->N, 256) >= 512;
+        // hidden) pay for long sums and nearly full rounds only.  Measured (bf16 -> fp32; 128 -> 256):
+        // 32768 rows, one expert of 4096 x 4096 (256 wide tiles), 994 -> 772 us, 4 of them 986 -> 821,
+        // 8192 rows, one of 8192 x 3328 (416) 439 -> 374; but one of 5120 x 4096 (320) 305 -> 344,
+        // 16384 rows, 16 experts of 4096 x 2048, 356 -> 416, 32768 rows, 8 of 1024 x 1024 (128) 114 -> 138.
+        const bool wide = avg >= 4096 && rounds_full(d->groups * ceil_div(d->M, 256) * ceil_div(d->N, 256));
         // 64-wide tiles where the 128-wide ones do not fill the chip or the sums are short: 1003
         // rows, 8 experts of 1024 x 704 (384 128-wide tiles), 12.1 -> 9.6 us, 2000 rows, 2 of 72 x
         // 3504, 17 -> 12, 40 rows, 4 of 1952 x 7264, 46 -> 42; 16000 rows, 8 of 2048 x 2048, 144 -> 192.
