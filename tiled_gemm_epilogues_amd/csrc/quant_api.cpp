@@ -53,17 +53,20 @@ int64_t grid_of(const gemm_quant_plan &p, bool by_expert) {
 }
 
 // Whether the 128 x 128 tiles beat the kernel for few rows (16 x 64).  Both take a time in
-// proportion to K; at K = 4096 a round of tiles takes 68 us however few there are and 0.195 us per
-// tile from two per CU on, the other kernel 0.0205 us per workgroup.  Measured (bf16, blocks of 128;
-// few rows -> tiles): 512 x 4096 x 4096 47 vs 69 us, 1024 x 4096 x 4096 87 -> 69, 2048 x 4096 x 4096
-// 169 -> 100, 2048 x 1024 x 4096 46 vs 68, 256 x 16384 x 2048 51 -> 41, 512 x 8192 x 8192 162 -> 127.
-// Experts' ranges end inside a tile: half a tile each is counted for them.
+// proportion to K; at K = 4096 a round of tiles takes 70 us however few there are and 0.19 us per tile
+// from two per CU on (blocks of 32: 95 and 0.25), the other kernel 0.022 to 0.037 us per workgroup, by
+// block and zero points.  Measured (bf16; few rows -> tiles), blocks of 128 without zero points: 512 x
+// 4096 x 4096 56 vs 70 us, 700 rows 62 vs 67, 1024 98 -> 71, 2048 177 -> 97, 2048 x 1024 x 4096 46 vs
+// 68, 256 x 16384 x 2048 56 -> 39, 512 x 8192 x 8192 174 -> 130; 700 x 4096 x 4096 with zero points 83
+// -> 71, with blocks of 64 81 -> 76 without them and 87 -> 79 with, with blocks of 32 106 vs 99
+// (fp16: 76 vs 89) and 105 -> 101.  Experts' ranges end inside a tile: half a tile each is counted.
 bool tiles_pay(const gemm_quant_plan &p) {
+    static const double few_us[3][2] = {{0.031, 0.037}, {0.027, 0.032}, {0.022, 0.030}};   // [block][zeros]
     const double ragged = p.groups > 1 ? 0.5 * (double)(p.rows < p.groups ? p.rows : p.groups) : 0.0;
     const double few = ((double)p.rows / 16 + ragged) * (double)ceil_div(p.N, 64);
     const double tiles = ((double)p.rows / 128 + ragged) * (double)ceil_div(p.N, 128);
-    const double t = 0.195 * tiles;
-    return 0.0205 * few > (t > 68.0 ? t : 68.0);
+    const double round = p.block == 32 ? 95.0 : 70.0, t = (p.block == 32 ? 0.25 : 0.19) * tiles;
+    return few_us[p.block == 32 ? 0 : p.block == 64 ? 1 : 2][p.zeros != 0] * few > (t > round ? t : round);
 }
 
 }  // namespace
