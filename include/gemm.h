@@ -439,7 +439,7 @@ gemm_status_t gemm_grouped_plan_describe(gemm_grouped_plan_t plan, char *buf, si
  * byte along k: the low half of byte k / 2 is an even k.  scales have the type of A, zeros are
  * uint8; without zeros the zero point is 8.  The sum over a block is taken with exact weights
  * (code - zero) in fp32, multiplied by its scale in fp32 and added up in fp32: no weight is
- * rounded.  With groups > 1 there is one W (and bias) per expert and D is computed for the row
+ * rounded.  An infinity in A gives NaN with BF16 (the sum is taken as two that cancel).  With groups > 1 there is one W (and bias) per expert and D is computed for the row
  * ranges that offsets give, as for the products grouped by expert above; with groups == 1 offsets
  * may be NULL (all rows).
  *

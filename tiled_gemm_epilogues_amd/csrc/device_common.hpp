@@ -342,7 +342,8 @@ __device__ __forceinline__ RangeChunk range_chunk(const GroupedParams &p, int e0
 // it has no tile (false).  The tiles of one expert are consecutive and each XCD takes a contiguous
 // run of them, so an expert's weights stay with few XCDs' L2.  On return the pointers stand at
 // the tile's first row (so that 32-bit offsets inside the tile are enough however long A and D
-// are), p.M is the number of the expert's rows from there on, and tn the column tile; `expert`,
+// are; the selection costs nothing measurable up to 64 ranges, 0.5 us at 128 and 7 us at 1024),
+// p.M is the number of the expert's rows from there on, and tn the column tile; `expert`,
 // where given, receives the expert.
 template <int EAB, int ECD>
 __device__ __forceinline__ bool select_rows(GroupedParams &p, int wg, int bm, int &tn, int *expert = nullptr) {

@@ -44,6 +44,14 @@
 //    ReLU functor of "CUTLASS", "Fusing Element-wise Operations"): alpha, beta*C, bias[j], ReLU
 //    and the conversion run on the accumulators; the result goes through a per-wave LDS staging
 //    buffer so that D is written in whole 128-byte lines.
+//  * products grouped by expert (GRP) are instances of the same kernel that first find their
+//    expert from the offsets on the device (select_rows, select_k): tiles of 256, 128 and 64, the last
+//    two register-staged too.  256-wide ones are bound by the MFMAs and by one workgroup per CU,
+//    whose start and stores nothing hides: 32768 rows, 8 experts of 14336 x 4096, bf16 2.9 ms (1.33
+//    PFLOP/s); with the gate's C read in the epilogue 16384 rows, 16 of 8192 x 2048, 604 us (480
+//    without it).  128-wide gradients wait for their slabs, two stages deep (MFMAs a third busy), and
+//    store fp32 sums: 16384 rows, 16 of 4096 x 2048, 361 us (0.76 PFLOP/s).  64-wide ones fill the
+//    chip where the others leave CUs empty: 1003 rows, 8 gradients of 1024 x 704, 9.6 us.
 //
 // Preconditions (checked by the host): 16- or 8-bit inputs and K of at least one slab; for the
 // direct loads also A/B base pointers, leading dimensions and batch strides 16-byte aligned and
@@ -73,7 +81,8 @@ typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 constexpr int SLAB_BYTES = 128;                      // K bytes per slab: 64 fp16/bf16 or 128 int8
 constexpr int NT = 256;                              // 4 waves
 
-// Tile geometry: TL x TL output tile (256, or 128 for mid-size products), 4 waves of TL/2 x TL/2.
+// Tile geometry: TL x TL output tile (256, 128 for mid-size products, 64 for small grouped ones), 4
+// waves of TL/2 x TL/2.
 // One operand slab is TL * 128 bytes in either layout (32 KiB at TL = 256).  LDS map: [A stage
 // 0 | A stage 1 | B stage 0 | B stage 1], so that every fragment read is (base register) +
 // (stage and k-slice offset as the instruction's 16-bit immediate).
@@ -91,13 +100,13 @@ __device__ __forceinline__ int swz_kc(int r) { return (r ^ (r >> 3)) & 7; }
 __device__ __forceinline__ int off_kc(int r, int c) { return r * 128 + ((c ^ swz_kc(r)) << 4); }
 
 // [k][mn] layout (M/N-contiguous operands): 64 rows of TL 16-bit elements (512 B at TL = 256, 256 B
-// at TL = 128) or 128 rows of 256 B (8-bit, TL = 256 only).  A transposing read (8 bytes per lane) is served 32 lanes at a time; the 16 lanes of
-// one k group touch 4 (16-bit) or 8 (8-bit) consecutive rows at 2 adjacent 16-byte chunks, and
-// the swizzle gives those accesses distinct banks.  With the 16x16 MFMA shape the two k groups
-// served together (lanes 0-15 and 16-31) lie 16 (16-bit) or 32 (8-bit) rows apart: one more
-// row bit of the swizzle moves the second group to the other half of the banks (the 32x32
-// shape keeps the k groups of a pass in one row block, and adds whole k-slices to a base
-// address, which must not change the swizzle).
+// at TL = 128, 128 B at TL = 64) or 128 rows of 256 B (8-bit, TL = 256 only).  A transposing read (8
+// bytes per lane) is served 32 lanes at a time; the 16 lanes of one k group touch 4 (16-bit) or 8
+// (8-bit) consecutive rows at 2 adjacent 16-byte chunks, and the swizzle gives those accesses
+// distinct banks.  With the 16x16 MFMA shape the two k groups served together (lanes 0-15 and 16-31)
+// lie 16 (16-bit) or 32 (8-bit) rows apart: one more row bit of the swizzle moves the second group to
+// the other half of the banks (the 32x32 shape keeps the k groups of a pass in one row block, and
+// adds whole k-slices to a base address, which must not change the swizzle).
 template <int E, int MF, int TL = 256>
 __device__ __forceinline__ int swz_mc(int k) {
     if constexpr (E == 1 && TL == 128) {
@@ -550,7 +559,8 @@ struct Sched {
 // (global -> VGPR -> LDS, same LDS image) for layouts the direct loads cannot take; the load
 // transforms are then applied once per element on the way to LDS (XF stays off).  TL: the
 // workgroup tile (256; 128 for mid-size products: two workgroups per CU, 16x16 shape, direct
-// loads, no load transforms).  GRP: GroupMode of the launch (products grouped by expert).
+// loads, no load transforms; 64, four of them, grouped only).  GRP: GroupMode of the launch
+// (products grouped by expert).
 template <class TI, class TO, bool AK, bool BK, int MF, bool XF, bool RS = false, int TL = 256,
           int GRP = GROUP_NONE>
 __global__ __launch_bounds__(NT, TL == 256 ? 1 : TL == 128 ? 2 : 4) void gemm_fast(ParamsOf<GRP> p) {

@@ -16,7 +16,8 @@
 //   sum A * (q - z) = sum A * (16 + q) - (16 + z) * sum A,
 //
 // with sum A from one more matrix instruction per A fragment, against a fragment of ones.  The
-// terms are at most 31 / 8 times larger than a centred sum's: two bits of fp32's 24.
+// terms are at most 31 / 8 times larger than a centred sum's: two bits of fp32's 24.  An infinite
+// A gives NaN that way (inf - inf) where the definition has an infinity; fp16 keeps it.
 //
 // A lane of a 16x16x32 matrix instruction holds 8 k of one weight row (n = lane % 16), its lane
 // group g = lane / 16 saying which 8 of 32.  A 16-byte load of a lane covers 32 k of its row: lane
@@ -260,6 +261,13 @@ __device__ __forceinline__ void wait_all_loads() { asm volatile("s_waitcnt vmcnt
 // lane order.  A comes from L2: every workgroup reads it, CG column groups share one reading.  The
 // waves' sums are added through LDS in wave order.  Two workgroups fit a CU, so that one's loads
 // are in flight while the other starts or ends.
+//
+// Bound by the weights' bytes, and below that by the latency of each wave's chunks, one ahead (the
+// vector units, which convert the codes, are a quarter busy).  Measured, cold: 1 row, 4096 x 4096,
+// block 128 (8.7 MB) 6.0 us, of which the launch 2.9; 16 rows, 16384 x 4096, block 64 with zero points
+// 15.1 us (2.5 TB/s); 32 rows over 32 experts of 2048 x 4096 25.8 us (3.4 TB/s).  4 or 16 waves and 32
+// columns measured no better; 16 columns take one row of 4096 x 4096 from 8.6 to 5.8 us (more
+// workgroups), 64 columns 16 rows of 16384 x 4096 from 16.4 to 13.7 (A read less often).
 constexpr int WAVES = 8;
 
 template <class TI, class TO, int G, bool Z, int CG>
