@@ -172,8 +172,15 @@ __device__ __forceinline__ void add_block(f32x4 &acc, f32x4 t, f32x4 sum, float 
 // row (lane / 4, lane % 4), so that the address unit sees whole 64-byte pieces (16 lanes on 16
 // different rows cost four times as many cache accesses, which bound the first version of this
 // kernel); a fragment takes row lane % 16, piece lane / 16.  LDS carries the data from one lane
-// order to the other.
-__device__ __forceinline__ int piece16(int r, int q) { return r * 64 + ((q ^ ((r >> 2) & 3)) << 4); }
+// order to the other.  A 16-byte read serves lanes 0-3, 12-15, 20-23 and 24-27 together, then 4-11, 16-19
+// and 28-31 (and 32 on likewise); with the pieces of row quads 0 .. 3 moved by swap16 = 0, 2, 3, 1
+// their 16 places differ (bank conflicts of the tiles 4.8 M -> 0.65 M cycles, 102.3 -> 101.1 us;
+// moved by 0, 1, 2, 3 half of the reads met).
+__device__ __forceinline__ int swap16(int r) {
+    const int t = r >> 2;
+    return ((t << 1) & 2) ^ (t & 2 ? 3 : 0);
+}
+__device__ __forceinline__ int piece16(int r, int q) { return r * 64 + ((q ^ swap16(r)) << 4); }
 
 // Orders this wave's LDS accesses (they execute in order; no instruction).
 __device__ __forceinline__ void wave_order() {
@@ -459,7 +466,7 @@ __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
     uint8_t *const slot = smem + 2 * BUF + wave * SLOT;
 
     // A: this wave brings row groups 2w, 2w+1.  A direct load's lane writes position lane % 4 of row
-    // lane / 4, where piece16 keeps piece lq ^ (row / 4) % 4.
+    // lane / 4, where piece16 keeps piece lq ^ swap16(row).
     const uint8_t *const abase = dma_base<GROUP_ROWS>(p.A);
     const bool direct = ((reinterpret_cast<uintptr_t>(abase) | (uintptr_t)p.lda * 2) & 15) == 0 && p.lda < (1 << 23);
     int ar[2];
@@ -467,7 +474,7 @@ __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         ar[i] = min(16 * (2 * wave + i) + lr, p.M - 1);
-        voff[i] = (uint32_t)ar[i] * (uint32_t)p.lda * 2u + 16u * (uint32_t)(lq ^ ((lr >> 2) & 3));
+        voff[i] = (uint32_t)ar[i] * (uint32_t)p.lda * 2u + 16u * (uint32_t)(lq ^ swap16(lr));
     }
     auto bring = [&](int ch) {
         const int k0 = ch * CHUNK, buf = (ch & 1) * BUF + 8192 * wave;

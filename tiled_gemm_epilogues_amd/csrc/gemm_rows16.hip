@@ -38,8 +38,12 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int WAVES = 8;
 
-// 16 rows x 64 bytes: 16-byte piece q of row r
-__device__ __forceinline__ int piece16(int r, int q) { return r * 64 + ((q ^ ((r >> 2) & 3)) << 4); }
+// 16 rows x 64 bytes: 16-byte piece q of row r, at q ^ {0, 2, 3, 1}[r / 4] (a 16-byte read serves lanes
+// 0-3, 12-15, 20-23 and 24-27 together, then 4-11, 16-19 and 28-31: 16 different places either way)
+__device__ __forceinline__ int piece16(int r, int q) {
+    const int t = r >> 2;
+    return r * 64 + ((q ^ ((t << 1) & 2) ^ (t & 2 ? 3 : 0)) << 4);
+}
 
 // Orders this wave's LDS accesses (they execute in order; no instruction).
 __device__ __forceinline__ void wave_order() {
