@@ -271,9 +271,9 @@ __device__ __forceinline__ void wait_all_loads() { asm volatile("s_waitcnt vmcnt
 //
 // Bound by the weights' bytes, and below that by the latency of each wave's chunks, one ahead (the
 // vector units, which convert the codes, are a quarter busy).  Measured, cold: 1 row, 4096 x 4096,
-// block 128 (8.7 MB) 6.0 us, of which the launch 2.9; 16 rows, 16384 x 4096, block 64 with zero points
-// 15.1 us (2.5 TB/s); 32 rows over 32 experts of 2048 x 4096 25.8 us (3.4 TB/s).  4 or 16 waves and 32
-// columns measured no better; 16 columns take one row of 4096 x 4096 from 8.6 to 5.8 us (more
+// block 128 (8.7 MB) 5.8 us, of which the launch 2.9; 16 rows, 16384 x 4096, block 64 with zero points
+// 14.7 us (2.5 TB/s); 32 rows over 32 experts of 2048 x 4096 25.8 us (3.4 TB/s).  4 or 16 waves and 32
+// columns measured no better, two chunks in flight slower (25.9 -> 32.5 for the last); 16 columns take one row of 4096 x 4096 from 8.6 to 5.8 us (more
 // workgroups), 64 columns 16 rows of 16384 x 4096 from 16.4 to 13.7 (A read less often).
 constexpr int WAVES = 8;
 
@@ -422,7 +422,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void quant_rows(QuantParams p) {
 //
 // Bound by issue: of a chunk's instructions per wave (bf16, block 128) 80 are matrix ones (1280
 // cycles) and some 330 vector ones (1320: 11 per word of codes, 2 per sum and block), shared by two
-// waves per SIMD.  2048 x 4096 x 4096, block 128 with zero points, bf16 99 us (0.69 PFLOP/s), fp16 96;
+// waves per SIMD.  2048 x 4096 x 4096, block 128 with zero points, bf16 98 us (0.70 PFLOP/s), fp16 96;
 // block 32 137.  Without its loads it takes 20 us less, without the conversion and scaling 20.
 // Earlier form, everything staged through registers and two barriers per chunk: 104 us.
 constexpr int TM = 128, TN = 128, TNT = 256;
