@@ -402,7 +402,12 @@ __device__ __forceinline__ void store_tile_staged(const ParamsOf<GRP> &p, int mb
     // workgroups than CUs), streaming stores keep the L2 and the infinity cache for the A and B
     // panels those rounds read (measured with the 16x16 shape: 3-8 % faster at 8192^3); in a
     // single round, and with the 32x32 shape, the plain stores measured faster
-    const bool stream_d = GRP != GROUP_NONE ? gridDim.x > (WT == 128 ? 256 : 512)
+    // Grouped: not where D's rows start off 64-byte lines and the sums are short, so that the stores
+    // are most of the work: a line's two parts then reach memory one by one (31 gradients of 1032 x
+    // 5896 from 24 rows, fp32: streaming 296 us, plain 158; 3000 x 14728, 4 experts, 16 bits, K 128:
+    // 43 and 31, K 256: 49 and 41, K 512: 66 and 82; fp32 K 64: 60 and 51, K 256: 64 and 80).
+    const bool apart = ((reinterpret_cast<uintptr_t>(p.D) | (uintptr_t)p.ldc * ES) & 63) != 0 && p.K * ES <= 512;
+    const bool stream_d = GRP != GROUP_NONE ? !apart && gridDim.x > (WT == 128 ? 256 : 512)
                           : MF == 16 && (int64_t)p.tiles_m * p.tiles_n * p.batch > (WT == 128 ? 256 : 512);
     typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
     // accumulator value e of group q in block b

@@ -113,8 +113,10 @@ bool few_rows_pay(int64_t avg, double few) { return avg <= 6 || few <= 700; }
 // full: 4096 x 4096 x 4096 (256 tiles) 111 -> 96, 6144 x 2048 x 4096 (192) 97 -> 83, 7168 x 4096 x
 // 4096 (448) 203 -> 171; but 5120 x 4096 x 4096 (320) 148 -> 158.
 bool rounds_full(int64_t wide_tiles) { return wide_tiles > 0 && 4 * wide_tiles >= 3 * 256 * ceil_div(wide_tiles, 256); }
-bool wide_tiles_pay(int64_t rows, int64_t groups, int64_t n, int64_t avg, int64_t N) {
-    if (avg < 512) return false;
+// Sums below 512 leave them mostly storing, which the other tiles overlap: 8192 x 8192 over 4, K 128, 41 ->
+// 54, K 256 58 -> 66, K 512 82 -> 89 (32768 x 8192 over 8: 161 -> 165, 216 -> 208, 338 -> 296).
+bool wide_tiles_pay(int64_t rows, int64_t groups, int64_t n, int64_t avg, int64_t N, int64_t K) {
+    if (avg < 512 || K < 512) return false;
     if (groups == 1) return rounds_full(ceil_div(rows, 256) * ceil_div(N, 256));
     return ((double)rows / 256 + 0.5 * (double)n) * (double)ceil_div(N, 256) >= 384;
 }
@@ -222,7 +224,7 @@ gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grou
             // 1000 over 7 (189) 18.2 -> 17.1; but 1000 x 4096 x 512 over 2 (281) 11.5 -> 13.4 and
             // 2100 x 1408 x 2048 over 32 (356) 46 -> 62
             if (fast_ok) {
-                const int tl = wide_tiles_pay(d->rows, d->groups, n, avg, d->N) ? 256 : tiles < 200 ? 64 : 128;
+                const int tl = wide_tiles_pay(d->rows, d->groups, n, avg, d->N, d->K) ? 256 : tiles < 200 ? 64 : 128;
                 p.fast = fast_table(ab, cd)(tge::GROUP_ROWS, op_b, tl, 0);
             }
             // register-staged: 390 x 1968 x 2581 41 -> 23 us, 3001 x 777 x 1001 over 7 experts 28 -> 24, 700
