@@ -378,7 +378,7 @@ struct EpiMap {
 
 // GATE (grouped products, float outputs): with p.gate, D = C > 0 ? alpha * acc : 0 in place of
 // the sum with beta * C.
-template <class O, class Acc, int MF, bool BETA, bool FULL, int GRP, class AccV, int NF>
+template <class O, class Acc, int MF, bool BETA, bool FULL, int GRP, bool RS, class AccV, int NF>
 __device__ __forceinline__ void store_tile_staged(const ParamsOf<GRP> &p, int mbase, int nbase, int lane,
                                                   AccV (&acc)[NF][NF], uint8_t *stg) {
     using T = typename O::T;
@@ -405,8 +405,10 @@ __device__ __forceinline__ void store_tile_staged(const ParamsOf<GRP> &p, int mb
     // Grouped: not where D's rows start off 64-byte lines and the sums are short, so that the stores
     // are most of the work: a line's two parts then reach memory one by one (31 gradients of 1032 x
     // 5896 from 24 rows, fp32: streaming 296 us, plain 158; 3000 x 14728, 4 experts, 16 bits, K 128:
-    // 43 and 31, K 256: 49 and 41, K 512: 66 and 82; fp32 K 64: 60 and 51, K 256: 64 and 80).
-    const bool apart = ((reinterpret_cast<uintptr_t>(p.D) | (uintptr_t)p.ldc * ES) & 63) != 0 && p.K * ES <= 512;
+    // 43 and 31, K 256: 49 and 41, K 512: 66 and 82; fp32 K 64: 60 and 51, K 256: 64 and 80).  Only
+    // the shortest sums of register-staged operands, whose loads need the caches more (10540 x 7800 x 121:
+    // 108 and 124; 31 gradients of 1031 x 5896 from 24 rows: 246 and 171).
+    const bool apart = ((reinterpret_cast<uintptr_t>(p.D) | (uintptr_t)p.ldc * ES) & 63) != 0 && p.K * ES <= (RS ? 32 : 512);
     const bool stream_d = GRP != GROUP_NONE ? !apart && gridDim.x > (WT == 128 ? 256 : 512)
                           : MF == 16 && (int64_t)p.tiles_m * p.tiles_n * p.batch > (WT == 128 ? 256 : 512);
     typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
@@ -527,18 +529,18 @@ __device__ __forceinline__ void store_tile_staged(const ParamsOf<GRP> &p, int mb
     }
 }
 
-template <class O, class Acc, int MF, int GRP, class AccV, int NF>
+template <class O, class Acc, int MF, int GRP, bool RS, class AccV, int NF>
 __device__ __forceinline__ void epilogue(const ParamsOf<GRP> &p, int mbase, int nbase, int lane,
                                          AccV (&acc)[NF][NF], uint8_t *stg) {
     // interior wave tiles (the common case) take a path with no edge checks
     constexpr int WT = NF * MF;
     const bool full = mbase + WT <= p.M && nbase + WT <= p.N;
     if (full) {
-        if (p.has_beta) store_tile_staged<O, Acc, MF, true, true, GRP>(p, mbase, nbase, lane, acc, stg);
-        else store_tile_staged<O, Acc, MF, false, true, GRP>(p, mbase, nbase, lane, acc, stg);
+        if (p.has_beta) store_tile_staged<O, Acc, MF, true, true, GRP, RS>(p, mbase, nbase, lane, acc, stg);
+        else store_tile_staged<O, Acc, MF, false, true, GRP, RS>(p, mbase, nbase, lane, acc, stg);
     } else {
-        if (p.has_beta) store_tile_staged<O, Acc, MF, true, false, GRP>(p, mbase, nbase, lane, acc, stg);
-        else store_tile_staged<O, Acc, MF, false, false, GRP>(p, mbase, nbase, lane, acc, stg);
+        if (p.has_beta) store_tile_staged<O, Acc, MF, true, false, GRP, RS>(p, mbase, nbase, lane, acc, stg);
+        else store_tile_staged<O, Acc, MF, false, false, GRP, RS>(p, mbase, nbase, lane, acc, stg);
     }
 }
 
@@ -832,7 +834,7 @@ __global__ __launch_bounds__(NT, TL == 256 ? 1 : TL == 128 ? 2 : 4) void gemm_fa
     }
 
     // every wave's reads of the stage-1 buffers ended before the last slab's barrier
-    epilogue<TO, acc_t, MF, GRP>(p, m0 + wm * G::WT, n0 + wn * G::WT, lane, acc, stg);
+    epilogue<TO, acc_t, MF, GRP, RS>(p, m0 + wm * G::WT, n0 + wn * G::WT, lane, acc, stg);
 }
 
 // MFMA shape of the fast path.  Both shapes give the same results (fp32/int32 accumulation of
