@@ -406,9 +406,9 @@ __device__ __forceinline__ void store_tile_staged(const ParamsOf<GRP> &p, int mb
     // are most of the work: a line's two parts then reach memory one by one (31 gradients of 1032 x
     // 5896 from 24 rows, fp32: streaming 296 us, plain 158; 3000 x 14728, 4 experts, 16 bits, K 128:
     // 43 and 31, K 256: 49 and 41, K 512: 66 and 82; fp32 K 64: 60 and 51, K 256: 64 and 80).  Only
-    // the shortest sums of register-staged operands, whose loads need the caches more (10540 x 7800 x 121:
-    // 108 and 124; 31 gradients of 1031 x 5896 from 24 rows: 246 and 171).
-    const bool apart = ((reinterpret_cast<uintptr_t>(p.D) | (uintptr_t)p.ldc * ES) & 63) != 0 && p.K * ES <= (RS ? 32 : 512);
+    // up to 32 for register-staged operands, whose loads need the caches more (10540 x 7800 x 121: 108 and
+    // 124; 4 gradients of 4147 x 6298, fp32, 9 rows each 158 and 101, 32 rows 158 and 102).
+    const bool apart = ((reinterpret_cast<uintptr_t>(p.D) | (uintptr_t)p.ldc * ES) & 63) != 0 && p.K <= (RS ? 32 : 512 / ES);
     const bool stream_d = GRP != GROUP_NONE ? !apart && gridDim.x > (WT == 128 ? 256 : 512)
                           : MF == 16 && (int64_t)p.tiles_m * p.tiles_n * p.batch > (WT == 128 ? 256 : 512);
     typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
