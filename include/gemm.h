@@ -437,11 +437,12 @@ gemm_status_t gemm_grouped_plan_describe(gemm_grouped_plan_t plan, char *buf, si
  *
  * A is rows x K, C and D rows x N, row-major; W has N rows of K codes of 4 bits (0 .. 15), two per
  * byte along k: the low half of byte k / 2 is an even k.  scales have the type of A, zeros are
- * uint8; without zeros the zero point is 8.  The sum over a block is taken with exact weights
- * (code - zero) in fp32, multiplied by its scale in fp32 and added up in fp32: no weight is
- * rounded.  An infinity in A gives NaN with BF16 (the sum is taken as two that cancel).  With groups > 1 there is one W (and bias) per expert and D is computed for the row
- * ranges that offsets give, as for the products grouped by expert above; with groups == 1 offsets
- * may be NULL (all rows).
+ * uint8; without zeros the zero point is 8.  The products of a block's values of A
+ * with code - zero (exact: -255 .. 15) are added up in fp32, multiplied by its scale in fp32 and added
+ * to the other blocks' in fp32: no weight is rounded, and one that is zero adds exactly 0 (NaN to an
+ * infinity or NaN in A).  With groups > 1 there is one W (and bias) per expert and D is computed for
+ * the row ranges that offsets give, as for the products grouped by expert above; with groups == 1
+ * offsets may be NULL (all rows).
  *
  * Types: F16 -> F16 | F32, BF16 -> BF16 | F32; bias is fp32.  No alignment beyond the elements'
  * own is required.  A plan holds no device memory.

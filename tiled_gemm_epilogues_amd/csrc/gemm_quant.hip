@@ -7,17 +7,15 @@
 // The inner sums run on the matrix cores in the type of A, in which the small integers are exact,
 // and the scale multiplies each block's sum in fp32: no weight is ever rounded.
 //
-// Codes become 16-bit floats by bit operations: the 4 bits are moved to the upper mantissa bits
-// below the exponent of 16.0, which gives 16 + q.  One 32-bit word of 8 codes yields the pairs
-// (k, k+4), k = 0 .. 3, with one shift and one and-or each; A's 8 values of the same k are brought
-// into that order with four byte permutes.  For fp16 the offset 16 + z is subtracted with packed
-// adds (exact).  bf16 has no packed add, so its sums keep the offset,
-//
-//   sum A * (q - z) = sum A * (16 + q) - (16 + z) * sum A,
-//
-// with sum A from one more matrix instruction per A fragment, against a fragment of ones.  The
-// terms are at most 31 / 8 times larger than a centred sum's: two bits of fp32's 24.  An infinite
-// A gives NaN that way (inf - inf) where the definition has an infinity; fp16 keeps it.
+// Codes become fp16 by bit operations: the 4 bits are set into the mantissa below the exponent of a
+// power of two, which gives that power + q; one 32-bit word of 8 codes yields the pairs (k, k+4),
+// k = 0 .. 3.  Then power + z is subtracted, so that the products are taken with q - z itself: -255
+// .. 15, exact in fp16 and in bf16 (8 bits).  For fp16 that is one packed subtraction per pair.
+// bf16 has no packed arithmetic: mixed-precision FMAs take the fp16 halves to fp32 differences, whose
+// upper halves are packed, in the order of A's rows at no cost (17 instructions per word; fp16 12, and 4
+// byte permutes for that order).  (bf16 sums of A * (16 + q) with (16 + z) * sum A subtracted take 7 per
+// word and one more matrix instruction per A fragment, but cancel: weights that are all zero left
+// rounding errors of sum A, and an infinite or very large A gave NaN.)
 //
 // A lane of a 16x16x32 matrix instruction holds 8 k of one weight row (n = lane % 16), its lane
 // group g = lane / 16 saying which 8 of 32.  A 16-byte load of a lane covers 32 k of its row: lane
@@ -59,33 +57,22 @@ __device__ __forceinline__ u32x4 pair_order(u32x4 a) {
 // pair (with literals it would be two).
 __device__ __forceinline__ void in_registers(uint32_t &m, uint32_t &o) { asm("" : "+s"(m), "+v"(o)); }
 
-// 16 + q of the 8 codes of a word, as pairs (0,4) (1,5) (2,6) (3,7)
-template <class TI>
-__device__ __forceinline__ u32x4 codes16(uint32_t w);
-template <>
-__device__ __forceinline__ u32x4 codes16<TF16>(uint32_t w) {
-    uint32_t m = 0x03c003c0u, o = 0x4c004c00u;   // mantissa bits 6-9; 16.0
-    in_registers(m, o);
-    return u32x4{((w << 6) & m) | o, ((w << 2) & m) | o, ((w >> 2) & m) | o, ((w >> 6) & m) | o};
-}
-template <>
-__device__ __forceinline__ u32x4 codes16<TBF16>(uint32_t w) {
-    uint32_t m = 0x00780078u, o = 0x41804180u;   // mantissa bits 3-6; 16.0
-    in_registers(m, o);
-    return u32x4{((w << 3) & m) | o, ((w >> 1) & m) | o, ((w >> 5) & m) | o, ((w >> 9) & m) | o};
-}
-
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 
+// Per input type: what a block's zero point is held as (Off), and the values q - z of a word's codes,
+// exact, as the pairs (0,4) (1,5) (2,6) (3,7) (PAIRS) or in the order of A's rows.
 template <class TI>
 struct Quant;
 template <>
 struct Quant<TF16> {
     using T = _Float16;
-    static constexpr bool SUMS = false;
-    // q - z of a word's codes (exact: integers below 32 in magnitude)
-    __device__ static u32x4 values(uint32_t w, float off) {
-        u32x4 v = codes16<TF16>(w);
+    static constexpr bool PAIRS = true;
+    using Off = float;                                       // 16 + z
+    __device__ static Off offset(float z) { return 16.0f + z; }
+    __device__ static u32x4 values(uint32_t w, Off off) {
+        uint32_t m = 0x03c003c0u, b = 0x4c004c00u;           // mantissa bits 6-9 of 16.0
+        in_registers(m, b);
+        u32x4 v = {((w << 6) & m) | b, ((w << 2) & m) | b, ((w >> 2) & m) | b, ((w >> 6) & m) | b};
         const _Float16 o = (_Float16)off;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -94,20 +81,51 @@ struct Quant<TF16> {
         }
         return v;
     }
-    __device__ static u32x4 ones() { return u32x4{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u}; }
 };
 template <>
 struct Quant<TBF16> {
     using T = __bf16;
-    static constexpr bool SUMS = true;
-    __device__ static u32x4 values(uint32_t w, float) { return codes16<TBF16>(w); }
-    __device__ static u32x4 ones() { return u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}; }
+    static constexpr bool PAIRS = false;
+    using Off = h2;                                          // -(1024 + z) and -(64 + z)
+    __device__ static Off offset(float z) { return h2{(_Float16)(-1024.0f - z), (_Float16)(-64.0f - z)}; }
+    // (the low halves are zero)
+    __device__ static uint32_t pack(float a, float b) {
+        return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
+    }
+    __device__ static u32x4 values(uint32_t w, Off off) {
+        // codes at bits 0 and 16 are the lowest of the mantissas of 1024.0, those at bits 4 and 20 the
+        // same of 64.0; codes 2, 3, 6 and 7 lie 8 bits further up
+        uint32_t m0 = 0x000f000fu, b0 = 0x64006400u, m1 = 0x00f000f0u, b1 = 0x54005400u;
+        in_registers(m0, b0);
+        in_registers(m1, b1);
+        float one = 1.0f;
+        asm("" : "+v"(one));                                 // keeps the product: fma(half, one, half) is one instruction
+        const uint32_t x[4] = {(w & m0) | b0, (w & m1) | b1, ((w >> 8) & m0) | b0, ((w >> 8) & m1) | b1};
+        float lo[4], hi[4];                                  // codes i and i + 4
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const h2 h = __builtin_bit_cast(h2, x[i]);
+            lo[i] = __builtin_fmaf((float)h[0], one, (float)off[i & 1]);
+            hi[i] = __builtin_fmaf((float)h[1], one, (float)off[i & 1]);
+        }
+        return u32x4{pack(lo[0], lo[1]), pack(lo[2], lo[3]), pack(hi[0], hi[1]), pack(hi[2], hi[3])};
+    }
 };
 
-// Scales and offsets 16 + z of a weight row's blocks in one chunk.
-template <int NBLK>
+// The values of a word in the order of A's rows: (0,1) (2,3) (4,5) (6,7)
+template <class TI>
+__device__ __forceinline__ u32x4 row_values(uint32_t w, typename Quant<TI>::Off off) {
+    const u32x4 v = Quant<TI>::values(w, off);
+    if constexpr (!Quant<TI>::PAIRS) return v;
+    else return u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x05040100u), __builtin_amdgcn_perm(v[3], v[2], 0x05040100u),
+                      __builtin_amdgcn_perm(v[1], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u)};
+}
+
+// Scales and zero points of a weight row's blocks in one chunk.
+template <class TI, int NBLK>
 struct Blocks {
-    float s[NBLK], off[NBLK];
+    float s[NBLK];
+    typename Quant<TI>::Off off[NBLK];
 };
 
 // Eight consecutive scales (16 bytes) and zero points (8 bytes) of one weight row, as loaded; a
@@ -143,29 +161,25 @@ struct ScaleRegs {
 };
 // A row's eight in LDS (16 bytes of scales; 8 of zero points), and the NBLK from block i on.
 template <class TI, int NBLK, bool Z>
-__device__ __forceinline__ Blocks<NBLK> read_blocks(const uint8_t *s, const uint8_t *z, int i) {
+__device__ __forceinline__ Blocks<TI, NBLK> read_blocks(const uint8_t *s, const uint8_t *z, int i) {
     using T = typename Quant<TI>::T;
     T v[NBLK];
     uint8_t w[NBLK];
     __builtin_memcpy(v, __builtin_assume_aligned(s + 2 * i, 2 * NBLK), sizeof v);
     if constexpr (Z) __builtin_memcpy(w, __builtin_assume_aligned(z + i, NBLK), sizeof w);
-    Blocks<NBLK> x;
+    Blocks<TI, NBLK> x;
 #pragma unroll
     for (int b = 0; b < NBLK; ++b) {
         x.s[b] = (float)v[b];
-        x.off[b] = Z ? 16.0f + (float)w[b] : 24.0f;
+        x.off[b] = Quant<TI>::offset(Z ? (float)w[b] : 8.0f);
     }
     return x;
 }
 
-// Adds one block's sum to the accumulator: the offset's part off, times the scale.
-template <class TI>
-__device__ __forceinline__ void add_block(f32x4 &acc, f32x4 t, f32x4 sum, float s, float off) {
+// Adds one block's sum, times its scale, to the accumulator.
+__device__ __forceinline__ void add_block(f32x4 &acc, f32x4 t, float s) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float x = Quant<TI>::SUMS ? __builtin_fmaf(-off, sum[e], t[e]) : t[e];
-        acc[e] = __builtin_fmaf(s, x, acc[e]);
-    }
+    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(s, t[e], acc[e]);
 }
 
 // 16 rows x 64 bytes in LDS: 16-byte piece q of row r.  Global loads take 4 consecutive lanes per
@@ -269,12 +283,13 @@ __device__ __forceinline__ void wait_all_loads() { asm volatile("s_waitcnt vmcnt
 // waves' sums are added through LDS in wave order.  Two workgroups fit a CU, so that one's loads
 // are in flight while the other starts or ends.
 //
-// Bound by the weights' bytes, and below that by the latency of each wave's chunks, one ahead (the
-// vector units, which convert the codes, are a quarter busy).  Measured, cold: 1 row, 4096 x 4096,
-// block 128 (8.7 MB) 5.8 us, of which the launch 2.9; 16 rows, 16384 x 4096, block 64 with zero points
-// 14.7 us (2.5 TB/s); 32 rows over 32 experts of 2048 x 4096 25.8 us (3.4 TB/s).  4 or 16 waves and 32
-// columns measured no better, two chunks in flight slower (25.9 -> 32.5 for the last); 16 columns take one row of 4096 x 4096 from 8.6 to 5.8 us (more
-// workgroups), 64 columns 16 rows of 16384 x 4096 from 16.4 to 13.7 (A read less often).
+// Bound by the weights' bytes, and below that by the latency of each wave's chunks, one ahead, and the
+// conversion of the codes.  Measured, operands cold: 1 row, 4096 x 4096, block 128 (8.7 MB), bf16 6.3
+// us, of which the launch 2.9; 16 rows, 16384 x 4096, block 64 with zero points, fp16 14.9 us (2.5 TB/s), bf16
+// 15.5; 32 rows over 32 experts (20 of them used) of 2048 x 4096, block 128, bf16 29.5, fp16 27.3.  4 or 16
+// waves and 32 columns measured no better, two chunks in flight slower (25.9 -> 32.5 for the last); 16
+// columns take one row of 4096 x 4096 from 8.6 to 5.8 us (more workgroups), 64 columns 16 rows of 16384 x
+// 4096 from 16.4 to 13.7 (A read less often; both with an earlier form of the conversion).
 constexpr int WAVES = 8;
 
 template <class TI, class TO, int G, bool Z, int CG>
@@ -327,13 +342,13 @@ __global__ __launch_bounds__(WAVES * 64, 2) void quant_rows(QuantParams p) {
     f32x4 acc[CG];
 #pragma unroll
     for (int j = 0; j < CG; ++j) acc[j] = f32x4{0, 0, 0, 0};
-    // chunk ch from registers to the slot, A in pair order
+    // chunk ch from registers to the slot, A in the order of the codes
     auto stage = [&](const Chunk &c, int ch) {
 #pragma unroll
         for (int j = 0; j < CG; ++j) *reinterpret_cast<u32x4 *>(slot + 1024 * j + put) = c.q[j];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            u32x4 v = pair_order(c.a[i]);
+            u32x4 v = QT::PAIRS ? pair_order(c.a[i]) : c.a[i];
             if constexpr (G < 128) {   // an instruction's 32 k are inside K or past it
                 if (ch * CHUNK + 32 * i >= p.K) v = u32x4{0, 0, 0, 0};
             }
@@ -343,7 +358,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void quant_rows(QuantParams p) {
     // the chunk in the slot, its scales from index bi on
     auto compute = [&](int bi) {
         u32x4 w[CG];
-        Blocks<NBLK> blk[CG];
+        Blocks<TI, NBLK> blk[CG];
 #pragma unroll
         for (int j = 0; j < CG; ++j) {
             const int row = 16 * j + (lane & 15);
@@ -352,18 +367,17 @@ __global__ __launch_bounds__(WAVES * 64, 2) void quant_rows(QuantParams p) {
         }
 #pragma unroll
         for (int b = 0; b < NBLK; ++b) {
-            f32x4 t[CG], sum = f32x4{0, 0, 0, 0};
+            f32x4 t[CG];
 #pragma unroll
             for (int j = 0; j < CG; ++j) t[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int i = b * SUB; i < (b + 1) * SUB; ++i) {
                 const u32x4 a = *reinterpret_cast<const u32x4 *>(slot + OFF_A + 1024 * i + get);
-                if constexpr (QT::SUMS) sum = TI::mma16(a, QT::ones(), sum);
 #pragma unroll
                 for (int j = 0; j < CG; ++j) t[j] = TI::mma16(a, QT::values(w[j][i], blk[j].off[b]), t[j]);
             }
 #pragma unroll
-            for (int j = 0; j < CG; ++j) add_block<TI>(acc[j], t[j], sum, blk[j].s[b], blk[j].off[b]);
+            for (int j = 0; j < CG; ++j) add_block(acc[j], t[j], blk[j].s[b]);
         }
     };
 
@@ -420,18 +434,12 @@ __global__ __launch_bounds__(WAVES * 64, 2) void quant_rows(QuantParams p) {
 // pairs are brought into A's: permuting A instead would take it through registers, and all 256
 // are in use.
 //
-// Bound by issue: of a chunk's instructions per wave (bf16, block 128) 80 are matrix ones (1280
-// cycles) and some 330 vector ones (1320: 11 per word of codes, 2 per sum and block), shared by two
-// waves per SIMD.  2048 x 4096 x 4096, block 128 with zero points, bf16 98 us (0.70 PFLOP/s), fp16 96;
-// block 32 137.  Without its loads it takes 20 us less, without the conversion and scaling 20.
+// Bound by issue: of a chunk's instructions per wave (bf16, block 128) 64 are matrix ones (1024
+// cycles) and some 350 vector ones (17 per word of codes, 1 per sum and block), shared by two
+// waves per SIMD.  2048 x 4096 x 4096, operands cold, block 128 with zero points, bf16 101 us (0.68
+// PFLOP/s), fp16 97, without them 95 and 92; block 32 130 and 129, 118 and 118.
 // Earlier form, everything staged through registers and two barriers per chunk: 104 us.
 constexpr int TM = 128, TN = 128, TNT = 256;
-
-// 8 values of a word in the order of A: (0,1) (2,3) (4,5) (6,7)
-__device__ __forceinline__ u32x4 row_order(u32x4 v) {
-    return u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x05040100u), __builtin_amdgcn_perm(v[3], v[2], 0x05040100u),
-                 __builtin_amdgcn_perm(v[1], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u)};
-}
 
 __device__ __forceinline__ uint32_t lds_addr(const uint8_t *p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)p;
@@ -539,7 +547,7 @@ __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
             next += SC;
         }
         const int bi = first_block(ch) - base;
-        Blocks<NBLK> blk[4];
+        Blocks<TI, NBLK> blk[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int row = 16 * j + (lane & 15);
@@ -548,14 +556,11 @@ __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
         const uint8_t *const la = smem + (ch & 1) * BUF + wm * 16384 + get;
         // Steps of 4 matrix instructions (one word of codes against 4 row groups).  Beside them run the
         // conversion of the next step's word and the scaling of the column group before.
-        u32x4 v = row_order(QT::values(w[0][0], blk[0].off[0]));
-        f32x4 tp[4], sump[4];
+        u32x4 v = row_values<TI>(w[0][0], blk[0].off[0]);
+        f32x4 tp[4];
 #pragma unroll
         for (int b = 0; b < NBLK; ++b) {
             u32x4 a[4][SUB];
-            f32x4 sum[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int s = 0; s < SUB; ++s) {
 #pragma unroll
@@ -571,36 +576,29 @@ __global__ __launch_bounds__(TNT, 2) void quant_tile(QuantParams p) {
                     const int nj = s + 1 < SUB ? j : (j + 1) & 3, ns = s + 1 < SUB ? s + 1 : 0;
                     const int nb = s + 1 < SUB || j < 3 ? b : b + 1;
                     u32x4 nv = v;
-                    if (nb < NBLK) nv = row_order(QT::values(w[nj][nb * SUB + ns], blk[nj].off[nb]));
+                    if (nb < NBLK) nv = row_values<TI>(w[nj][nb * SUB + ns], blk[nj].off[nb]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        t[i] = TI::mma16(a[i][s], v, s ? t[i] : f32x4{0, 0, 0, 0});
-                        if (QT::SUMS && j == 0) sum[i] = TI::mma16(a[i][s], QT::ones(), sum[i]);
-                    }
+                    for (int i = 0; i < 4; ++i) t[i] = TI::mma16(a[i][s], v, s ? t[i] : f32x4{0, 0, 0, 0});
                     if (j > 0 || b > 0) {
                         const int pj = (j + 3) & 3, pb = j > 0 ? b : b - 1;
 #pragma unroll
                         for (int i = s * 4 / SUB; i < (s + 1) * 4 / SUB; ++i)
-                            add_block<TI>(acc[i][pj], tp[i], sump[i], blk[pj].s[pb], blk[pj].off[pb]);
+                            add_block(acc[i][pj], tp[i], blk[pj].s[pb]);
                     }
                     v = nv;
-                    // one matrix instruction (two with the sums), then the vector ones that fit beside it
+                    // one matrix instruction, then the vector ones that fit beside it
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        if (QT::SUMS && j == 0) __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
-                        else __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
                         __builtin_amdgcn_sched_group_barrier(0x2, SUB == 4 ? 5 : SUB == 2 ? 7 : 11, 0);
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    tp[i] = t[i];
-                    sump[i] = sum[i];
-                }
+                for (int i = 0; i < 4; ++i) tp[i] = t[i];
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) add_block<TI>(acc[i][3], tp[i], sump[i], blk[3].s[NBLK - 1], blk[3].off[NBLK - 1]);
+        for (int i = 0; i < 4; ++i) add_block(acc[i][3], tp[i], blk[3].s[NBLK - 1]);
     }
 
     // The sums go through LDS, so that a store covers whole rows of 64 columns (8 lanes of 8 columns);

@@ -53,20 +53,22 @@ int64_t grid_of(const gemm_quant_plan &p, bool by_expert) {
 }
 
 // Whether the 128 x 128 tiles beat the kernel for few rows (16 x 64).  Both take a time in
-// proportion to K; at K = 4096 a round of tiles takes 70 us however few there are and 0.19 us per tile
-// from two per CU on (blocks of 32: 95 and 0.25), the other kernel 0.022 to 0.037 us per workgroup, by
-// block and zero points.  Measured (bf16; few rows -> tiles), blocks of 128 without zero points: 512 x
-// 4096 x 4096 56 vs 70 us, 700 rows 62 vs 67, 1024 98 -> 71, 2048 177 -> 97, 2048 x 1024 x 4096 46 vs
-// 68, 256 x 16384 x 2048 56 -> 39, 512 x 8192 x 8192 174 -> 130; 700 x 4096 x 4096 with zero points 83
-// -> 71, with blocks of 64 81 -> 76 without them and 87 -> 79 with, with blocks of 32 106 vs 99
-// (fp16: 76 vs 89) and 105 -> 101.  Experts' ranges end inside a tile: half a tile each is counted.
+// proportion to K; at K = 4096 a round of tiles takes 58 to 79 us however few there are and 0.19 us per
+// tile from two per CU on (blocks of 32: 88 to 102, and 0.25), the other kernel 0.022 to 0.045 us per
+// workgroup, by type, block and zero points.  Measured (few rows -> tiles): bf16, blocks of 128 without
+// zero points, 512 x 4096 x 4096 62 vs 69 us, 700 rows 78 -> 68, 1024 113 -> 70, 2048 x 1024 x 4096 57 vs 68,
+// 256 x 16384 x 2048 64 -> 39, 512 x 8192 x 8192 192 -> 129; with zero points 512 x 4096 x 4096 74 -> 58,
+// 256 rows 40 vs 58; 600 rows, blocks of 64 75 vs 74 without them and 95 -> 79 with, blocks of 32
+// 97 vs 92 and 111 -> 102.  fp16, 700 rows: blocks of 128 69 -> 67 and 90 -> 65, of 64 77 -> 71 and
+// 94 -> 75, of 32 79 vs 88 and 108 -> 97.  Experts' ranges end inside a tile: half a tile each is counted.
 bool tiles_pay(const gemm_quant_plan &p) {
-    static const double few_us[3][2] = {{0.031, 0.037}, {0.027, 0.032}, {0.022, 0.030}};   // [block][zeros]
+    static const double few_us[2][3][2] = {{{0.031, 0.037}, {0.027, 0.032}, {0.022, 0.030}},    // [bf16][block][zeros]
+                                           {{0.038, 0.045}, {0.029, 0.038}, {0.028, 0.037}}};
     const double ragged = p.groups > 1 ? 0.5 * (double)(p.rows < p.groups ? p.rows : p.groups) : 0.0;
     const double few = ((double)p.rows / 16 + ragged) * (double)ceil_div(p.N, 64);
     const double tiles = ((double)p.rows / 128 + ragged) * (double)ceil_div(p.N, 128);
     const double round = p.block == 32 ? 95.0 : 70.0, t = (p.block == 32 ? 0.25 : 0.19) * tiles;
-    return few_us[p.block == 32 ? 0 : p.block == 64 ? 1 : 2][p.zeros != 0] * few > (t > round ? t : round);
+    return few_us[p.ab == GEMM_BF16][p.block == 32 ? 0 : p.block == 64 ? 1 : 2][p.zeros != 0] * few > (t > round ? t : round);
 }
 
 }  // namespace
