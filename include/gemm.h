@@ -398,9 +398,9 @@ typedef struct {
 /*
  * Host-only, like gemm_plan_create.  Return INVALID_VALUE for a NULL argument, a negative size,
  * groups < 1, a leading dimension or stride below its minimum, or an enum or tile out of range;
- * NOT_SUPPORTED for a type pair outside the table, a size or leading dimension of 2^31 or more, 2^20
- * groups or more, one expert's B spanning 2^31 bytes or more, or a grid of 2^23
- * workgroups; ALLOC_FAILED without host memory.
+ * NOT_SUPPORTED for a type pair outside the table, a size or leading dimension of 2^31 or more, more
+ * than 2^31 - 1024 rows of a gradient plan, 2^20 groups or more, one expert's B spanning 2^31 bytes or
+ * more, or a grid of 2^23 workgroups; ALLOC_FAILED without host memory.
  */
 gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grouped_desc_t *desc);
 gemm_status_t gemm_grouped_grad_plan_create(gemm_grouped_plan_t *out,

@@ -28,6 +28,8 @@ struct gemm_grouped_plan {
 namespace {
 
 constexpr int64_t FAST_MIN_K = 64;         // one slab of the fast kernel (16-bit inputs)
+// Rows of a gradient plan, at most: the kernels add a step of up to 256 to a row number in 32 bits.
+constexpr int64_t MAX_SUM_ROWS = LIM31 - 1024;
 
 using TableFn = const GroupedEntry *(*)(int, int, int);
 using FastFn = const GroupedEntry *(*)(int, int, int, int);
@@ -255,6 +257,7 @@ gemm_status_t gemm_grouped_grad_plan_create(gemm_grouped_plan_t *out, const gemm
     }
     const gemm_status_t st = check_common(d->rows, d->N, d->M, d->groups, d->lda, d->ldb, d->ldc, ab, cd);
     if (st != GEMM_STATUS_SUCCESS) return st;
+    if (d->rows > MAX_SUM_ROWS) return GEMM_STATUS_NOT_SUPPORTED;
     if (d->lda < (d->M > 1 ? d->M : 1) || d->ldb < (d->N > 1 ? d->N : 1) || d->ldc < (d->N > 1 ? d->N : 1))
         return GEMM_STATUS_INVALID_VALUE;
     const int64_t span = d->M > 0 && d->N > 0 ? (d->M - 1) * d->ldc + d->N : 0;
