@@ -385,7 +385,8 @@ typedef struct {
 /*
  * Description of a gradient plan.  A is rows x M (lda >= M), B rows x N (ldb >= N); D_e and C_e
  * are M x N at D, C + e * stride_c (ldc >= N; stride_c at least one D_e).  An expert without rows
- * gets beta * C_e and a zero bias_grad.  algo and tile as above, without SKINNY.
+ * gets beta * C_e and a zero bias_grad.  algo and tile as above, without SKINNY; FAST falls back to the
+ * register-staged kernel first.
  */
 typedef struct {
     int64_t rows, M, N, groups;

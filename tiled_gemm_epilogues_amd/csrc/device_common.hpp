@@ -407,9 +407,9 @@ __device__ __forceinline__ void select_k(GroupedParams &p, int id, int &tm, int 
 // extra workgroups of 256 threads in front of the products': COLSUM_COLS columns of one range, 32
 // rows at a time, eight times in flight; the 32 partial sums of a column are added through `part`
 // (256 x 8 floats of LDS).  Sums are in fp32 and in a fixed order.  They read B once more, hidden
-// beside the products: 16384 rows, 16 experts of 4096 x 2048, 316 us with and without them; 32768
-// rows, one expert of 4096 x 4096 (two full rounds of tiles), 987 -> 1067 (128 columns, 16 rows four
-// times in flight: 1223).
+// beside the products: 16384 rows, 16 experts of 4096 x 2048, 365 us without and 371 with them; 32768
+// rows, one expert of 4096 x 4096 (one full round of 256-wide tiles), 778 and 857 (in two rounds of
+// 128-wide ones 987 and 1067; with 128 columns, 16 rows four times in flight 1223).
 template <class T>
 __device__ __forceinline__ void colsum_block(const GroupedParams &p, int id, float *part) {
     constexpr int LPR = COLSUM_COLS / 8, ROWS = 256 / LPR;   // threads per row, rows at a time

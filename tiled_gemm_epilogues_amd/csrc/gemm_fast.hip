@@ -47,11 +47,11 @@
 //  * products grouped by expert (GRP) are instances of the same kernel that first find their
 //    expert from the offsets on the device (select_rows, select_k): tiles of 256, 128 and 64, the last
 //    two register-staged too.  256-wide ones are bound by the MFMAs and by one workgroup per CU,
-//    whose start and stores nothing hides: 32768 rows, 8 experts of 14336 x 4096, bf16 2.9 ms (1.33
-//    PFLOP/s); with the gate's C read in the epilogue 16384 rows, 16 of 8192 x 2048, 604 us (480
+//    whose start and stores nothing hides: 32768 rows, 8 experts of 14336 x 4096, bf16 2.9 ms (1.32
+//    PFLOP/s); with the gate's C read in the epilogue 16384 rows, 16 of 8192 x 2048, 603 us (492
 //    without it).  128-wide gradients wait for their slabs, two stages deep (MFMAs a third busy), and
-//    store fp32 sums: 16384 rows, 16 of 4096 x 2048, 361 us (0.76 PFLOP/s).  64-wide ones fill the
-//    chip where the others leave CUs empty: 1003 rows, 8 gradients of 1024 x 704, 9.6 us.
+//    store fp32 sums: 16384 rows, 16 of 4096 x 2048, 366 us (0.75 PFLOP/s).  64-wide ones fill the
+//    chip where the others leave CUs empty: 1003 rows, 8 gradients of 1024 x 704, 8.4 us.
 //
 // Preconditions (checked by the host): 16- or 8-bit inputs and K of at least one slab; for the
 // direct loads also A/B base pointers, leading dimensions and batch strides 16-byte aligned and
@@ -376,8 +376,8 @@ struct EpiMap {
     __device__ static int bgroup(int q) { return MF == 32 ? q : (q % NBG); }
 };
 
-// GATE (grouped products, float outputs): with p.gate, D = C > 0 ? alpha * acc : 0 in place of
-// the sum with beta * C.
+// BETA: C is read.  GRP: GroupMode; in GROUP_ROWS launches with p.gate D = C > 0 ? alpha * acc : 0 in place
+// of the sum with beta * C.  RS: the operands came through registers (for the choice of stores).
 template <class O, class Acc, int MF, bool BETA, bool FULL, int GRP, bool RS, class AccV, int NF>
 __device__ __forceinline__ void store_tile_staged(const ParamsOf<GRP> &p, int mbase, int nbase, int lane,
                                                   AccV (&acc)[NF][NF], uint8_t *stg) {
@@ -404,7 +404,7 @@ __device__ __forceinline__ void store_tile_staged(const ParamsOf<GRP> &p, int mb
     // single round, and with the 32x32 shape, the plain stores measured faster
     // Grouped: not where D's rows start off 64-byte lines and the sums are short, so that the stores
     // are most of the work: a line's two parts then reach memory one by one (31 gradients of 1032 x
-    // 5896 from 24 rows, fp32: streaming 296 us, plain 158; 3000 x 14728, 4 experts, 16 bits, K 128:
+    // 5896 from 24 rows, fp32: streaming 296 us, plain 154; 3000 x 14728, 4 experts, 16 bits, K 128:
     // 43 and 31, K 256: 49 and 41, K 512: 66 and 82; fp32 K 64: 60 and 51, K 256: 64 and 80).  Only
     // up to 32 for register-staged operands, whose loads need the caches more (10540 x 7800 x 121: 108 and
     // 124; 4 gradients of 4147 x 6298, fp32, 9 rows each 158 and 101, 32 rows 158 and 102).

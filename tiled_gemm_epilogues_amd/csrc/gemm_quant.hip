@@ -288,8 +288,8 @@ __device__ __forceinline__ void wait_all_loads() { asm volatile("s_waitcnt vmcnt
 // us, of which the launch 2.9; 16 rows, 16384 x 4096, block 64 with zero points, fp16 14.9 us (2.5 TB/s), bf16
 // 15.5; 32 rows over 32 experts (20 of them used) of 2048 x 4096, block 128, bf16 29.5, fp16 27.3.  4 or 16
 // waves and 32 columns measured no better, two chunks in flight slower (25.9 -> 32.5 for the last); 16
-// columns take one row of 4096 x 4096 from 8.6 to 5.8 us (more workgroups), 64 columns 16 rows of 16384 x
-// 4096 from 16.4 to 13.7 (A read less often; both with an earlier form of the conversion).
+// columns take one row of 4096 x 4096 from 10.6 to 6.4 us (more workgroups), 64 columns 16 rows of 16384 x
+// 4096 from 21.1 to 15.7 (A read less often).
 constexpr int WAVES = 8;
 
 template <class TI, class TO, int G, bool Z, int CG>

@@ -1,8 +1,8 @@
 // Products of few rows per expert on gfx950, any alignment and any K: 16 rows and 16 * CG columns
 // of one expert per workgroup.  Bound by the weights' bytes, each read once (twice 16 rows read
-// them twice, mostly from cache): 64 rows over 64 experts of 2048 x 4096 (bf16, B transposed; about 40
-// have rows) 128 us, 5.3 TB/s.  Few or small experts are bound by the launch (2.9 us) and
-// the latency of a wave's chunks, one after another: 8 rows over 16 experts of 1024 x 2048 8.5 us.
+// them twice, mostly from cache): 64 rows over 64 experts of 2048 x 4096 (bf16, B transposed; 38 have
+// rows) 109 us, 5.7 TB/s.  Few or small experts are bound by the launch (2.9 us) and the latency of a
+// wave's chunks, one after another: 8 rows over 16 experts of 1024 x 2048 7.2 us (cold 8.6).
 //
 // K is divided over the 8 waves of a workgroup (4 and 16 measured no better): with few rows a
 // workgroup per tile walks K too slowly (9 rows over 2 experts of 2745 x 6793: 93 us in 128-wide

@@ -1,6 +1,6 @@
 // C ABI of the products grouped by expert: plan creation and validation, kernel choice, launch.
-// Host code only; the kernels are the grouped instances of gemm_kernels.hip, gemm_fast.hip and
-// gemm_skinny.hip.
+// Host code only; the kernels are the grouped instances of gemm_kernels.hip and gemm_fast.hip, and
+// gemm_rows16.hip.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -20,8 +20,8 @@ struct gemm_grouped_plan {
     int64_t rows, M, N, K, groups;   // K unused by GROUP_K, M by GROUP_ROWS
     int64_t lda, ldb, ldc, stride_b, stride_bias, stride_c;
     int ab, cd, epi;
-    const GroupedEntry *any;         // general kernel (always valid)
-    const GroupedEntry *fast;        // aligned pointers: the fast or skinny kernel, else nullptr
+    const GroupedEntry *any;         // the kernel for any alignment: general, register-staged or for few rows
+    const GroupedEntry *fast;        // aligned pointers: the fast kernel with direct loads, else nullptr
     char desc[256];
 };
 
@@ -116,7 +116,8 @@ bool few_rows_pay(int64_t avg, double few) { return avg <= 6 || few <= 700; }
 // 4096 (448) 203 -> 171; but 5120 x 4096 x 4096 (320) 148 -> 158.
 bool rounds_full(int64_t wide_tiles) { return wide_tiles > 0 && 4 * wide_tiles >= 3 * 256 * ceil_div(wide_tiles, 256); }
 // Sums below 512 leave them mostly storing, which the other tiles overlap: 8192 x 8192 over 4, K 128, 41 ->
-// 54, K 256 58 -> 66, K 512 82 -> 89 (32768 x 8192 over 8: 161 -> 165, 216 -> 208, 338 -> 296).
+// 54, K 256 58 -> 66, K 512 82 -> 89 (32768 x 8192 over 8: 161 -> 165, 216 -> 208, 338 -> 296).  With the
+// gate, which reads C, 16384 x 8192 x 2048 over 16 683 -> 604 (614 -> 492 without it in the same run).
 bool wide_tiles_pay(int64_t rows, int64_t groups, int64_t n, int64_t avg, int64_t N, int64_t K) {
     if (avg < 512 || K < 512) return false;
     if (groups == 1) return rounds_full(ceil_div(rows, 256) * ceil_div(N, 256));
@@ -198,10 +199,11 @@ gemm_status_t gemm_grouped_plan_create(gemm_grouped_plan_t *out, const gemm_grou
     // direct loads: whole 16-byte chunks
     const bool fast_ok = eab == 2 && d->K >= FAST_MIN_K && d->lda % 8 == 0 && d->ldb % 8 == 0 &&
                          d->stride_b % 8 == 0 && (t || (d->N % 8 == 0 && d->N > 0)) && offsets_ok;
-    // 16 x 64 tiles where they give every CU a workgroup, else narrower ones: B transposed 16 x 16 (4097
-    // x 4097, one row, 16.5 -> 11.8 us, 2048 x 4096 10.1 -> 6.0; 200 rows over 8 experts, 1001 x 1001,
-    // 8.7 vs 11.3), else 16 x 32 (2048 x 4096, one row, 11.0 -> 9.2 us, 4097 x 4097 16.6 -> 12.8; 200 rows over
-    // 8 experts, 1001 x 1001, 8.2 vs 9.2)
+    // 16 x 64 tiles where they give every CU a workgroup, else narrower ones.  Operands cold (in the
+    // cache): B transposed 16 x 16 (4097 x 4097, one row, 24.7 -> 14.9 us (16.4 -> 12.0), 2048 x 4096 14.4 ->
+    // 8.4 (9.8 -> 6.0); 200 rows over 8 experts, 1001 x 1001, 11.4 vs 13.8 (8.6 vs 11.5)), else 16 x 32 (2048 x
+    // 4096, one row, 18.8 -> 17.1 us (10.9 -> 9.1), 4097 x 4097 23.9 -> 17.7 (16.6 -> 12.8); 200 rows over 8
+    // experts, 1001 x 1001, 11.4 vs 12.3 (8.4 vs 9.4))
     const auto rows16 = [&]() {
         p.any = rows16_table(ab, cd)(op_b, 4);
         if (grid_of(p, *p.any, false) < 256) p.any = rows16_table(ab, cd)(op_b, t ? 1 : 2);
