@@ -470,7 +470,7 @@ def exact(case, seed):
 
 def _define_act(name, z):
     return {"none": lambda: z, "relu": lambda: z * (z > 0),
-            "gelu": lambda: z * torch.special.ndtr(z),
+            "gelu": lambda: z / 2 * torch.erfc(z * -math.sqrt(0.5)),
             "gelu_tanh": lambda: z / 2 * (1 + torch.tanh(math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3))),
             "silu": lambda: z * torch.sigmoid(z)}[name]()
 
