@@ -262,13 +262,13 @@ def _own_norm(s):
 
 def _own_norm_grad(s):
     s["plan"].run_grad(s["dY"], s["X"], s["weight"], s["mean"], s["rstd"], s["dX"], s["dweight"], s["dbias"],
-                       s["C"], beta=1.0 if s["C"] is not None else 0.0, workspace=s["workspace"])
+                       s["C"], beta=1.0 if s["C"] is not None else 0.0, workspace=s.get("workspace"))
     return [s["dX"], s["dweight"], s["dbias"]]
 
 
 def _own_route(s):
     s["plan"].run(s["logits"], s["index"], s["weight"], s["order"], s["place"], s["offsets"], s["slope"],
-                  s["loss"], s["mask"], workspace=s["workspace"])
+                  s["loss"], s["mask"], workspace=s.get("workspace"))
     out = [s["index"], s["weight"], s["order"], s["place"], s["offsets"]]
     return out + [s["slope"], s["loss"]] if s["case"]["loss"] else out
 
