@@ -492,6 +492,200 @@ gemm_status_t gemm_quant_plan_destroy(gemm_quant_plan_t plan);
 /* The plan's kernel as text, like gemm_plan_describe. */
 gemm_status_t gemm_quant_plan_describe(gemm_quant_plan_t plan, char *buf, size_t len);
 
+/* ---- a layer's products: bias, activation, residual, and the gradient through them ------------
+ *
+ *   forward:   Z = alpha * A * op(B) + bias,  D = act(Z) + beta * C,  Z stored where asked for
+ *   gradient:  D = act'(Z) * alpha * A * op(B)
+ *
+ * for all rows and one matrix B, or, with groups > 1, for the row ranges that offsets give and one B
+ * (and bias) per expert, as in the products grouped by expert above.  A layer Y = act(X W1^T + b1) W2^T
+ * + b2 + R trains with a forward run that keeps Z and one with act NONE and C = R; the gradient run
+ * takes dY, W2 (op_b N) and Z, and gives what the gradient plans above take for W1 and b1.
+ *
+ *   GEMM_ACT_RELU       max(z, 0) (NaN stays NaN), slope 0 at 0
+ *   GEMM_ACT_GELU       z Phi(z), Phi the normal distribution function
+ *   GEMM_ACT_GELU_TANH  z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2
+ *   GEMM_ACT_SILU       z / (1 + e^-z)
+ * computed in fp32 from the accumulated sums (from the stored Z in the gradient) and rounded once.
+ * Their limits at infinities are those of the formulas taken as products (0 times infinity is NaN).
+ *
+ * Types, alignment, offsets and the absence of device memory are those of the grouped products;
+ * bias is fp32, C, D and Z have one type and layout.
+ */
+typedef enum {
+    GEMM_ACT_NONE = 0,
+    GEMM_ACT_RELU = 1,
+    GEMM_ACT_GELU = 2,
+    GEMM_ACT_GELU_TANH = 3,
+    GEMM_ACT_SILU = 4
+} gemm_act_t;
+
+typedef struct gemm_layer_plan *gemm_layer_plan_t;
+
+/* Fields as in gemm_grouped_desc_t; algo and tile too. */
+typedef struct {
+    int64_t rows, N, K, groups;
+    gemm_op_t op_b;
+    int64_t lda, ldb, ldc, stride_b, stride_bias;
+    gemm_dtype_t ab_type, cd_type;
+    gemm_act_t act;
+    gemm_algo_t algo;
+    int32_t tile;
+} gemm_layer_desc_t;
+
+/* Host-only.  Errors as gemm_grouped_plan_create's. */
+gemm_status_t gemm_layer_plan_create(gemm_layer_plan_t *out, const gemm_layer_desc_t *desc);
+
+/*
+ * Enqueues the forward product on `stream`: one kernel, no allocation, no synchronisation.  C is
+ * read when beta != 0 (C == D is allowed); Z: receives the activation's argument, NULL leaves it out
+ * (Z must be neither D nor a C that is read); bias: NULL is none; offsets may be NULL with groups == 1 (all
+ * rows).  Returns INVALID_VALUE for a NULL plan, a missing pointer, a pointer off its element's
+ * alignment or a NaN scalar; HIP_ERROR when the launch fails.
+ */
+gemm_status_t gemm_layer_run(gemm_layer_plan_t plan, const void *A, const void *B, const void *C, void *D,
+                             void *Z, const void *bias, const int32_t *offsets, float alpha, float beta,
+                             void *stream);
+
+/* Enqueues the gradient product: one kernel.  Z is read (not with GEMM_ACT_NONE, where it may be
+ * NULL); Z == D is allowed.  Errors as above. */
+gemm_status_t gemm_layer_grad_run(gemm_layer_plan_t plan, const void *A, const void *B, const void *Z, void *D,
+                                  const int32_t *offsets, float alpha, void *stream);
+
+/* Frees a plan (NULL is a no-op).  Always returns SUCCESS. */
+gemm_status_t gemm_layer_plan_destroy(gemm_layer_plan_t plan);
+
+/* The plan's kernel as text, like gemm_plan_describe. */
+gemm_status_t gemm_layer_plan_describe(gemm_layer_plan_t plan, char *buf, size_t len);
+
+/* ---- layer norm --------------------------------------------------------------------------------
+ *
+ *   forward:   Y = (X - m) r * weight + bias,  m = mean of the row, r = 1 / sqrt(mean of (X - m)^2 + eps)
+ *   gradient:  with h = (X - m) r and g = dY * weight, row by row
+ *              dX = r (g - mean(g) - h mean(g h)) + beta * C,
+ *              dweight = the sum of dY h over the rows, dbias = that of dY
+ *
+ * X and dX are rows x N with leading dimension ldx (C too), Y and dY with ldy; F32, F16 or BF16, all of
+ * one type.  weight, bias, dweight, dbias (N values) and mean, rstd (one per row) are fp32.  Statistics
+ * and sums are fp32 in a fixed order: equal inputs give equal bits.  No alignment beyond the
+ * elements' own is required.  A plan holds no device memory: the gradient's partial sums go to a
+ * workspace of the caller's, which one run uses at a time.
+ */
+typedef struct gemm_norm_plan *gemm_norm_plan_t;
+typedef struct {
+    int64_t rows, N, ldx, ldy;
+    gemm_dtype_t type;
+    float eps;
+} gemm_norm_desc_t;
+
+/*
+ * Host-only.  Returns INVALID_VALUE for a NULL argument, a negative size, a leading dimension below
+ * N, eps below 0, infinite or NaN, or an enum out of range; NOT_SUPPORTED for another type, rows of more than
+ * 64 KiB, more than 2^31 - 2^20 - 1 rows or a leading dimension of 2^31 or more; ALLOC_FAILED without host
+ * memory.
+ */
+gemm_status_t gemm_norm_plan_create(gemm_norm_plan_t *out, const gemm_norm_desc_t *desc);
+
+/* Bytes of workspace that gemm_norm_grad_run needs for dweight or dbias (at most 4 MiB per 1024
+ * columns). */
+gemm_status_t gemm_norm_workspace_bytes(gemm_norm_plan_t plan, size_t *bytes);
+
+/*
+ * Enqueues the forward pass on `stream`: one kernel.  weight NULL is 1, bias NULL is 0; mean, rstd:
+ * NULL leaves them out.  Y == X is allowed with ldy == ldx.  Returns INVALID_VALUE for a NULL plan, a missing
+ * pointer or one off its element's alignment; HIP_ERROR when the launch fails.
+ */
+gemm_status_t gemm_norm_run(gemm_norm_plan_t plan, const void *X, const float *weight, const float *bias, void *Y,
+                            float *mean, float *rstd, void *stream);
+
+/*
+ * Enqueues the gradient: one kernel, and one more when dweight or dbias is wanted (both are written, not
+ * added to; NULL leaves one out; without rows they are 0).  mean, rstd: those of the forward pass.  C
+ * is read when beta != 0; C == dX is allowed, and dX == dY with ldx == ldy.  workspace: 4-byte aligned, of
+ * at least gemm_norm_workspace_bytes (workspace_bytes says how many); not needed when both sums are
+ * left out.  Errors as above, a workspace too small and a NaN beta included.
+ */
+gemm_status_t gemm_norm_grad_run(gemm_norm_plan_t plan, const void *dY, const void *X, const float *weight,
+                                 const float *mean, const float *rstd, const void *C, void *dX, float *dweight,
+                                 float *dbias, float beta, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Frees a plan (NULL is a no-op).  Always returns SUCCESS. */
+gemm_status_t gemm_norm_plan_destroy(gemm_norm_plan_t plan);
+
+/* The plan's kernels as text, like gemm_plan_describe. */
+gemm_status_t gemm_norm_plan_describe(gemm_norm_plan_t plan, char *buf, size_t len);
+
+/* ---- routing of rows to experts ----------------------------------------------------------------
+ *
+ * From a router's logits (rows x experts, leading dimension ldl; F32, F16 or BF16), for every row t:
+ *   index[t][j]   the expert of the j-th largest logit, j < k; of equal logits the lowest expert's
+ *                 comes first
+ *   weight[t][j]  its probability under the softmax of the row's logits, with `normalize` divided by
+ *                 the sum of the k
+ * and over all rows the per-expert counts and the rows in the order of their experts:
+ *   offsets[e]    (experts + 1 values) the number of choices of experts below e: the offsets that the
+ *                 products grouped by expert take
+ *   order[i]      (rows * k) the i-th choice in the order of expert, row and j, as the number t * k + j;
+ *                 -1 from offsets[experts] on.  Row i of a sorted token buffer is row order[i] / k
+ *   place[t][j]   the inverse: where choice t * k + j stands in the order; -1 where it was not made
+ *   loss          (1 value) the balance loss E * sum over e of f_e P_e: f_e = choices of e / (k T'), P_e =
+ *                 the mean of e's probability over the T' rows in use
+ *   slope[e]      (experts values) E f_e / T', the loss's derivative by every row's probability of e
+ * Left out are rows whose mask is 0 and those without a logit above minus infinity: index and place
+ * -1, weight 0, no part in T'.  Logits that are minus infinity or NaN are never chosen (index and place
+ * -1, weight 0 where fewer than k are left); a NaN or plus infinity makes its row's weights and the loss
+ * NaN, as the softmax does.
+ *
+ *   gradient: dlogits = the derivative of  sum of dweight * weight + dloss * loss  by the logits,
+ * the choice and f held constant; 0 for rows left out.
+ *
+ * index, order, place, offsets are int32, mask one byte per row, the rest fp32.  Sums over rows have
+ * a fixed order: equal inputs give equal bits.  A plan holds no device memory: runs over many rows use a
+ * workspace of the caller's, one run at a time.
+ */
+typedef struct gemm_route_plan *gemm_route_plan_t;
+typedef struct {
+    int64_t rows, experts, k, ldl;
+    gemm_dtype_t type;
+    int32_t normalize;      /* 0 or 1 */
+} gemm_route_desc_t;
+
+/*
+ * Host-only.  Returns INVALID_VALUE for a NULL argument, a negative size, experts < 1, k outside 1 ..
+ * experts, ldl < experts, or an enum or flag out of range; NOT_SUPPORTED for another type, more than 1024
+ * experts, k above 16, rows * k above 2^31 - 2^20 - 1 or ldl of 2^31 or more; ALLOC_FAILED without host
+ * memory.
+ */
+gemm_status_t gemm_route_plan_create(gemm_route_plan_t *out, const gemm_route_desc_t *desc);
+
+/* Bytes of workspace that gemm_route_run needs (0 for few rows). */
+gemm_status_t gemm_route_workspace_bytes(gemm_route_plan_t plan, size_t *bytes);
+
+/*
+ * Enqueues the routing on `stream`: one kernel for few rows, else three.  mask, slope and loss: NULL
+ * leaves them out.  workspace: 4-byte aligned, of workspace_bytes >= gemm_route_workspace_bytes bytes.
+ * Returns INVALID_VALUE for a NULL plan, a missing pointer, one off its element's alignment or a
+ * workspace too small; HIP_ERROR when a launch fails.
+ */
+gemm_status_t gemm_route_run(gemm_route_plan_t plan, const void *logits, const uint8_t *mask, int32_t *index,
+                             float *weight, int32_t *order, int32_t *place, int32_t *offsets, float *slope,
+                             float *loss, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Enqueues the gradient: one kernel.  mask, index and slope: those of the forward run (an index outside
+ * 0 .. experts - 1 is skipped; a row's others are distinct).  dweight (rows x k) or dloss (1 value on the
+ * device): NULL is 0, and then index or slope may be NULL.  dlogits == logits is allowed.  Errors as above.
+ */
+gemm_status_t gemm_route_grad_run(gemm_route_plan_t plan, const void *logits, const uint8_t *mask,
+                                  const int32_t *index, const float *dweight, const float *slope,
+                                  const float *dloss, void *dlogits, void *stream);
+
+/* Frees a plan (NULL is a no-op).  Always returns SUCCESS. */
+gemm_status_t gemm_route_plan_destroy(gemm_route_plan_t plan);
+
+/* The plan's kernels as text, like gemm_plan_describe. */
+gemm_status_t gemm_route_plan_describe(gemm_route_plan_t plan, char *buf, size_t len);
+
 #ifdef __cplusplus
 }
 #endif

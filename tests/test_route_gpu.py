@@ -1,0 +1,334 @@
+"""The routing of rows to experts against a plain implementation in 64 bits: choice and ties, weights,
+order, offsets, balance loss, gradient; masks, rows without a choice, NaN and infinities; few rows (one
+launch) and many."""
+import numpy as np
+import pytest
+import torch
+
+import tiled_gemm_epilogues_amd as tge
+from grouped_helpers import TORCH_DT
+from layer_helpers import U, close, rounding
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+NAN, INF = float("nan"), float("inf")
+# every shape of lanes and experts per lane, whole and ragged
+EXPERTS = [1, 2, 7, 16, 17, 32, 33, 60, 64, 100, 128, 129, 160, 256, 257, 384, 512, 700, 1024]
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def reference(logits, k, mask=None):
+    """(index, order, place, offsets, p, rows in use): the definition, in 64 bits on the host."""
+    x = logits.double().numpy()
+    T, E = x.shape
+    on = np.ones(T, bool) if mask is None else mask.numpy() != 0
+    keys = np.where(np.isnan(x), -np.inf, x)
+    index = np.argsort(-keys, axis=1, kind="stable")[:, :k]
+    index = np.where(np.take_along_axis(keys, index, 1) == -np.inf, -1, index)
+    index[~on] = -1
+    used = on & (keys.max(1) > -np.inf)
+    flat = index.reshape(-1)
+    chosen = np.nonzero(flat >= 0)[0]
+    srt = chosen[np.argsort(flat[chosen], kind="stable")]
+    order, place = np.full(T * k, -1), np.full(T * k, -1)
+    order[:len(srt)] = srt
+    place[srt] = np.arange(len(srt))
+    offsets = np.concatenate([[0], np.cumsum(np.bincount(flat[chosen], minlength=E))])
+    p = torch.zeros(T, E, dtype=torch.float64)
+    p[used] = torch.softmax(torch.from_numpy(x[used]), 1)
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a).astype(np.int32))
+    return t(index), t(order), t(place.reshape(T, k)), t(offsets), p, torch.from_numpy(used)
+
+
+def weights64(index, p, normalize):
+    w = torch.gather(p, 1, index.long().clamp(min=0)) * (index >= 0)
+    if normalize:
+        s = w.sum(1, keepdim=True)
+        w = torch.where(s > 0, w / s, torch.zeros_like(w))
+    return w
+
+
+class Run:
+    def __init__(self, logits, k, type, normalize, mask=None, pad=0, loss=True):
+        T, E = logits.shape
+        self.plan = tge.RoutePlan(T, E, k, type=type, normalize=normalize, ldl=E + pad)
+        x = torch.full((T, E + pad), NAN, dtype=TORCH_DT[type], device=DEV)
+        x[:, :E] = logits.to(DEV)
+        self.logits, self.mask = x, None if mask is None else mask.to(DEV)
+        i = lambda *s: torch.full(s, 99, dtype=torch.int32, device=DEV)
+        f = lambda *s: torch.full(s, NAN, device=DEV)
+        self.index, self.weight, self.order, self.place, self.offsets = i(T, k), f(T, k), i(T * k), i(T, k), i(E + 1)
+        self.slope, self.loss = (f(E), f(1)) if loss else (None, None)
+        self.plan.run(self.logits, self.index, self.weight, self.order, self.place, self.offsets, self.slope,
+                      self.loss, self.mask)
+
+    def outputs(self):
+        return [t.cpu() for t in (self.index, self.weight, self.order, self.place, self.offsets)]
+
+
+def spread(logits):
+    """Roundings of a probability: its exponent (up to 3 times the distance from the row's largest
+    logit in U), the exponential's step, a sum of up to 1024, a quotient."""
+    x = logits.double()
+    top = torch.where(x.isfinite(), x, torch.zeros_like(x)).abs().max(1, keepdim=True)[0]
+    return (6 * top + 48) * U
+
+
+def check(logits, k, type, normalize, mask=None, pad=0):
+    T, E = logits.shape
+    r = Run(logits, k, type, normalize, mask, pad)
+    index, order, place, offsets, p, used = reference(logits, k, mask)
+    got = r.outputs()
+    assert torch.equal(got[0], index), "index"
+    assert torch.equal(got[4], offsets), "offsets"
+    assert torch.equal(got[2], order), "order"
+    assert torch.equal(got[3], place), "place"
+    w = weights64(index, p, normalize)
+    close(got[1], w, w * spread(logits) * (2 if normalize else 1) + 1e-37, "weight")
+    n = int(used.sum())
+    counts = (offsets[1:] - offsets[:-1]).double()
+    slope = counts * E / k / n / n if n else torch.zeros(E, dtype=torch.float64)
+    close(r.slope, slope, slope * 2 * U, "slope")
+    P = p.sum(0)
+    rel = spread(logits).max() + (min(T, 4096) + 64) * U
+    close(r.loss, (slope * P).sum().reshape(1), ((slope * P).sum() * rel + 1e-37).reshape(1), "loss")
+    return r, index, p, used, slope
+
+
+def logits_of(seed, T, E, type, ties=False):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, E, generator=g) * 2
+    return ((x * 2).round() / 2 if ties else x).to(TORCH_DT[type])
+
+
+@pytest.mark.parametrize("type", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("E", EXPERTS)
+def test_experts(E, type):
+    for T in (1, 40, 700):
+        for k in sorted({1, min(2, E), min(8, E), min(16, E)}):
+            check(logits_of(E + T, T, E, type), k, type, normalize=k > 1, pad=E % 3)
+    # many equal logits: the lowest experts come first
+    check(logits_of(E, 50, E, type, ties=True), min(5, E), type, normalize=False)
+
+
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 127, 128, 129, 130, 1023, 1025, 4000, 20000, 70001])
+def test_rows(T):
+    for E, k in ((8, 2), (64, 6), (160, 8)):
+        mask = (torch.rand(T, generator=torch.Generator().manual_seed(T)) < 0.8).to(torch.uint8)
+        check(logits_of(T, T, E, "f32"), k, "f32", True, mask)
+        check(logits_of(T, T, E, "bf16", ties=True), k, "bf16", False)
+
+
+def test_all_rows_choose_one_expert():
+    for T in (100, 3000):
+        x = torch.zeros(T, 64)
+        x[:, 41] = 5
+        r, index, _, _, _ = check(x, 1, "f32", False)
+        assert (index == 41).all() and torch.equal(r.order.cpu(), torch.arange(T, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("T", [30, 600])
+def test_rows_and_experts_left_out(T):
+    E, k = 24, 4
+    x = logits_of(5, T, E, "f32")
+    mask = torch.ones(T, dtype=torch.uint8)
+    mask[[0, 7, T - 1]] = 0
+    x[7], x[0, 3], x[T - 1] = NAN, INF, INF                 # in masked rows: without effect
+    x[2] = -INF                                             # nothing to choose
+    x[3, 1:] = -INF                                         # one choice
+    x[4, :22] = -INF                                        # two choices
+    x[:, 5] = -INF                                          # an expert that is off
+    x[9] = torch.finfo(torch.float32).min                   # the type's lowest value is a logit like others
+    r, index, p, used, slope = check(x, k, "f32", True, mask)
+    assert index[3].tolist() == [0, -1, -1, -1] and index[2].tolist() == [-1] * 4 and index[9].tolist() == [0, 1, 2, 3]
+    assert not (index == 5).any() or (index[9] == 5).any()
+    dw, dl = torch.randn(T, k, generator=torch.Generator().manual_seed(2)), torch.full((1,), 3.0)
+    out = torch.full_like(r.logits, NAN)
+    r.plan.run_grad(r.logits, r.index, dw.to(DEV), r.slope, dl.to(DEV), out, r.mask)
+    assert (out[[0, 7, T - 1, 2]] == 0).all() and out.isfinite().all()
+    assert (out[torch.isinf(r.logits) & (out == out)] == 0).all()
+    # nothing in use at all
+    none = torch.zeros(T, dtype=torch.uint8)
+    r = Run(x, k, "f32", True, none)
+    assert (r.index == -1).all() and (r.weight == 0).all() and (r.order == -1).all() and (r.place == -1).all()
+    assert (r.offsets == 0).all() and (r.slope == 0).all() and float(r.loss) == 0
+    r.plan.run_grad(r.logits, r.index, dw.to(DEV), r.slope, torch.full((1,), NAN, device=DEV), out, r.mask)
+    assert (out == 0).all()
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+def test_nan_and_infinities(normalize):
+    T, E, k = 40, 20, 3
+    x = logits_of(6, T, E, "f32")
+    x[1, 4], x[2, 0], x[3, 7] = NAN, INF, -INF
+    r = Run(x, k, "f32", normalize)
+    index, order, place, offsets, _, _ = reference(x, k)
+    got = r.outputs()
+    assert torch.equal(got[0], index) and torch.equal(got[2], order) and torch.equal(got[4], offsets)
+    assert 4 not in got[0][1].tolist() and got[0][2, 0] == 0
+    assert got[1][1].isnan().all() and got[1][2].isnan().all() and r.loss.isnan().all()
+    ok = torch.ones(T, dtype=torch.bool)
+    ok[[1, 2]] = False
+    assert got[1][ok].isfinite().all()
+
+
+def grad64(logits, index, dw, slope, dloss, normalize, used):
+    x = logits.double()
+    x = torch.where(used[:, None], x, torch.zeros_like(x)).requires_grad_()
+    p = torch.softmax(x, 1)
+    w = torch.gather(p, 1, index.long().clamp(min=0)) * (index >= 0)
+    if normalize:
+        w = w / w.sum(1, keepdim=True).clamp(min=1e-300)
+    total = ((w * dw.double()).sum(1)[used]).sum() + dloss * (p[used] * slope.double()).sum()
+    return torch.autograd.grad(total, x)[0], p.detach()
+
+
+@pytest.mark.parametrize("type", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("E", [1, 5, 16, 24, 64, 100, 128, 256, 300, 1024])
+def test_gradient(E, normalize, type):
+    for T in (3, 130, 1000):
+        k = min(E, 1 + T % 8)
+        x = logits_of(E * T, T, E, type)
+        mask = (torch.rand(T, generator=torch.Generator().manual_seed(T)) < 0.9).to(torch.uint8)
+        r, index, p, used, slope = check(x, k, type, normalize, mask, pad=T % 4)
+        g = torch.Generator().manual_seed(T + 1)
+        dw = torch.randn(T, k, generator=g)
+        slope32 = r.slope.cpu()
+        for give_w, dl in ((True, 0.7), (True, None), (False, 2.0), (False, None)):
+            out = torch.full_like(r.logits, NAN)
+            r.plan.run_grad(r.logits, r.index, dw.to(DEV) if give_w else None, r.slope,
+                            None if dl is None else torch.full((1,), dl, device=DEV), out, r.mask)
+            dl = dl or 0.0
+            dl32 = float(torch.tensor(dl, dtype=torch.float32))
+            zero = dw if give_w else torch.zeros_like(dw)
+            want, pr = grad64(x, index, zero, slope32, dl32, normalize, used)
+            # d = p (h - sum p h): p's roundings on both terms, a sum of up to 1024 and three more
+            h = torch.zeros(T, E, dtype=torch.float64).scatter_add_(1, index.long().clamp(min=0), zero.double().abs() * (index >= 0))
+            if normalize:
+                w = weights64(index, pr * used[:, None], True)
+                a = (w * zero.double().abs()).sum(1, keepdim=True)
+                ws = torch.zeros(T, E, dtype=torch.float64).scatter_add_(1, index.long().clamp(min=0), w * (index >= 0))
+                size = pr * (dl32 * (slope32.double() + (pr * slope32.double()).sum(1, keepdim=True))) + ws * (h + a)
+                # where an expert is not chosen the weights' part is 0, but the reference takes it as p times
+                # a sum of terms w (dw - a) that cancel, each rounded in 64 bits (2^-53, up to 8 times)
+                own = pr * 2 * a * 2.0 ** -50
+            else:
+                h = h + dl32 * slope32.double()
+                size = pr * (h + (pr * h).sum(1, keepdim=True))
+                own = 0.0
+            bound = size * spread(x) * 4 + own + 1e-37
+            bound = bound + rounding(want.abs() + bound, TORCH_DT[type]) * 1.0001
+            close(out[:, :E], want * used[:, None], bound, f"gradient {give_w} {dl}")
+            if r.logits.shape[1] > E:
+                assert out[:, E:].isnan().all()
+
+
+def test_gradient_against_differences():
+    # the loss as the kernel computes it, with f held: sum_e slope_e sum_t p_te from weights with k = E
+    T, E = 12, 6
+    x = logits_of(3, T, E, "f32")
+    r = Run(x, E, "f32", False)
+    slope = torch.rand(E, generator=torch.Generator().manual_seed(4))
+    dw = torch.randn(T, E, generator=torch.Generator().manual_seed(5))
+
+    def total(logits):
+        q = Run(logits, E, "f32", False)
+        w, idx = q.weight.cpu().double(), q.index.cpu().long()
+        p = torch.zeros(T, E, dtype=torch.float64).scatter_(1, idx, w)
+        by_first = torch.gather(p, 1, r.index.cpu().long())
+        return (by_first * dw.double()).sum(1) + 0.5 * (p * slope.double()).sum(1)
+    v = torch.randn(T, E, generator=torch.Generator().manual_seed(6))
+    h = 2.0 ** -7
+    diff = (total(x + h * v) - total(x - h * v)) / (2 * h)
+    out = torch.zeros_like(r.logits)
+    r.plan.run_grad(r.logits, r.index, dw.to(DEV), slope.to(DEV), torch.full((1,), 0.5, device=DEV), out)
+    got = (out.cpu().double() * v.double()).sum(1)
+    # third derivatives along v are below 8 times the largest |v|^3 |dw| here
+    scale = (dw.abs().max() + 1).double() * v.abs().max().double() ** 3
+    assert ((got - diff).abs() <= scale * (8 * h * h + 200 * U / h)).all()
+
+
+def test_in_place_gradient():
+    x = logits_of(8, 90, 40, "bf16")
+    r = Run(x, 4, "bf16", True)
+    dw = torch.randn(90, 4).to(DEV)
+    one = torch.ones(1, device=DEV)
+    a, b = torch.zeros_like(r.logits), r.logits.clone()
+    r.plan.run_grad(r.logits, r.index, dw, r.slope, one, a)
+    r.plan.run_grad(b, r.index, dw, r.slope, one, b)
+    assert torch.equal(a, b)
+
+
+def test_indices_outside_are_skipped():
+    x = logits_of(8, 10, 20, "f32")
+    r = Run(x, 2, "f32", False)
+    r.index[3, 0], r.index[4, 1], r.index[5, 0] = 20, -5, 2 ** 31 - 1
+    out = torch.zeros_like(r.logits)
+    r.plan.run_grad(r.logits, r.index, torch.ones(10, 2, device=DEV), r.slope, None, out)
+    assert out.isfinite().all()
+
+
+def test_no_rows():
+    plan = tge.RoutePlan(0, 9, 2)
+    i, f = torch.zeros(0, dtype=torch.int32, device=DEV), torch.zeros(0, device=DEV)
+    offsets = torch.full((10,), 7, dtype=torch.int32, device=DEV)
+    slope, loss = torch.full((9,), NAN, device=DEV), torch.full((1,), NAN, device=DEV)
+    plan.run(f, i, f, i, i, offsets, slope, loss)
+    assert (offsets == 0).all() and (slope == 0).all() and float(loss) == 0
+
+
+@pytest.mark.parametrize("T", [60, 5000])
+def test_runs_repeat_in_graphs_and_on_streams(T):
+    E, k = 96, 6
+    logits = [logits_of(s, T, E, "f32").to(DEV) for s in (1, 2, 3)]
+    x = logits[0].clone()
+    plan = tge.RoutePlan(T, E, k, normalize=True)
+    dw, dl = torch.randn(T, k).to(DEV), torch.ones(1, device=DEV)
+
+    def out():
+        i = lambda *s: torch.zeros(s, dtype=torch.int32, device=DEV)
+        f = lambda *s: torch.zeros(s, device=DEV)
+        return [i(T, k), f(T, k), i(T * k), i(T, k), i(E + 1), f(E), f(1), f(T, E)]
+
+    def step(o, ws=None, stream=None):
+        plan.run(x, *o[:7], workspace=ws, stream=stream)
+        plan.run_grad(x, o[0], dw, o[5], dl, o[7], stream=stream)
+    a, b = out(), out()
+    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=DEV)
+    step(a)
+    torch.cuda.synchronize()
+    graphs = []
+    for o, w in ((a, None), (b, ws)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(o, w)
+        graphs.append(g)
+    for turn in range(5):
+        x.copy_(logits[turn % 3])
+        for o in (a, b):
+            for t in o:
+                t.fill_(7)
+        for g in graphs:
+            g.replay()
+        want = out()
+        step(want)
+        torch.cuda.synchronize()
+        for o in (a, b):
+            for p, q in zip(o, want):
+                assert torch.equal(p, q)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs, wss = [out() for _ in streams], [torch.empty_like(ws) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, o, w in zip(streams, outs, wss):
+            step(o, w, s)
+    torch.cuda.synchronize()
+    for o in outs:
+        for p, q in zip(o, want):
+            assert torch.equal(p, q)

@@ -8,7 +8,9 @@ gemm_run_noalloc, gemm_plan_create_batched, gemm_plan_create_desc, gemm_plan_des
 gemm_status_string, gemm_plan_describe); `Plan` wraps them for torch tensors, whose device
 memory and streams are the only things taken from PyTorch.  `GroupedPlan` and `GroupedGradPlan`
 wrap the products grouped by expert (gemm_grouped_*) the same way, `QuantPlan` the products with
-4-bit weights (gemm_quant_*).
+4-bit weights (gemm_quant_*), `LayerPlan` a layer's products with activation and residual
+(gemm_layer_*), `NormPlan` layer norm (gemm_norm_*) and `RoutePlan` the routing of rows to experts
+(gemm_route_*).
 
 The library is loaded on first use, not at import, so that the build module of this package
 can run on a checkout that has no library yet.  There is no fallback: the first call fails with
@@ -27,6 +29,7 @@ DTYPE = {"f32": 0, "f16": 1, "bf16": 2, "i8": 3, "i32": 4, "cf16": 5, "cf32": 6,
 ELEM_BYTES = {"f32": 4, "f16": 2, "bf16": 2, "i8": 1, "i32": 4, "cf16": 4, "cf32": 8, "df16": 4,
               "df32": 8}
 EPILOGUE = {"none": 0, "relu": 1, "bias": 2, "bias_relu": 3, "gate": 4}
+ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 TRANSFORM = {"none": 0, "relu": 1, "from_f32": 2, "from_i8": 3}
 # stored element type of an operand whose load transform converts it to the input type
 STORED_BY_TRANSFORM = {"from_f32": "f32", "from_i8": "i8"}
@@ -43,7 +46,11 @@ EXPORTED = ("gemm_plan_create", "gemm_plan_create_batched", "gemm_plan_create_de
             "gemm_grouped_plan_create", "gemm_grouped_grad_plan_create", "gemm_grouped_run",
             "gemm_grouped_grad_run", "gemm_grouped_plan_destroy", "gemm_grouped_plan_describe",
             "gemm_quant_plan_create", "gemm_quant_run", "gemm_quant_plan_destroy",
-            "gemm_quant_plan_describe")
+            "gemm_quant_plan_describe", "gemm_layer_plan_create", "gemm_layer_run", "gemm_layer_grad_run",
+            "gemm_layer_plan_destroy", "gemm_layer_plan_describe", "gemm_norm_plan_create",
+            "gemm_norm_workspace_bytes", "gemm_norm_run", "gemm_norm_grad_run", "gemm_norm_plan_destroy",
+            "gemm_norm_plan_describe", "gemm_route_plan_create", "gemm_route_workspace_bytes",
+            "gemm_route_run", "gemm_route_grad_run", "gemm_route_plan_destroy", "gemm_route_plan_describe")
 
 _i64, _vp, _ci, _f = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
 
@@ -81,6 +88,25 @@ class QuantDesc(ctypes.Structure):
                 ("stride_s", _i64), ("stride_bias", _i64), ("ab_type", _ci), ("cd_type", _ci),
                 ("epilogue", _ci), ("zeros", ctypes.c_int32), ("algo", _ci),
                 ("tile", ctypes.c_int32)]
+
+
+class LayerDesc(ctypes.Structure):
+    """gemm_layer_desc_t of include/gemm.h."""
+    _fields_ = [("rows", _i64), ("N", _i64), ("K", _i64), ("groups", _i64), ("op_b", _ci),
+                ("lda", _i64), ("ldb", _i64), ("ldc", _i64), ("stride_b", _i64),
+                ("stride_bias", _i64), ("ab_type", _ci), ("cd_type", _ci), ("act", _ci),
+                ("algo", _ci), ("tile", ctypes.c_int32)]
+
+
+class NormDesc(ctypes.Structure):
+    """gemm_norm_desc_t of include/gemm.h."""
+    _fields_ = [("rows", _i64), ("N", _i64), ("ldx", _i64), ("ldy", _i64), ("type", _ci), ("eps", _f)]
+
+
+class RouteDesc(ctypes.Structure):
+    """gemm_route_desc_t of include/gemm.h."""
+    _fields_ = [("rows", _i64), ("experts", _i64), ("k", _i64), ("ldl", _i64), ("type", _ci),
+                ("normalize", ctypes.c_int32)]
 
 
 _lib = None
@@ -127,11 +153,23 @@ def lib():
     L.gemm_quant_run.argtypes = [_vp] * 9 + [_f, _f, _vp]
     L.gemm_quant_plan_destroy.argtypes = [_vp]
     L.gemm_quant_plan_describe.argtypes = [_vp, ctypes.c_char_p, ctypes.c_size_t]
-    for fn in ("gemm_grouped_plan_create", "gemm_grouped_grad_plan_create", "gemm_grouped_run",
-               "gemm_grouped_grad_run", "gemm_grouped_plan_destroy", "gemm_grouped_plan_describe",
-               "gemm_quant_plan_create", "gemm_quant_run", "gemm_quant_plan_destroy",
-               "gemm_quant_plan_describe"):
-        getattr(L, fn).restype = _ci
+    L.gemm_layer_plan_create.argtypes = [ctypes.POINTER(_vp), ctypes.POINTER(LayerDesc)]
+    L.gemm_layer_run.argtypes = [_vp] * 8 + [_f, _f, _vp]
+    L.gemm_layer_grad_run.argtypes = [_vp] * 6 + [_f, _vp]
+    L.gemm_norm_plan_create.argtypes = [ctypes.POINTER(_vp), ctypes.POINTER(NormDesc)]
+    L.gemm_norm_run.argtypes = [_vp] * 8
+    L.gemm_norm_grad_run.argtypes = [_vp] * 10 + [_f, _vp, ctypes.c_size_t, _vp]
+    L.gemm_route_plan_create.argtypes = [ctypes.POINTER(_vp), ctypes.POINTER(RouteDesc)]
+    L.gemm_route_run.argtypes = [_vp] * 11 + [ctypes.c_size_t, _vp]
+    L.gemm_route_grad_run.argtypes = [_vp] * 9
+    for kind in ("norm", "route"):
+        getattr(L, f"gemm_{kind}_workspace_bytes").argtypes = [_vp, ctypes.POINTER(ctypes.c_size_t)]
+    for kind in ("layer", "norm", "route"):
+        getattr(L, f"gemm_{kind}_plan_destroy").argtypes = [_vp]
+        getattr(L, f"gemm_{kind}_plan_describe").argtypes = [_vp, ctypes.c_char_p, ctypes.c_size_t]
+    for fn in EXPORTED:
+        if fn != "gemm_status_string":
+            getattr(L, fn).restype = _ci
     _lib = L
     return _lib
 
@@ -267,6 +305,108 @@ def gemm_quant_plan_destroy(plan):
 def gemm_quant_plan_describe(plan):
     buf = ctypes.create_string_buffer(256)
     st = lib().gemm_quant_plan_describe(plan, buf, 256)
+    return st, buf.value.decode()
+
+
+def gemm_layer_plan_create(rows, N, K, groups, op_b, lda, ldb, ldc, stride_b, stride_bias, ab_type,
+                           cd_type, act, algo="auto", tile=0):
+    """Returns (status, handle) of a plan for a layer's products."""
+    d = LayerDesc(rows, N, K, groups, _enum(OP, op_b), lda, ldb, ldc, stride_b, stride_bias,
+                  _enum(DTYPE, ab_type), _enum(DTYPE, cd_type), _enum(ACT, act), _enum(ALGO, algo), int(tile))
+    h = _vp()
+    st = lib().gemm_layer_plan_create(ctypes.byref(h), ctypes.byref(d))
+    return st, h.value
+
+
+def gemm_layer_run(plan, A, B, C, D, Z, bias, offsets, alpha, beta, stream):
+    """Raw pointers (ints or None) and a hipStream_t handle (int or None)."""
+    return lib().gemm_layer_run(plan, A, B, C, D, Z, bias, offsets, alpha, beta, stream)
+
+
+def gemm_layer_grad_run(plan, A, B, Z, D, offsets, alpha, stream):
+    """Raw pointers (ints or None) and a hipStream_t handle (int or None)."""
+    return lib().gemm_layer_grad_run(plan, A, B, Z, D, offsets, alpha, stream)
+
+
+def gemm_layer_plan_destroy(plan):
+    return lib().gemm_layer_plan_destroy(plan)
+
+
+def gemm_layer_plan_describe(plan):
+    buf = ctypes.create_string_buffer(256)
+    st = lib().gemm_layer_plan_describe(plan, buf, 256)
+    return st, buf.value.decode()
+
+
+def gemm_norm_plan_create(rows, N, ldx, ldy, type, eps):
+    """Returns (status, handle) of a layer norm plan."""
+    d = NormDesc(rows, N, ldx, ldy, _enum(DTYPE, type), eps)
+    h = _vp()
+    st = lib().gemm_norm_plan_create(ctypes.byref(h), ctypes.byref(d))
+    return st, h.value
+
+
+def gemm_norm_workspace_bytes(plan):
+    """Returns (status, bytes)."""
+    n = ctypes.c_size_t()
+    return lib().gemm_norm_workspace_bytes(plan, ctypes.byref(n)), n.value
+
+
+def gemm_norm_run(plan, X, weight, bias, Y, mean, rstd, stream):
+    """Raw pointers (ints or None) and a hipStream_t handle (int or None)."""
+    return lib().gemm_norm_run(plan, X, weight, bias, Y, mean, rstd, stream)
+
+
+def gemm_norm_grad_run(plan, dY, X, weight, mean, rstd, C, dX, dweight, dbias, beta, workspace,
+                       workspace_bytes, stream):
+    """Raw pointers (ints or None) and a hipStream_t handle (int or None)."""
+    return lib().gemm_norm_grad_run(plan, dY, X, weight, mean, rstd, C, dX, dweight, dbias, beta,
+                                    workspace, workspace_bytes, stream)
+
+
+def gemm_norm_plan_destroy(plan):
+    return lib().gemm_norm_plan_destroy(plan)
+
+
+def gemm_norm_plan_describe(plan):
+    buf = ctypes.create_string_buffer(256)
+    st = lib().gemm_norm_plan_describe(plan, buf, 256)
+    return st, buf.value.decode()
+
+
+def gemm_route_plan_create(rows, experts, k, ldl, type, normalize):
+    """Returns (status, handle) of a routing plan."""
+    d = RouteDesc(rows, experts, k, ldl, _enum(DTYPE, type), int(normalize))
+    h = _vp()
+    st = lib().gemm_route_plan_create(ctypes.byref(h), ctypes.byref(d))
+    return st, h.value
+
+
+def gemm_route_workspace_bytes(plan):
+    """Returns (status, bytes)."""
+    n = ctypes.c_size_t()
+    return lib().gemm_route_workspace_bytes(plan, ctypes.byref(n)), n.value
+
+
+def gemm_route_run(plan, logits, mask, index, weight, order, place, offsets, slope, loss, workspace,
+                   workspace_bytes, stream):
+    """Raw pointers (ints or None) and a hipStream_t handle (int or None)."""
+    return lib().gemm_route_run(plan, logits, mask, index, weight, order, place, offsets, slope, loss,
+                                workspace, workspace_bytes, stream)
+
+
+def gemm_route_grad_run(plan, logits, mask, index, dweight, slope, dloss, dlogits, stream):
+    """Raw pointers (ints or None) and a hipStream_t handle (int or None)."""
+    return lib().gemm_route_grad_run(plan, logits, mask, index, dweight, slope, dloss, dlogits, stream)
+
+
+def gemm_route_plan_destroy(plan):
+    return lib().gemm_route_plan_destroy(plan)
+
+
+def gemm_route_plan_describe(plan):
+    buf = ctypes.create_string_buffer(256)
+    st = lib().gemm_route_plan_describe(plan, buf, 256)
     return st, buf.value.decode()
 
 
@@ -682,3 +822,200 @@ class QuantPlan(_GroupedBase):
             ptr("offsets", offsets, dev), float(alpha), float(beta), self._stream(stream, dev))
         if st != STATUS_SUCCESS:
             raise GemmError(st, "gemm_quant_run")
+
+
+def _matrix(dtype, rows, cols, ld):
+    """The check of a rows x cols operand with leading dimension ld; one without columns has no rows
+    to check."""
+    return dtype, _span(rows, cols, ld), ld if cols > 0 else None
+
+
+class LayerPlan(_GroupedBase):
+    """A layer's products with bias, activation and residual (see include/gemm.h): Z = alpha * A *
+    op(B) + bias, D = act(Z) + beta * C, and the product that carries a gradient back through the
+    activation, D = act'(Z) * alpha * A * op(B).  act: "none", "relu", "gelu", "gelu_tanh" or "silu".
+    One matrix B for all rows, or with groups > 1 one (and a bias) per expert for the row ranges that
+    offsets give; B and bias as in GroupedPlan."""
+
+    _destroy, _describe = staticmethod(gemm_layer_plan_destroy), staticmethod(gemm_layer_plan_describe)
+
+    def __init__(self, rows, N, K, groups=1, op_b="T", lda=None, ldb=None, ldc=None, stride_b=None,
+                 stride_bias=None, ab="f16", cd="f16", act="none", algo="auto", tile=0):
+        import torch
+        self.rows, self.N, self.K, self.groups = rows, N, K, groups
+        self.op_b, self.ab, self.cd, self.act = op_b, ab, cd, act
+        b_rows, b_cols = (K, N) if op_b in ("N", 0) else (N, K)
+        self.lda = lda if lda is not None else max(1, K)
+        self.ldb = ldb if ldb is not None else max(1, b_cols)
+        self.ldc = ldc if ldc is not None else max(1, N)
+        self.stride_b = stride_b if stride_b is not None else b_rows * self.ldb
+        self.stride_bias = stride_bias if stride_bias is not None else N
+        st, h = gemm_layer_plan_create(rows, N, K, groups, op_b, self.lda, self.ldb, self.ldc,
+                                       self.stride_b, self.stride_bias, ab, cd, act, algo, tile)
+        if st != STATUS_SUCCESS:
+            raise GemmError(st, "gemm_layer_plan_create")
+        self._h = h
+        self._start(lib().gemm_layer_run)
+        self._grad = lib().gemm_layer_grad_run
+        tab, tcd = _torch_dtype(ab), _torch_dtype(cd)
+        b = _span(b_rows, b_cols, self.ldb)
+        cdn = _matrix(tcd, rows, N, self.ldc)
+        self._spec = {
+            "A": _matrix(tab, rows, K, self.lda),
+            "B": (tab, (groups - 1) * self.stride_b + b if b else 0, self.ldb if b else None),
+            "C": cdn, "D": cdn, "pre": cdn,
+            "bias": (torch.float32, (groups - 1) * self.stride_bias + N if N else 0, None),
+            "offsets": (torch.int32, groups + 1, None)}
+
+    def run(self, A, B, C, D, offsets=None, bias=None, pre=None, alpha=1.0, beta=0.0, stream=None):
+        """Enqueue the forward product on `stream` (as Plan.run).  C is read when beta != 0; bias: None
+        is none; pre: receives Z, for run_grad; offsets: as in GroupedPlan.run, None with one B for
+        all rows.  Rows of D and pre outside the ranges are left as they are.  Raises ValueError /
+        TypeError before anything is enqueued when a tensor does not fit the plan."""
+        dev = self._torch.cuda.current_device()
+        ptr = self._ptr
+        st = self._entry(
+            self._h, ptr("A", A, dev), ptr("B", B, dev), ptr("C", C, dev) if beta != 0 else None,
+            ptr("D", D, dev), ptr("pre", pre, dev), ptr("bias", bias, dev), ptr("offsets", offsets, dev),
+            float(alpha), float(beta), self._stream(stream, dev))
+        if st != STATUS_SUCCESS:
+            raise GemmError(st, "gemm_layer_run")
+
+    def run_grad(self, A, B, pre, D, offsets=None, alpha=1.0, stream=None):
+        """Enqueue the gradient product: D = act'(pre) * alpha * A * op(B), pre as run() left it (None
+        with act "none"; D may be pre itself)."""
+        dev = self._torch.cuda.current_device()
+        ptr = self._ptr
+        st = self._grad(
+            self._h, ptr("A", A, dev), ptr("B", B, dev), ptr("pre", pre, dev), ptr("D", D, dev),
+            ptr("offsets", offsets, dev), float(alpha), self._stream(stream, dev))
+        if st != STATUS_SUCCESS:
+            raise GemmError(st, "gemm_layer_grad_run")
+
+
+class _WorkspaceBase(_GroupedBase):
+    """Plans whose runs need a workspace of the caller's: `workspace_bytes` says how many bytes."""
+
+    def _workspace(self, workspace, needed, device):
+        """(pointer, bytes) of the given uint8 tensor, or of a new one from torch's allocator, which
+        lends its memory to the current stream (also inside a graph's capture)."""
+        if not needed:
+            return None, 0
+        if workspace is None:
+            workspace = self._torch.empty(self.workspace_bytes, dtype=self._torch.uint8, device=f"cuda:{device}")
+        return self._ptr("workspace", workspace, device), workspace.numel()
+
+    def _own_stream(self, workspace, needed, stream):
+        if needed and workspace is None and stream is not None:
+            raise ValueError("a run on a stream other than the current one needs a workspace of the caller's")
+
+
+class NormPlan(_WorkspaceBase):
+    """Layer norm over rows of N values and its gradients (see include/gemm.h): Y = (X - mean) * rstd *
+    weight + bias.  X, Y and their gradients have one type; weight, bias, mean, rstd, dweight and
+    dbias are fp32."""
+
+    _destroy, _describe = staticmethod(gemm_norm_plan_destroy), staticmethod(gemm_norm_plan_describe)
+
+    def __init__(self, rows, N, type="bf16", eps=1e-5, ldx=None, ldy=None):
+        import torch
+        self.rows, self.N, self.type, self.eps = rows, N, type, eps
+        self.ldx = ldx if ldx is not None else max(1, N)
+        self.ldy = ldy if ldy is not None else max(1, N)
+        st, h = gemm_norm_plan_create(rows, N, self.ldx, self.ldy, type, eps)
+        if st != STATUS_SUCCESS:
+            raise GemmError(st, "gemm_norm_plan_create")
+        self._h = h
+        self.workspace_bytes = gemm_norm_workspace_bytes(h)[1]
+        self._start(lib().gemm_norm_run)
+        self._grad = lib().gemm_norm_grad_run
+        t = _torch_dtype(type)
+        x, y = _matrix(t, rows, N, self.ldx), _matrix(t, rows, N, self.ldy)
+        cols, per_row = (torch.float32, N, None), (torch.float32, rows, None)
+        self._spec = {"X": x, "dX": x, "C": x, "Y": y, "dY": y, "weight": cols, "bias": cols, "dweight": cols,
+                      "dbias": cols, "mean": per_row, "rstd": per_row,
+                      "workspace": (torch.uint8, self.workspace_bytes, None)}
+
+    def run(self, X, weight, bias, Y, mean=None, rstd=None, stream=None):
+        """Enqueue the forward pass on `stream` (as Plan.run).  weight None is 1, bias None is 0; mean
+        and rstd receive what run_grad needs.  Y may be X itself."""
+        dev = self._torch.cuda.current_device()
+        ptr = self._ptr
+        st = self._entry(
+            self._h, ptr("X", X, dev), ptr("weight", weight, dev), ptr("bias", bias, dev), ptr("Y", Y, dev),
+            ptr("mean", mean, dev), ptr("rstd", rstd, dev), self._stream(stream, dev))
+        if st != STATUS_SUCCESS:
+            raise GemmError(st, "gemm_norm_run")
+
+    def run_grad(self, dY, X, weight, mean, rstd, dX, dweight=None, dbias=None, C=None, beta=0.0,
+                 workspace=None, stream=None):
+        """Enqueue the gradient: dX (+ beta * C, read when beta != 0; C may be dX itself), and where asked
+        for dweight and dbias, which are overwritten.  These need a workspace (uint8, at least
+        workspace_bytes, used by one run at a time); None takes one from torch's allocator for the
+        current stream."""
+        dev = self._torch.cuda.current_device()
+        ptr = self._ptr
+        sums = (dweight is not None or dbias is not None) and self.workspace_bytes > 0
+        self._own_stream(workspace, sums, stream)
+        args = (self._h, ptr("dY", dY, dev), ptr("X", X, dev), ptr("weight", weight, dev), ptr("mean", mean, dev),
+                ptr("rstd", rstd, dev), ptr("C", C, dev) if beta != 0 else None, ptr("dX", dX, dev),
+                ptr("dweight", dweight, dev), ptr("dbias", dbias, dev), float(beta))
+        st = self._grad(*args, *self._workspace(workspace, sums, dev), self._stream(stream, dev))
+        if st != STATUS_SUCCESS:
+            raise GemmError(st, "gemm_norm_grad_run")
+
+
+class RoutePlan(_WorkspaceBase):
+    """The routing of rows to experts from a router's logits (see include/gemm.h): the k largest of each
+    row with their softmax weights (divided by their sum with normalize), the offsets and the order
+    that the plans over row ranges take, the balance loss, and the gradient towards the logits."""
+
+    _destroy, _describe = staticmethod(gemm_route_plan_destroy), staticmethod(gemm_route_plan_describe)
+
+    def __init__(self, rows, experts, k, type="f32", normalize=False, ldl=None):
+        import torch
+        self.rows, self.experts, self.k, self.type, self.normalize = rows, experts, k, type, bool(normalize)
+        self.ldl = ldl if ldl is not None else experts
+        st, h = gemm_route_plan_create(rows, experts, k, self.ldl, type, self.normalize)
+        if st != STATUS_SUCCESS:
+            raise GemmError(st, "gemm_route_plan_create")
+        self._h = h
+        self.workspace_bytes = gemm_route_workspace_bytes(h)[1]
+        self._start(lib().gemm_route_run)
+        self._grad = lib().gemm_route_grad_run
+        logits = _matrix(_torch_dtype(type), rows, experts, self.ldl)
+        n = rows * k
+        ints, floats = (torch.int32, n, None), (torch.float32, n, None)
+        self._spec = {"logits": logits, "dlogits": logits, "index": ints, "place": ints, "order": ints,
+                      "weight": floats, "dweight": floats, "mask": (torch.uint8, rows, None),
+                      "offsets": (torch.int32, experts + 1, None), "slope": (torch.float32, experts, None),
+                      "loss": (torch.float32, 1, None), "dloss": (torch.float32, 1, None),
+                      "workspace": (torch.uint8, self.workspace_bytes, None)}
+
+    def run(self, logits, index, weight, order, place, offsets, slope=None, loss=None, mask=None,
+            workspace=None, stream=None):
+        """Enqueue the routing on `stream` (as Plan.run).  slope and loss: None leaves them out; mask:
+        uint8 per row, 0 leaves it out.  Many rows need a workspace (uint8, at least workspace_bytes,
+        used by one run at a time); None takes one from torch's allocator for the current stream."""
+        dev = self._torch.cuda.current_device()
+        ptr = self._ptr
+        self._own_stream(workspace, self.workspace_bytes, stream)
+        args = (self._h, ptr("logits", logits, dev), ptr("mask", mask, dev), ptr("index", index, dev),
+                ptr("weight", weight, dev), ptr("order", order, dev), ptr("place", place, dev),
+                ptr("offsets", offsets, dev), ptr("slope", slope, dev), ptr("loss", loss, dev))
+        st = self._entry(*args, *self._workspace(workspace, self.workspace_bytes, dev), self._stream(stream, dev))
+        if st != STATUS_SUCCESS:
+            raise GemmError(st, "gemm_route_run")
+
+    def run_grad(self, logits, index, dweight, slope, dloss, dlogits, mask=None, stream=None):
+        """Enqueue the gradient towards the logits from those of the weights (None: 0) and the loss (one
+        fp32 value on the device; None: 0), with index, slope and mask of the forward run.  dlogits may
+        be logits itself."""
+        dev = self._torch.cuda.current_device()
+        ptr = self._ptr
+        st = self._grad(
+            self._h, ptr("logits", logits, dev), ptr("mask", mask, dev), ptr("index", index, dev),
+            ptr("dweight", dweight, dev), ptr("slope", slope, dev), ptr("dloss", dloss, dev),
+            ptr("dlogits", dlogits, dev), self._stream(stream, dev))
+        if st != STATUS_SUCCESS:
+            raise GemmError(st, "gemm_route_grad_run")

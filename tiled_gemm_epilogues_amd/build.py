@@ -18,6 +18,7 @@ PAIRS = ["F32_F32", "F16_F16", "F16_F32", "BF16_BF16", "BF16_F32", "I8_I32"]
 FAST_PAIRS = ["F16_F16", "F16_F32", "BF16_BF16", "BF16_F32", "I8_I32"]
 SKINNY_PAIRS = ["F16_F16", "F16_F32", "BF16_BF16", "BF16_F32", "I8_I32"]
 GROUPED_PAIRS = ["F16_F16", "F16_F32", "BF16_BF16", "BF16_F32"]
+TYPES = ["F32", "F16", "BF16"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -54,9 +55,16 @@ def steps():
     for pair in GROUPED_PAIRS:
         for name in ("gemm_rows16", "gemm_quant"):
             add(name + ".hip", f"{name}_{pair.lower()}", f"-DTGE_PAIR_{pair}")
+    # the same kernels with a layer's epilogue
+    for name, pairs in (("gemm_kernels", GROUPED_PAIRS + ["F32_F32"]), ("gemm_fast", GROUPED_PAIRS)):
+        for pair in pairs:
+            add(name + ".hip", f"layer_{name}_{pair.lower()}", f"-DTGE_PAIR_{pair}", "-DTGE_LAYER")
+    for name in ("layer_norm", "route"):
+        for t in TYPES:
+            add(name + ".hip", f"{name}_{t.lower()}", f"-DTGE_TYPE_{t}")
     for name in ("gemm_complex", "gemm_diag", "gemm_repack"):
         add(name + ".hip", name)
-    for name in ("gemm_api", "grouped_api", "quant_api"):
+    for name in ("gemm_api", "grouped_api", "quant_api", "layer_api", "norm_api", "route_api"):
         add(name + ".cpp", name, host=True)
     return out
 

@@ -266,7 +266,8 @@ __device__ __forceinline__ void raster(int id, int tiles_m, int tiles_n, int gro
 // ---- groups ----------------------------------------------------------------------------------
 
 template <int GRP>
-using ParamsOf = typename std::conditional<GRP == GROUP_NONE, GemmParams, GroupedParams>::type;
+using ParamsOf = typename std::conditional<GRP == GROUP_NONE, GemmParams,
+                 typename std::conditional<GRP == GROUP_LAYER, LayerParams, GroupedParams>::type>::type;
 
 // A value that is the same in every lane, in scalar registers.
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
@@ -381,6 +382,30 @@ __device__ __forceinline__ bool select_rows(GroupedParams &p, int wg, int bm, in
     if (p.C) p.C = static_cast<const uint8_t *>(p.C) + row * p.ldc * ECD;
     p.D = static_cast<uint8_t *>(p.D) + row * p.ldc * ECD;
     if (p.bias) p.bias = static_cast<const uint8_t *>(p.bias) + e * p.stride_bias * 4;
+    return true;
+}
+
+// GROUP_LAYER: as GROUP_ROWS, Z moved with D; without offsets the tiles of one product.
+template <int EAB, int ECD>
+__device__ __forceinline__ bool select_layer(LayerParams &p, int wg, int bm, int &tn) {
+    int64_t moved;
+    if (p.offs) {
+        const uint8_t *d = static_cast<const uint8_t *>(p.D);
+        if (!select_rows<EAB, ECD>(p, wg, bm, tn)) return false;
+        moved = static_cast<const uint8_t *>(p.D) - d;
+    } else {
+        int tm;
+        raster(xcd_remap(wg, p.tiles_m * p.tiles_n), p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+        tm = __builtin_amdgcn_readfirstlane(tm);
+        tn = __builtin_amdgcn_readfirstlane(tn);
+        const int64_t row = (int64_t)tm * bm;
+        p.M = __builtin_amdgcn_readfirstlane(p.rows - (int)row);
+        p.A = static_cast<const uint8_t *>(p.A) + uniform64(row * p.lda * EAB);
+        moved = row * p.ldc * ECD;
+        if (p.C) p.C = static_cast<const uint8_t *>(p.C) + moved;
+        p.D = static_cast<uint8_t *>(p.D) + moved;
+    }
+    if (p.Z) p.Z = static_cast<uint8_t *>(p.Z) + moved;
     return true;
 }
 

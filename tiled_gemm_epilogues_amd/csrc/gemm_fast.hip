@@ -66,6 +66,7 @@
 
 #include "device_common.hpp"
 #include "gemm_internal.h"
+#include "layer_epilogue.hpp"
 
 namespace tge {
 namespace {
@@ -589,7 +590,7 @@ __global__ __launch_bounds__(NT, TL == 256 ? 1 : TL == 128 ? 2 : 4) void gemm_fa
     // two pipeline stages of both operands; after the main loop the stage-1 halves of A and B
     // (never used by the K tail) hold the four waves' epilogue staging buffers
     __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * G::OPND];
-    constexpr int STG = stg_bytes<TO, G::WT>();
+    constexpr int STG = GRP == GROUP_LAYER ? LayerStage<TO, G::WT>::BYTES : stg_bytes<TO, G::WT>();
     static_assert(2 * STG <= G::KC, "two staging buffers fit in one operand stage");
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -600,6 +601,8 @@ __global__ __launch_bounds__(NT, TL == 256 ? 1 : TL == 128 ? 2 : 4) void gemm_fa
     int lid = 0, gtm = 0, gtn = 0;
     if constexpr (GRP == GROUP_ROWS) {
         if (!select_rows<TI::E, (int)sizeof(typename TO::T)>(p, blockIdx.x, TL, gtn)) return;
+    } else if constexpr (GRP == GROUP_LAYER) {
+        if (!select_layer<TI::E, (int)sizeof(typename TO::T)>(p, blockIdx.x, TL, gtn)) return;
     } else if constexpr (GRP == GROUP_K) {
         using TS = typename std::conditional<std::is_same<TI, TF16>::value, _Float16, __bf16>::type;
         const int nc = colsum_blocks(p);
@@ -834,7 +837,13 @@ __global__ __launch_bounds__(NT, TL == 256 ? 1 : TL == 128 ? 2 : 4) void gemm_fa
     }
 
     // every wave's reads of the stage-1 buffers ended before the last slab's barrier
-    epilogue<TO, acc_t, MF, GRP, RS>(p, m0 + wm * G::WT, n0 + wn * G::WT, lane, acc, stg);
+    if constexpr (GRP == GROUP_LAYER) {
+        const int mb = m0 + wm * G::WT, nb = n0 + wn * G::WT;
+        if (mb + G::WT <= p.M && nb + G::WT <= p.N) store_layer_staged<TO, true>(p, mb, nb, lane, acc, stg);
+        else store_layer_staged<TO, false>(p, mb, nb, lane, acc, stg);
+    } else {
+        epilogue<TO, acc_t, MF, GRP, RS>(p, m0 + wm * G::WT, n0 + wn * G::WT, lane, acc, stg);
+    }
 }
 
 // MFMA shape of the fast path.  Both shapes give the same results (fp32/int32 accumulation of
@@ -942,9 +951,49 @@ const GroupedEntry *lookup_grouped(int mode, int op_b, int tile, int rs) {
     return tile == 256 ? &direct[layout][0] : tile == 128 ? &direct[layout][1] : tile == 64 ? &direct[layout][2] : nullptr;
 }
 
+// ---- a layer's instances -------------------------------------------------------------------------
+
+template <class TI, class TO, int TL, bool BT, bool RS>
+hipError_t launch_layer(const LayerParams &p, unsigned grid, hipStream_t s) {
+    hipLaunchKernelGGL((gemm_fast<TI, TO, true, BT, 16, false, RS, TL, GROUP_LAYER>), dim3(grid), dim3(NT), 0, s, p);
+    return hipGetLastError();
+}
+
+template <class TI, class TO>
+const LayerEntry *lookup_layer(int op_b, int tile, int rs) {
+    // [op_b][tile 256, 128, 64]; register-staged [op_b][128, 64]
+    static const LayerEntry direct[2][3] = {
+        {{launch_layer<TI, TO, 256, false, false>, 256, 256, "gemm_fast_256x256"},
+         {launch_layer<TI, TO, 128, false, false>, 128, 128, "gemm_fast_128x128"},
+         {launch_layer<TI, TO, 64, false, false>, 64, 64, "gemm_fast_64x64"}},
+        {{launch_layer<TI, TO, 256, true, false>, 256, 256, "gemm_fast_256x256"},
+         {launch_layer<TI, TO, 128, true, false>, 128, 128, "gemm_fast_128x128"},
+         {launch_layer<TI, TO, 64, true, false>, 64, 64, "gemm_fast_64x64"}}};
+    static const LayerEntry staged[2][2] = {
+        {{launch_layer<TI, TO, 128, false, true>, 128, 128, "gemm_fast_128x128_rs"},
+         {launch_layer<TI, TO, 64, false, true>, 64, 64, "gemm_fast_64x64_rs"}},
+        {{launch_layer<TI, TO, 128, true, true>, 128, 128, "gemm_fast_128x128_rs"},
+         {launch_layer<TI, TO, 64, true, true>, 64, 64, "gemm_fast_64x64_rs"}}};
+    if (op_b < 0 || op_b > 1) return nullptr;
+    if (rs) return tile == 128 ? &staged[op_b][0] : tile == 64 ? &staged[op_b][1] : nullptr;
+    return tile == 256 ? &direct[op_b][0] : tile == 128 ? &direct[op_b][1] : tile == 64 ? &direct[op_b][2] : nullptr;
+}
+
 }  // namespace
 
-#if defined(TGE_GROUPED)
+#if defined(TGE_LAYER)
+#if defined(TGE_PAIR_F16_F16)
+const LayerEntry *layer_fast_f16_f16(int b, int t, int rs) { return lookup_layer<TF16, OF16>(b, t, rs); }
+#elif defined(TGE_PAIR_F16_F32)
+const LayerEntry *layer_fast_f16_f32(int b, int t, int rs) { return lookup_layer<TF16, OF32>(b, t, rs); }
+#elif defined(TGE_PAIR_BF16_BF16)
+const LayerEntry *layer_fast_bf16_bf16(int b, int t, int rs) { return lookup_layer<TBF16, OBF16>(b, t, rs); }
+#elif defined(TGE_PAIR_BF16_F32)
+const LayerEntry *layer_fast_bf16_f32(int b, int t, int rs) { return lookup_layer<TBF16, OF32>(b, t, rs); }
+#else
+#error "define one TGE_PAIR_* macro of a 16-bit float type"
+#endif
+#elif defined(TGE_GROUPED)
 // the grouped instances are a build of their own (one object per type pair)
 #if defined(TGE_PAIR_F16_F16)
 const GroupedEntry *grouped_fast_f16_f16(int m, int b, int t, int rs) { return lookup_grouped<TF16, OF16>(m, b, t, rs); }

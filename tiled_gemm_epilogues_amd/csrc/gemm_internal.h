@@ -41,7 +41,9 @@ using LaunchFn = hipError_t (*)(const GemmParams &, unsigned grid, hipStream_t);
 //               transposed, B not): product e sums over range e into D + e * stride_c; K is set
 //               per workgroup
 // A range is clamped to [0, rows], so that no offset makes a kernel leave the operands.
-enum GroupMode { GROUP_NONE = 0, GROUP_ROWS = 1, GROUP_K = 2 };
+//   GROUP_LAYER as GROUP_ROWS, with a layer's epilogue (LayerParams); without offsets all rows are
+//               one range
+enum GroupMode { GROUP_NONE = 0, GROUP_ROWS = 1, GROUP_K = 2, GROUP_LAYER = 3 };
 constexpr int COLSUM_COLS = 64;   // columns of a workgroup that sums B (gradient plans)
 struct GroupedParams : GemmParams {
     const int32_t *offs;
@@ -52,6 +54,22 @@ struct GroupedParams : GemmParams {
 using GroupedLaunchFn = hipError_t (*)(const GroupedParams &, unsigned grid, hipStream_t);
 struct GroupedEntry {
     GroupedLaunchFn launch;
+    int bm, bn;              // workgroup tile
+    const char *name;
+};
+
+// One launch of a layer's products (GROUP_LAYER).  Forward: z = alpha * product + bias, D = act(z) +
+// beta * C (C read where has_beta is set), z written to Z where it is not nullptr.  grad: D =
+// act'(Z) * alpha * product, Z read.  Z is laid out like D.
+enum ActKind { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
+struct LayerParams : GroupedParams {
+    void *Z;
+    int act, grad;
+    int stream;              // stores past the caches
+};
+using LayerLaunchFn = hipError_t (*)(const LayerParams &, unsigned grid, hipStream_t);
+struct LayerEntry {
+    LayerLaunchFn launch;
     int bm, bn;              // workgroup tile
     const char *name;
 };
@@ -216,6 +234,21 @@ const GroupedEntry *grouped_rows16_f16_f32(int op_b, int cg);
 const GroupedEntry *grouped_rows16_bf16_bf16(int op_b, int cg);
 const GroupedEntry *grouped_rows16_bf16_f32(int op_b, int cg);
 
+// A layer's products: the kernels of GROUP_ROWS, under the same preconditions.
+const LayerEntry *layer_any_f32_f32(int op_b, int cfg);
+const LayerEntry *layer_any_f16_f16(int op_b, int cfg);
+const LayerEntry *layer_any_f16_f32(int op_b, int cfg);
+const LayerEntry *layer_any_bf16_bf16(int op_b, int cfg);
+const LayerEntry *layer_any_bf16_f32(int op_b, int cfg);
+const LayerEntry *layer_fast_f16_f16(int op_b, int tile, int rs);
+const LayerEntry *layer_fast_f16_f32(int op_b, int tile, int rs);
+const LayerEntry *layer_fast_bf16_bf16(int op_b, int tile, int rs);
+const LayerEntry *layer_fast_bf16_f32(int op_b, int tile, int rs);
+const LayerEntry *layer_rows16_f16_f16(int op_b, int cg);
+const LayerEntry *layer_rows16_f16_f32(int op_b, int cg);
+const LayerEntry *layer_rows16_bf16_bf16(int op_b, int cg);
+const LayerEntry *layer_rows16_bf16_f32(int op_b, int cg);
+
 // Products with 4-bit weights (gemm_quant.hip): W_e[n][k] = scale * (code - zero), codes packed
 // two per byte along k (low half: even k), one scale (of A's type) and zero point (uint8; nullptr:
 // 8) per `block` consecutive k.  offs == nullptr: one weight matrix for all rows.
@@ -245,5 +278,81 @@ const QuantEntry *quant_tile_f16_f16(int block);
 const QuantEntry *quant_tile_f16_f32(int block);
 const QuantEntry *quant_tile_bf16_bf16(int block);
 const QuantEntry *quant_tile_bf16_f32(int block);
+
+// Layer norm (layer_norm.hip).  A row belongs to a team of `waves` waves, whose lanes hold 16-byte
+// chunks lane, lane + 64 * waves, ... (`chunks` of them) of it; N elements fill at most the team's
+// chunks.  Workgroups have `teams` teams and take rows blockIdx * teams + team, then every
+// grid * teams-th.  Pointers need their elements' alignment only.
+struct NormParams {
+    const void *X;           // rows x N, ldx
+    const float *weight, *bias;      // nullptr: 1 and 0
+    void *Y;                 // rows x N, ldy (gradient: dY, read)
+    float *mean, *rstd;      // one per row; forward: nullptr leaves them out
+    const void *C;           // gradient: dX = ... + beta * C (read where has_beta is set), ldx
+    void *dX;                // ldx
+    float *part;             // gradient: grid x 2 x N partial sums (weight's, bias's); nullptr: none
+    int rows, N, ldx, ldy;
+    float eps, rn;           // 1 / N
+    float beta;
+    int has_beta;
+};
+struct NormShape {
+    int waves, chunks, teams;
+};
+// Teams of a workgroup, which so has 4 waves, or 8 in the gradient, unless one row needs more.
+constexpr int norm_teams(int waves, bool grad) { return waves < (grad ? 8 : 4) ? (grad ? 8 : 4) / waves : 1; }
+// The team of a row of `units` (1 to 64) KiB: one chunk per lane, or two, in as few waves as hold it; more
+// than two (of 16 waves) for the longest rows only, as they cost the registers that keep the next
+// row on its way.
+inline NormShape norm_shape(int64_t units, bool grad) {
+    int waves = 1, chunks = units <= 1 ? 1 : 2;
+    while (waves * chunks < units && waves < 16) waves = waves < 4 ? waves + 1 : waves % 3 ? waves / 2 * 3 : waves / 3 * 4;
+    while (waves * chunks < units) ++chunks;
+    return {waves, chunks, norm_teams(waves, grad)};
+}
+constexpr int NORM_SUM_COLS = 32;    // columns of a workgroup that joins partial sums
+hipError_t norm_forward_f32(const NormParams &p, NormShape s, unsigned grid, hipStream_t stream);
+hipError_t norm_forward_f16(const NormParams &p, NormShape s, unsigned grid, hipStream_t stream);
+hipError_t norm_forward_bf16(const NormParams &p, NormShape s, unsigned grid, hipStream_t stream);
+hipError_t norm_grad_f32(const NormParams &p, NormShape s, unsigned grid, hipStream_t stream);
+hipError_t norm_grad_f16(const NormParams &p, NormShape s, unsigned grid, hipStream_t stream);
+hipError_t norm_grad_bf16(const NormParams &p, NormShape s, unsigned grid, hipStream_t stream);
+// dweight[j] (dbias[j]) = the sum of `count` partial sums; nullptr: left out.
+hipError_t norm_join(const float *part, int count, int N, float *dweight, float *dbias, hipStream_t stream);
+
+// Routing of rows to experts (route.hip).  A row belongs to `lanes` lanes (16, 32 or 64) of a wave
+// with `per` consecutive experts each (lanes * per >= experts).  Workgroup b takes rows b *
+// block_rows .. + block_rows - 1.
+constexpr int ROUTE_MAX_K = 16, ROUTE_MAX_EXPERTS = 1024;
+struct RouteParams {
+    const void *logits;      // rows x experts, ldl
+    const uint8_t *mask;     // one per row, 0: left out; nullptr: none is
+    int32_t *index;          // rows x k (gradient: read)
+    float *weight;           // rows x k
+    int32_t *order, *place;  // rows * k
+    int32_t *offsets;        // experts + 1
+    float *slope, *loss;     // experts, 1; nullptr: left out
+    // gradient
+    const float *dweight, *dloss;    // rows x k; 1 (nullptr: 0)
+    void *dlogits;           // ldl
+    // workspace, blocks workgroups: choices per expert and used rows (blocks x (experts + 1)), summed
+    // probabilities (blocks x experts), and their totals
+    int32_t *hist, *total;
+    float *psum, *ptotal;
+    int rows, experts, k, ldl, normalize;
+    int block_rows, blocks;
+};
+struct RouteShape {
+    int lanes, per;
+};
+// Choice, weights and the workgroups' sums; with one workgroup everything.
+hipError_t route_choose_f32(const RouteParams &p, RouteShape s, hipStream_t stream);
+hipError_t route_choose_f16(const RouteParams &p, RouteShape s, hipStream_t stream);
+hipError_t route_choose_bf16(const RouteParams &p, RouteShape s, hipStream_t stream);
+// The rest for several workgroups: running sums over them, then order, place, offsets, slope, loss.
+hipError_t route_place(const RouteParams &p, hipStream_t stream);
+hipError_t route_grad_f32(const RouteParams &p, RouteShape s, unsigned grid, hipStream_t stream);
+hipError_t route_grad_f16(const RouteParams &p, RouteShape s, unsigned grid, hipStream_t stream);
+hipError_t route_grad_bf16(const RouteParams &p, RouteShape s, unsigned grid, hipStream_t stream);
 
 }  // namespace tge

@@ -33,6 +33,7 @@
 
 #include "device_common.hpp"
 #include "gemm_internal.h"
+#include "layer_epilogue.hpp"
 
 namespace tge {
 namespace {
@@ -162,6 +163,8 @@ __global__ __launch_bounds__(WGM * WGN * 64, 1) void gemm_mfma(ParamsOf<GRP> p) 
     int tile_m = 0, tile_n;
     if constexpr (GRP == GROUP_ROWS) {
         if (!select_rows<TI::E, (int)sizeof(typename TO::T)>(p, blockIdx.x, BM, tile_n)) return;
+    } else if constexpr (GRP == GROUP_LAYER) {
+        if (!select_layer<TI::E, (int)sizeof(typename TO::T)>(p, blockIdx.x, BM, tile_n)) return;
     } else if constexpr (GRP == GROUP_K) {
         static_assert(NT == 256 && STAGE >= 256 * 8 * 4, "column sums: 256 threads and their LDS");
         using TS = typename std::conditional<std::is_same<TI, TF16>::value, _Float16,
@@ -242,7 +245,8 @@ __global__ __launch_bounds__(WGM * WGN * 64, 1) void gemm_mfma(ParamsOf<GRP> p) 
         __syncthreads();
     }
 
-    if constexpr (GRP == GROUP_ROWS) store_tile<TO, acc_t>(p, m0 + wm * WTM, n0 + wn * WTN, lane, acc, p.gate);
+    if constexpr (GRP == GROUP_LAYER) store_layer_tile<TO>(p, m0 + wm * WTM, n0 + wn * WTN, lane, acc);
+    else if constexpr (GRP == GROUP_ROWS) store_tile<TO, acc_t>(p, m0 + wm * WTM, n0 + wn * WTN, lane, acc, p.gate);
     else store_tile<TO, acc_t>(p, m0 + wm * WTM, n0 + wn * WTN, lane, acc);
 }
 
@@ -303,9 +307,41 @@ const GroupedEntry *lookup_grouped(int mode, int op_b, int cfg) {
     return nullptr;
 }
 
+// ---- a layer's instances: 128- and 64-wide tiles, any alignment --------------------------------
+
+template <int BM, class TI, class TO, bool BT>
+hipError_t launch_layer(const LayerParams &p, unsigned grid, hipStream_t s) {
+    hipLaunchKernelGGL((gemm_mfma<BM, BM, 2, 2, TI, TO, false, BT, GROUP_LAYER>), dim3(grid), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+template <class TI, class TO>
+const LayerEntry *lookup_layer(int op_b, int cfg) {
+    static const LayerEntry e[2][2] = {{{launch_layer<128, TI, TO, false>, 128, 128, "gemm_mfma_128x128"},
+                                        {launch_layer<64, TI, TO, false>, 64, 64, "gemm_mfma_64x64"}},
+                                       {{launch_layer<128, TI, TO, true>, 128, 128, "gemm_mfma_128x128"},
+                                        {launch_layer<64, TI, TO, true>, 64, 64, "gemm_mfma_64x64"}}};
+    if (op_b < 0 || op_b > 1 || (cfg != CFG_128 && cfg != CFG_64)) return nullptr;
+    return &e[op_b][cfg == CFG_128 ? 0 : 1];
+}
+
 }  // namespace
 
-#if defined(TGE_GROUPED)
+#if defined(TGE_LAYER)
+#if defined(TGE_PAIR_F32_F32)
+const LayerEntry *layer_any_f32_f32(int b, int c) { return lookup_layer<TF32, OF32>(b, c); }
+#elif defined(TGE_PAIR_F16_F16)
+const LayerEntry *layer_any_f16_f16(int b, int c) { return lookup_layer<TF16, OF16>(b, c); }
+#elif defined(TGE_PAIR_F16_F32)
+const LayerEntry *layer_any_f16_f32(int b, int c) { return lookup_layer<TF16, OF32>(b, c); }
+#elif defined(TGE_PAIR_BF16_BF16)
+const LayerEntry *layer_any_bf16_bf16(int b, int c) { return lookup_layer<TBF16, OBF16>(b, c); }
+#elif defined(TGE_PAIR_BF16_F32)
+const LayerEntry *layer_any_bf16_f32(int b, int c) { return lookup_layer<TBF16, OF32>(b, c); }
+#else
+#error "define one TGE_PAIR_* macro of a float type"
+#endif
+#elif defined(TGE_GROUPED)
 // the grouped instances are a build of their own (one object per type pair)
 #if defined(TGE_PAIR_F32_F32)
 const GroupedEntry *grouped_any_f32_f32(int m, int b, int c) { return lookup_grouped<TF32, OF32>(m, b, c); }

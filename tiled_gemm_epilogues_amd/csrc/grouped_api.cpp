@@ -98,32 +98,6 @@ gemm_status_t launch(const gemm_grouped_plan &p, const void *A, const void *B, c
                                                                                 : GEMM_STATUS_HIP_ERROR;
 }
 
-// Whether the kernel for few rows (16 rows per workgroup, K split over its waves) beats the tiles,
-// which waste most of a tile but move more weights per workgroup: for a few rows per expert, and as
-// long as its 16 x 64 workgroups (`few`) are about one round.  Measured (bf16, B not transposed, N 2048,
-// K 4096; few rows -> best tile): 1 row per expert, 64 experts, 107 vs 146 us; 1 expert, 128 rows (272
-// workgroups) 13 vs 30; 8 experts, 256 rows (640) 35 vs 44, 512 (1152) 49 vs 46, 1024 (2176) 81 vs 50;
-// 64 experts, 512 rows (2048) 196 vs 193, 2048 (5120) 254 vs 200.
-bool few_rows_pay(int64_t avg, double few) { return avg <= 6 || few <= 700; }
-
-// Whether the 256-wide tiles (one workgroup per CU) beat the 128-wide ones (two): with rows enough
-// to fill them and a few rounds of them.  Measured (bf16, B not transposed; 128 -> 256): 8192 x 4096
-// x 4096 over 8 experts 310 -> 275 us, 4096 x 14336 x 4096 over 8 562 -> 490, 16384 x 8192 x 2048
-// over 16 592 -> 475, 32768 x 2048 x 1024 over 64 189 -> 182; but 8192 x 2048 x 4096 over 16 even
-// and 2048 x 8192 x 2048 over 2 75 -> 87.
-// With one expert the number of tiles is known, and what counts is that the last round is nearly
-// full: 4096 x 4096 x 4096 (256 tiles) 111 -> 96, 6144 x 2048 x 4096 (192) 97 -> 83, 7168 x 4096 x
-// 4096 (448) 203 -> 171; but 5120 x 4096 x 4096 (320) 148 -> 158.
-bool rounds_full(int64_t wide_tiles) { return wide_tiles > 0 && 4 * wide_tiles >= 3 * 256 * ceil_div(wide_tiles, 256); }
-// Sums below 512 leave them mostly storing, which the other tiles overlap: 8192 x 8192 over 4, K 128, 41 ->
-// 54, K 256 58 -> 66, K 512 82 -> 89 (32768 x 8192 over 8: 161 -> 165, 216 -> 208, 338 -> 296).  With the
-// gate, which reads C, 16384 x 8192 x 2048 over 16 683 -> 604 (614 -> 492 without it in the same run).
-bool wide_tiles_pay(int64_t rows, int64_t groups, int64_t n, int64_t avg, int64_t N, int64_t K) {
-    if (avg < 512 || K < 512) return false;
-    if (groups == 1) return rounds_full(ceil_div(rows, 256) * ceil_div(N, 256));
-    return ((double)rows / 256 + 0.5 * (double)n) * (double)ceil_div(N, 256) >= 384;
-}
-
 // Hands a finished plan out, with its description.
 gemm_status_t finish_plan(gemm_grouped_plan_t *out, const gemm_grouped_plan &p, const char *what) {
     const GroupedEntry *k = p.fast ? p.fast : p.any;

@@ -1,0 +1,245 @@
+// C ABI of a layer's products (bias, activation, residual; the gradient through the activation): plan
+// creation and validation, kernel choice, launch.  Host code only; the kernels are the layer
+// instances of gemm_kernels.hip, gemm_fast.hip and gemm_rows16.hip.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <stdio.h>
+
+#include <new>
+
+#include "../../include/gemm.h"
+#include "gemm_internal.h"
+#include "host_common.h"
+
+using namespace tge::host;
+using tge::LayerEntry;
+using tge::LayerParams;
+
+struct gemm_layer_plan {
+    int64_t rows, N, K, groups;
+    int64_t lda, ldb, ldc, stride_b, stride_bias;
+    int ab, cd, act;
+    const LayerEntry *any;           // the kernel for any alignment: general, register-staged or for few rows
+    const LayerEntry *fast;          // aligned pointers: the fast kernel with direct loads, else nullptr
+    char desc[256];
+};
+
+namespace {
+
+constexpr int64_t FAST_MIN_K = 64;         // one slab of the fast kernel (16-bit inputs)
+
+using TableFn = const LayerEntry *(*)(int, int);
+using FastFn = const LayerEntry *(*)(int, int, int);
+
+TableFn any_table(int ab, int cd) {
+    if (ab == GEMM_F32 && cd == GEMM_F32) return tge::layer_any_f32_f32;
+    if (ab == GEMM_F16 && cd == GEMM_F16) return tge::layer_any_f16_f16;
+    if (ab == GEMM_F16 && cd == GEMM_F32) return tge::layer_any_f16_f32;
+    if (ab == GEMM_BF16 && cd == GEMM_BF16) return tge::layer_any_bf16_bf16;
+    if (ab == GEMM_BF16 && cd == GEMM_F32) return tge::layer_any_bf16_f32;
+    return nullptr;
+}
+
+// The tables of the 16-bit kernels (nullptr for fp32).
+FastFn fast_table(int ab, int cd) {
+    if (ab == GEMM_F16) return cd == GEMM_F16 ? tge::layer_fast_f16_f16 : tge::layer_fast_f16_f32;
+    if (ab == GEMM_BF16) return cd == GEMM_BF16 ? tge::layer_fast_bf16_bf16 : tge::layer_fast_bf16_f32;
+    return nullptr;
+}
+TableFn rows16_table(int ab, int cd) {
+    if (ab == GEMM_F16) return cd == GEMM_F16 ? tge::layer_rows16_f16_f16 : tge::layer_rows16_f16_f32;
+    if (ab == GEMM_BF16) return cd == GEMM_BF16 ? tge::layer_rows16_bf16_bf16 : tge::layer_rows16_bf16_f32;
+    return nullptr;
+}
+
+// Workgroups of a launch, at most MAX_GRID; with one range and no offsets every one has a tile.
+int64_t grid_of(const gemm_layer_plan &p, const LayerEntry &k) {
+    const __int128 g = (__int128)row_tiles(p.rows, p.groups, k.bm) * ceil_div(p.N, k.bn);
+    return g < MAX_GRID ? (int64_t)g : MAX_GRID;
+}
+
+// Whether D (and Z) are stored past the caches: as in the grouped plans, when rounds of tiles
+// follow that read the operands again, except in rows off 64-byte lines after short sums.
+bool stream_stores(const gemm_layer_plan &p, const LayerEntry &k, const void *D, int64_t grid, bool staged) {
+    const int ecd = elem_bytes(p.cd);
+    const bool apart = (((uintptr_t)D | (uintptr_t)(p.ldc * ecd)) & 63) != 0 && p.K <= (staged ? 32 : 512 / ecd);
+    return !apart && grid > (k.bm == 256 ? 256 : 512);
+}
+
+gemm_status_t launch(const gemm_layer_plan &p, LayerParams &prm, const void *A, const void *B, void *D,
+                     const int32_t *offsets, float alpha, void *stream) {
+    prm.A = A; prm.B = B; prm.D = D;
+    prm.M = (int)p.rows; prm.N = (int)p.N; prm.K = (int)p.K;
+    prm.lda = (int)p.lda; prm.ldb = (int)p.ldb; prm.ldc = (int)p.ldc;
+    prm.alpha = alpha;
+    prm.group_m = GROUP_M;
+    prm.batch = prm.batch2 = 1;
+    prm.stride_b = p.stride_b; prm.stride_bias = p.stride_bias;
+    prm.offs = offsets;
+    prm.groups = (int)p.groups;
+    prm.rows = (int)p.rows;
+    prm.act = p.act;
+    const bool direct = p.fast && aligned(A, 16) && aligned(B, 16);
+    const LayerEntry *k = direct ? p.fast : p.any;
+    prm.tiles_m = (int)ceil_div(p.rows, k->bm);
+    prm.tiles_n = (int)ceil_div(p.N, k->bn);
+    const int64_t grid = grid_of(p, *k);
+    prm.stream = stream_stores(p, *k, D, grid, !direct);
+    return k->launch(prm, (unsigned)grid, static_cast<hipStream_t>(stream)) == hipSuccess ? GEMM_STATUS_SUCCESS
+                                                                                          : GEMM_STATUS_HIP_ERROR;
+}
+
+// What both runs check; the plan is not empty.
+gemm_status_t check_run(const gemm_layer_plan &p, const void *A, const void *B, const void *D,
+                        const int32_t *offsets, float alpha) {
+    if (alpha != alpha) return GEMM_STATUS_INVALID_VALUE;   // NaN
+    const int eab = elem_bytes(p.ab);
+    if (!D || !aligned(D, elem_bytes(p.cd))) return GEMM_STATUS_INVALID_VALUE;
+    if (p.K > 0 && (!A || !B || !aligned(A, eab) || !aligned(B, eab))) return GEMM_STATUS_INVALID_VALUE;
+    if (offsets ? !aligned(offsets, 4) : p.groups > 1) return GEMM_STATUS_INVALID_VALUE;
+    return GEMM_STATUS_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_layer_plan_create(gemm_layer_plan_t *out, const gemm_layer_desc_t *d) {
+    if (!out) return GEMM_STATUS_INVALID_VALUE;
+    *out = nullptr;
+    if (!d) return GEMM_STATUS_INVALID_VALUE;
+    const int op_b = bits(d->op_b), ab = bits(d->ab_type), cd = bits(d->cd_type), act = bits(d->act),
+              algo = bits(d->algo), tile = d->tile;
+    if (!in(op_b, GEMM_OP_N, GEMM_OP_T) || !in(ab, GEMM_F32, GEMM_DF32) || !in(cd, GEMM_F32, GEMM_DF32) ||
+        !in(act, GEMM_ACT_NONE, GEMM_ACT_SILU))
+        return GEMM_STATUS_INVALID_VALUE;
+    switch (algo) {
+    case GEMM_ALGO_AUTO: if (tile != 0) return GEMM_STATUS_INVALID_VALUE; break;
+    case GEMM_ALGO_FAST: if (tile != 0 && tile != 256 && tile != 128 && tile != 64) return GEMM_STATUS_INVALID_VALUE; break;
+    case GEMM_ALGO_FAST_STAGED: if (tile != 0 && tile != 128 && tile != 64) return GEMM_STATUS_INVALID_VALUE; break;
+    case GEMM_ALGO_GENERAL: if (tile != 0 && tile != 128 && tile != 64) return GEMM_STATUS_INVALID_VALUE; break;
+    case GEMM_ALGO_SKINNY:
+        if (tile != 0 && tile != 64 && tile != (op_b == GEMM_OP_T ? 16 : 32)) return GEMM_STATUS_INVALID_VALUE;
+        break;
+    default: return GEMM_STATUS_INVALID_VALUE;
+    }
+    if (d->rows < 0 || d->N < 0 || d->K < 0 || d->groups < 1) return GEMM_STATUS_INVALID_VALUE;
+    if (d->rows >= LIM31 || d->N >= LIM31 || d->K >= LIM31 || d->lda >= LIM31 || d->ldb >= LIM31 ||
+        d->ldc >= LIM31 || d->groups >= MAX_GROUPS || !any_table(ab, cd))
+        return GEMM_STATUS_NOT_SUPPORTED;
+    const int64_t min_ldb = op_b == GEMM_OP_N ? d->N : d->K;
+    if (d->lda < (d->K > 1 ? d->K : 1) || d->ldb < (min_ldb > 1 ? min_ldb : 1) ||
+        d->ldc < (d->N > 1 ? d->N : 1) || d->stride_b < 0 || d->stride_bias < 0)
+        return GEMM_STATUS_INVALID_VALUE;
+    const int eab = elem_bytes(ab);
+    // 32-bit offsets inside one expert's weights, 63-bit ones between them
+    const int64_t b_rows = op_b == GEMM_OP_N ? d->K : d->N;
+    const int64_t big = ((int64_t)1 << 62) / 8 / d->groups;
+    if ((b_rows > 0 && (b_rows - 1) * d->ldb + min_ldb >= LIM31 / eab) || d->stride_b > big || d->stride_bias > big)
+        return GEMM_STATUS_NOT_SUPPORTED;
+
+    gemm_layer_plan p = {};
+    p.rows = d->rows; p.N = d->N; p.K = d->K; p.groups = d->groups;
+    p.lda = d->lda; p.ldb = d->ldb; p.ldc = d->ldc; p.stride_b = d->stride_b; p.stride_bias = d->stride_bias;
+    p.ab = ab; p.cd = cd; p.act = act;
+    // Kernels: `any` runs whatever the pointers' alignment is, `fast` on aligned ones.  The rules are
+    // those of the grouped plans.
+    const bool t = op_b == GEMM_OP_T;
+    const int64_t avg = ceil_div(d->rows, d->groups);                      // rows of an expert, on average
+    const int64_t n = d->rows < d->groups ? d->rows : d->groups;           // experts with rows, at most
+    const double ragged = d->groups > 1 ? 0.5 * (double)n : 0.0;           // half a tile at each range's end
+    const double tiles = ((double)d->rows / 128 + ragged) * (double)ceil_div(d->N, 128);
+    const double few = ((double)d->rows / 16 + ragged) * (double)ceil_div(d->N, 64);
+    const bool small = algo == GEMM_ALGO_GENERAL && tile ? tile == 64 : avg < 128 || d->N < 128;
+    p.any = any_table(ab, cd)(op_b, small ? tge::CFG_64 : tge::CFG_128);
+    const bool offsets_ok = d->lda * eab * 256 < LIM31;                    // 32-bit offsets within a tile's rows
+    const bool staged_ok = eab == 2 && d->N >= 8 && d->K > 0 && offsets_ok;
+    const bool rows16_ok = eab == 2 && d->K >= 8 && (t || d->N >= 8);
+    // direct loads: whole 16-byte chunks
+    const bool fast_ok = eab == 2 && d->K >= FAST_MIN_K && d->lda % 8 == 0 && d->ldb % 8 == 0 &&
+                         d->stride_b % 8 == 0 && (t || (d->N % 8 == 0 && d->N > 0)) && offsets_ok;
+    const auto rows16 = [&]() {
+        p.any = rows16_table(ab, cd)(op_b, 4);
+        if (grid_of(p, *p.any) < 256) p.any = rows16_table(ab, cd)(op_b, t ? 1 : 2);
+    };
+    switch (algo) {
+    case GEMM_ALGO_SKINNY:
+        if (rows16_ok && tile) p.any = rows16_table(ab, cd)(op_b, tile / 16);
+        else if (rows16_ok) rows16();
+        break;
+    case GEMM_ALGO_FAST:
+        if (fast_ok) p.fast = fast_table(ab, cd)(op_b, tile ? tile : 128, 0);
+        break;
+    case GEMM_ALGO_FAST_STAGED:
+        if (staged_ok) p.any = fast_table(ab, cd)(op_b, tile ? tile : 128, 1);
+        break;
+    case GEMM_ALGO_AUTO:
+        if (rows16_ok && few_rows_pay(avg, few)) {
+            rows16();
+        } else {
+            if (fast_ok) {
+                const int tl = wide_tiles_pay(d->rows, d->groups, n, avg, d->N, d->K) ? 256 : tiles < 200 ? 64 : 128;
+                p.fast = fast_table(ab, cd)(op_b, tl, 0);
+            }
+            if (staged_ok) p.any = fast_table(ab, cd)(op_b, tiles < 400 ? 64 : 128, 1);
+        }
+        break;
+    default: break;
+    }
+    const LayerEntry *k = p.fast ? p.fast : p.any;
+    if (grid_of(p, *p.any) >= MAX_GRID || grid_of(p, *k) >= MAX_GRID) return GEMM_STATUS_NOT_SUPPORTED;
+    gemm_layer_plan *q = new (std::nothrow) gemm_layer_plan(p);
+    if (!q) return GEMM_STATUS_ALLOC_FAILED;
+    static const char *const names[] = {"none", "relu", "gelu", "gelu_tanh", "silu"};
+    snprintf(q->desc, sizeof q->desc, "layer N%c %s %s %s->%s tile %dx%d groups %lld grid %lld", t ? 'T' : 'N',
+             names[act], k->name, type_name(ab), type_name(cd), k->bm, k->bn, (long long)p.groups,
+             (long long)grid_of(p, *k));
+    *out = q;
+    return GEMM_STATUS_SUCCESS;
+}
+
+gemm_status_t gemm_layer_run(gemm_layer_plan_t p, const void *A, const void *B, const void *C, void *D, void *Z,
+                             const void *bias, const int32_t *offsets, float alpha, float beta, void *stream) {
+    if (!p) return GEMM_STATUS_INVALID_VALUE;
+    if (p->rows == 0 || p->N == 0) return GEMM_STATUS_SUCCESS;
+    const gemm_status_t st = check_run(*p, A, B, D, offsets, alpha);
+    if (st != GEMM_STATUS_SUCCESS) return st;
+    const int ecd = elem_bytes(p->cd);
+    if (beta != beta || (beta != 0.0f && (!C || !aligned(C, ecd))) || (bias && !aligned(bias, 4)))
+        return GEMM_STATUS_INVALID_VALUE;
+    if (Z && (!aligned(Z, ecd) || Z == D || (beta != 0.0f && Z == C))) return GEMM_STATUS_INVALID_VALUE;
+    LayerParams prm = {};
+    prm.C = C; prm.Z = Z; prm.bias = bias;
+    prm.beta = beta;
+    prm.has_beta = beta != 0.0f;
+    prm.has_bias = bias != nullptr;
+    return launch(*p, prm, A, B, D, offsets, alpha, stream);
+}
+
+gemm_status_t gemm_layer_grad_run(gemm_layer_plan_t p, const void *A, const void *B, const void *Z, void *D,
+                                  const int32_t *offsets, float alpha, void *stream) {
+    if (!p) return GEMM_STATUS_INVALID_VALUE;
+    if (p->rows == 0 || p->N == 0) return GEMM_STATUS_SUCCESS;
+    const gemm_status_t st = check_run(*p, A, B, D, offsets, alpha);
+    if (st != GEMM_STATUS_SUCCESS) return st;
+    // without an activation the slope is 1 and Z is not read
+    const bool reads = p->act != tge::ACT_NONE;
+    if (reads && (!Z || !aligned(Z, elem_bytes(p->cd)))) return GEMM_STATUS_INVALID_VALUE;
+    LayerParams prm = {};
+    prm.Z = reads ? const_cast<void *>(Z) : nullptr;
+    prm.grad = reads;
+    return launch(*p, prm, A, B, D, offsets, alpha, stream);
+}
+
+gemm_status_t gemm_layer_plan_destroy(gemm_layer_plan_t p) {
+    delete p;
+    return GEMM_STATUS_SUCCESS;
+}
+
+gemm_status_t gemm_layer_plan_describe(gemm_layer_plan_t p, char *buf, size_t len) {
+    if (!p || !buf || len == 0) return GEMM_STATUS_INVALID_VALUE;
+    snprintf(buf, len, "%s", p->desc);
+    return GEMM_STATUS_SUCCESS;
+}
+
+}  // extern "C"
