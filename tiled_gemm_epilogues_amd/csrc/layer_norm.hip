@@ -44,68 +44,67 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
-// A lane's part of a row: C chunks of VE elements from columns col(c) on.
+// A lane's part of a row: C chunks of VE elements.  Chunk c stands at column n = (c W 64 + lane) VE; one
+// that would cross the row's end is moved back to end with it, and its first `skip` elements, which the lane
+// before has too, count for nothing: they are left out of sums, and stored twice with equal values.
+// So no load or store is narrower than 16 bytes, unless the row is (SHORT: it may be).
 template <class T, int W, int C>
 struct Part {
-    static constexpr int VE = 16 / (int)sizeof(T);
-    __device__ __forceinline__ static int col(int lane, int c) { return (c * W * 64 + lane) * VE; }
+    static constexpr int ES = (int)sizeof(T), VE = 16 / ES;
+    static constexpr bool SHORT = W * C == 1;
+    int col[C], skip[C];     // skip >= VE: outside the row
+    bool whole[C];           // (uniform) no chunk of the wave is moved
+    int n;                   // SHORT: the row's elements where they are fewer than a chunk's, else VE
+
+    __device__ __forceinline__ static int column(int lane, int c) { return (c * W * 64 + lane) * VE; }
+    __device__ __forceinline__ void init(int lane, int wave, int N) {
+        n = SHORT ? min(N, VE) : VE;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int at = column(lane, c);
+            col[c] = max(min(at, N - VE), 0);
+            skip[c] = at - col[c];
+            whole[c] = column(wave * 64 + 64, c) <= N;
+            if (SHORT && n < VE) skip[c] = lane == 0 ? 0 : VE;
+        }
+    }
+    __device__ __forceinline__ bool counts(int c, int e) const { return e >= skip[c] && (!SHORT || e < n); }
+    __device__ __forceinline__ u32x4 load(const T *row, int c) const {
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(row + col[c]);
+        if constexpr (SHORT) {
+            if (n < VE) return ldg16_partial<ES>(p, skip[c] ? 0 : n);
+        }
+        return ldg16(p);
+    }
+    __device__ __forceinline__ void store(T *row, int c, const float *v) const {
+        T out[VE];
+#pragma unroll
+        for (int e = 0; e < VE; ++e) out[e] = (T)v[e];
+        if (skip[c] >= VE) return;
+        if (SHORT && n < VE) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+                if (e < n) row[col[c] + e] = out[e];
+        } else {
+            __builtin_memcpy(row + col[c], out, 16);
+        }
+    }
+    // its columns of weight or bias (`none` each without them)
+    __device__ __forceinline__ void columns(float (&to)[VE], const float *v, int c, float none) const {
+        if (!v) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) to[e] = none;
+        } else if (SHORT && n < VE) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) to[e] = v[min(e, n - 1)];
+        } else {
+            __builtin_memcpy(to, v + col[c], sizeof(to));
+        }
+    }
 };
 
-// Chunk at column n of a row, zero past its N elements.  whole: every chunk of the wave lies inside
-// the row.  Else a load that ends with the row at the latest, moved down, so that no lane branches;
-// SHORT: the row may be shorter than a chunk.
-template <class T, bool SHORT>
-__device__ __forceinline__ u32x4 load_chunk(const T *row, int n, int N, bool whole) {
-    constexpr int ES = (int)sizeof(T), VE = 16 / ES;
-    if (whole) return ldg16(reinterpret_cast<const uint8_t *>(row + n));
-    if constexpr (SHORT) {
-        if (N < VE) return ldg16_partial<ES>(reinterpret_cast<const uint8_t *>(row + min(n, N)), N - n);
-    }
-    const int at = min(n, N - VE), past = n - at;
-    const u32x4 v = ldg16(reinterpret_cast<const uint8_t *>(row + at));
-    uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
-    if (past * ES >= 8) {
-        lo = hi;
-        hi = 0;
-    }
-    const int bits = 8 * (past * ES & 7);
-    lo = lo >> bits | (bits ? hi << (64 - bits) : 0);
-    hi >>= bits;
-    if (past >= VE) lo = 0;
-    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-}
-template <class T>
-__device__ __forceinline__ void store_chunk(T *row, int n, int N, bool whole, const float *v) {
-    constexpr int ES = (int)sizeof(T), VE = 16 / ES;
-    T out[VE];
-#pragma unroll
-    for (int e = 0; e < VE; ++e) out[e] = (T)v[e];
-    if (whole || n + VE <= N) {
-        __builtin_memcpy(row + n, out, 16);
-    } else if (n < N) {                  // the row's last elements, in pieces of 4, 2 and 1
-        const int have = N - n;
-        uint8_t *to = reinterpret_cast<uint8_t *>(row + n);
-        uint64_t w[2];
-        __builtin_memcpy(w, out, 16);
-        if (have * ES & 8) {
-            __builtin_memcpy(to, &w[0], 8);
-            w[0] = w[1];
-            to += 8;
-        }
-        if (have * ES & 4) {
-            const uint32_t x = (uint32_t)w[0];
-            __builtin_memcpy(to, &x, 4);
-            w[0] >>= 32;
-            to += 4;
-        }
-        if (have * ES & 2) {
-            const uint16_t x = (uint16_t)w[0];
-            __builtin_memcpy(to, &x, 2);
-        }
-    }
-}
-// A value of the row's loop that the compiler does not see to be the same in every turn: what is
-// derived from it is derived again, rather than held in registers (masks of every element) throughout.
+// v, which the compiler does not see to be the same in every turn of a loop: what is loaded from there is
+// loaded again, rather than held in registers throughout.
 __device__ __forceinline__ int renewed(int v) {
     asm volatile("" : "+s"(v));
     return v;
@@ -123,21 +122,6 @@ __device__ __forceinline__ float element(const u32x4 &v, int e) {
     __builtin_memcpy(t, &v, 16);
     return (float)t[e];
 }
-// VE columns of weight or bias from n on (`none` each without them); past N the last one's, for
-// values that are not used.
-template <int VE>
-__device__ __forceinline__ void load_columns(float (&to)[VE], const float *v, int n, int N, bool whole, float none) {
-    if (!v) {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) to[e] = none;
-    } else if (whole) {
-        __builtin_memcpy(to, v + n, sizeof(to));
-    } else {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) to[e] = v[min(n + e, N - 1)];
-    }
-}
-
 template <class T, int W, int C, int TEAMS>
 __global__ __launch_bounds__(W * 64 * TEAMS) void norm_forward(NormParams p) {
     using P = Part<T, W, C>;
@@ -147,22 +131,23 @@ __global__ __launch_bounds__(W * 64 * TEAMS) void norm_forward(NormParams p) {
     __shared__ float slots[2][TEAMS][W][2];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), team = wave / W, tw = wave % W;
     const int lane = threadIdx.x - team * W * 64;
-    int N = p.N;
+    const int N = p.N;
     const T *X = static_cast<const T *>(p.X);
     T *Y = static_cast<T *>(p.Y);
+    P part;
+    part.init(lane, tw, N);
 
     // elements of this wave's part of a row
     int mine = 0;
 #pragma unroll
-    for (int c = 0; c < C; ++c) mine += min(max(N - P::col(tw * 64, c), 0), 64 * VE);
-    const float n_w = (float)mine, rn_w = mine ? 1.0f / n_w : 0.0f;
-    const bool whole = mine == C * 64 * VE;
+    for (int c = 0; c < C; ++c) mine += min(max(N - P::column(tw * 64, c), 0), 64 * VE);
+    const float rn_w = mine ? 1.0f / (float)mine : 0.0f;
     float w[KEEP ? C : 1][VE], b[KEEP ? C : 1][VE];
     if constexpr (KEEP) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            load_columns(w[c], p.weight, P::col(lane, c), N, whole, 1.0f);
-            load_columns(b[c], p.bias, P::col(lane, c), N, whole, 0.0f);
+            part.columns(w[c], p.weight, c, 1.0f);
+            part.columns(b[c], p.bias, c, 0.0f);
         }
     }
 
@@ -171,14 +156,13 @@ __global__ __launch_bounds__(W * 64 * TEAMS) void norm_forward(NormParams p) {
     u32x4 next[C];
     auto fetch = [&](int r) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) next[c] = load_chunk<T, W * C == 1>(X + (int64_t)r * p.ldx, P::col(lane, c), N, whole);
+        for (int c = 0; c < C; ++c) next[c] = part.load(X + (int64_t)r * p.ldx, c);
     };
     if (KEEP && row < p.rows) fetch(row);
     int flip = 0;
     // the workgroup's first team has a row in every pass, so that all meet at the barriers
 #pragma unroll 1
     for (int first = blockIdx.x * TEAMS; first < p.rows; first += step, row += step, flip ^= 1) {
-        N = renewed(p.N);
         if (!KEEP && row < p.rows) fetch(row);
         u32x4 x[C];
 #pragma unroll
@@ -186,26 +170,31 @@ __global__ __launch_bounds__(W * 64 * TEAMS) void norm_forward(NormParams p) {
         if (KEEP && p.rows - row > step) fetch(row + step);
         float s = 0.0f;
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c) {
+            if (part.whole[c]) {
 #pragma unroll
-            for (int e = 0; e < VE; ++e) s += element<T>(x[c], e);
+                for (int e = 0; e < VE; ++e) s += element<T>(x[c], e);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) s += part.counts(c, e) ? element<T>(x[c], e) : 0.0f;
+            }
+        }
         float m = wave_sum(s) * rn_w, q = 0.0f;
-        if (whole) {
 #pragma unroll
-            for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c) {
+            if (part.whole[c]) {
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
                     const float d = element<T>(x[c], e) - m;
                     q = __builtin_fmaf(d, d, q);
                 }
-        } else {
-#pragma unroll
-            for (int c = 0; c < C; ++c)
+            } else {
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    const float d = P::col(lane, c) + e < N ? element<T>(x[c], e) - m : 0.0f;
+                    const float d = part.counts(c, e) ? element<T>(x[c], e) - m : 0.0f;
                     q = __builtin_fmaf(d, d, q);
                 }
+            }
         }
         q = wave_sum(q);
         if constexpr (W > 1) {
@@ -220,7 +209,7 @@ __global__ __launch_bounds__(W * 64 * TEAMS) void norm_forward(NormParams p) {
             for (int v = 0; v < W; ++v) {
                 n[v] = 0;
 #pragma unroll
-                for (int c = 0; c < C; ++c) n[v] += min(max(N - P::col(v * 64, c), 0), 64 * VE);
+                for (int c = 0; c < C; ++c) n[v] += min(max(N - P::column(v * 64, c), 0), 64 * VE);
                 mean = __builtin_fmaf(slots[flip][team][v][0], (float)n[v] * p.rn, mean);
             }
             q = 0.0f;
@@ -240,13 +229,13 @@ __global__ __launch_bounds__(W * 64 * TEAMS) void norm_forward(NormParams p) {
                 constexpr bool K = KEEP;
                 float (&wc)[VE] = w[K ? c : 0], (&bc)[VE] = b[K ? c : 0];
                 if (!K) {
-                    load_columns(wc, p.weight, P::col(lane, c) + renewed(0), N, whole, 1.0f);
-                    load_columns(bc, p.bias, P::col(lane, c) + renewed(0), N, whole, 0.0f);
+                    part.columns(wc, p.weight + renewed(0), c, 1.0f);
+                    part.columns(bc, p.bias + renewed(0), c, 0.0f);
                 }
                 float y[VE];
 #pragma unroll
                 for (int e = 0; e < VE; ++e) y[e] = __builtin_fmaf((element<T>(x[c], e) - m) * r, wc[e], bc[e]);
-                store_chunk(Y + (int64_t)row * p.ldy, P::col(lane, c), N, whole, y);
+                part.store(Y + (int64_t)row * p.ldy, c, y);
             }
             if (lane == 0) {
                 if (p.mean) p.mean[row] = m;
@@ -266,15 +255,15 @@ __global__ __launch_bounds__(W * 64 * TEAMS) void norm_grad(NormParams p) {
     __shared__ float sums[TEAMS > 1 ? (TEAMS - 1) * W * 64 * VE * C : 1];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), team = wave / W, tw = wave % W;
     const int lane = threadIdx.x - team * W * 64;
-    int N = p.N;
+    const int N = p.N;
     const T *X = static_cast<const T *>(p.X), *dY = static_cast<const T *>(p.Y), *Cm = static_cast<const T *>(p.C);
     T *dX = static_cast<T *>(p.dX);
-
-    const bool whole = P::col(tw * 64 + 64, C - 1) <= N;   // the wave's chunks all lie inside the row
+    P part;
+    part.init(lane, tw, N);
     float w[KEEP ? C : 1][VE];
     if constexpr (KEEP) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) load_columns(w[c], p.weight, P::col(lane, c), N, whole, 1.0f);
+        for (int c = 0; c < C; ++c) part.columns(w[c], p.weight, c, 1.0f);
     }
     float dw[C][VE], db[C][VE];
 #pragma unroll
@@ -294,8 +283,8 @@ __global__ __launch_bounds__(W * 64 * TEAMS) void norm_grad(NormParams p) {
     auto fetch = [&](int r) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            nx[c] = load_chunk<T, W * C == 1>(X + (int64_t)r * p.ldx, P::col(lane, c), N, whole);
-            ny[c] = load_chunk<T, W * C == 1>(dY + (int64_t)r * p.ldy, P::col(lane, c), N, whole);
+            nx[c] = part.load(X + (int64_t)r * p.ldx, c);
+            ny[c] = part.load(dY + (int64_t)r * p.ldy, c);
         }
         nm = p.mean[r];
         nr = p.rstd[r];
@@ -305,7 +294,6 @@ __global__ __launch_bounds__(W * 64 * TEAMS) void norm_grad(NormParams p) {
     int flip = 0;
 #pragma unroll 1
     for (int first = blockIdx.x * TEAMS; first < p.rows; first += step, row += step, flip ^= 1) {
-        N = renewed(p.N);
         const bool on = row < p.rows;
         if (!KEEP) fetch(row);               // (one team: it has a row)
         u32x4 x[C], y[C], res[C];
@@ -317,7 +305,7 @@ __global__ __launch_bounds__(W * 64 * TEAMS) void norm_grad(NormParams p) {
         const float m = nm, r = nr;
         if (KEEP && p.has_beta && on) {
 #pragma unroll
-            for (int c = 0; c < C; ++c) res[c] = load_chunk<T, W * C == 1>(Cm + (int64_t)row * p.ldx, P::col(lane, c), N, whole);
+            for (int c = 0; c < C; ++c) res[c] = part.load(Cm + (int64_t)row * p.ldx, c);
         }
         // a team past the last row sums nothing
         if (KEEP) {
@@ -328,10 +316,12 @@ __global__ __launch_bounds__(W * 64 * TEAMS) void norm_grad(NormParams p) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             float (&wc)[VE] = w[KEEP ? c : 0];
-            if (!KEEP) load_columns(wc, p.weight, P::col(lane, c) + renewed(0), N, whole, 1.0f);
+            if (!KEEP) part.columns(wc, p.weight + renewed(0), c, 1.0f);
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                const float dy = element<T>(y[c], e), h = (element<T>(x[c], e) - m) * r, g = dy * wc[e];
+                const float dy = element<T>(y[c], e), h = (element<T>(x[c], e) - m) * r;
+                // (elements that do not count add to column sums that are not stored)
+                const float g = part.whole[c] || part.counts(c, e) ? dy * wc[e] : 0.0f;
                 sg += g;
                 sgh = __builtin_fmaf(g, h, sgh);
                 dw[c][e] = __builtin_fmaf(dy, h, dw[c][e]);
@@ -361,12 +351,12 @@ __global__ __launch_bounds__(W * 64 * TEAMS) void norm_grad(NormParams p) {
             for (int c = 0; c < C; ++c) {
                 forget(x[c]);
                 forget(y[c]);
-                if (!KEEP && p.has_beta) res[c] = load_chunk<T, W * C == 1>(Cm + (int64_t)row * p.ldx, P::col(lane, c), N, whole);
+                if (!KEEP && p.has_beta) res[c] = part.load(Cm + (int64_t)row * p.ldx, c);
             }
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 float (&wc)[VE] = w[KEEP ? c : 0];
-                if (!KEEP) load_columns(wc, p.weight, P::col(lane, c) + renewed(0), N, whole, 1.0f);
+                if (!KEEP) part.columns(wc, p.weight + renewed(0), c, 1.0f);
                 float d[VE];
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
@@ -374,12 +364,11 @@ __global__ __launch_bounds__(W * 64 * TEAMS) void norm_grad(NormParams p) {
                     d[e] = r * (__builtin_fmaf(dy, wc[e], -sg) - h * sgh);
                     if (p.has_beta) d[e] = __builtin_fmaf(p.beta, element<T>(res[c], e), d[e]);
                 }
-                store_chunk(dX + (int64_t)row * p.ldx, P::col(lane, c), N, whole, d);
+                part.store(dX + (int64_t)row * p.ldx, c, d);
                 chunk_done();
             }
         }
     }
-    N = p.N;
     if (!p.part) return;
     // one partial sum per column and workgroup
     float *out = p.part + (int64_t)blockIdx.x * 2 * N;
@@ -411,10 +400,10 @@ __global__ __launch_bounds__(W * 64 * TEAMS) void norm_grad(NormParams p) {
         if (team == 0) {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int n = P::col(lane, c);
+                float *to = out + half * N + part.col[c];
 #pragma unroll
                 for (int e = 0; e < VE; ++e)
-                    if (n + e < N) out[half * N + n + e] = half ? db[c][e] : dw[c][e];
+                    if (part.counts(c, e)) to[e] = half ? db[c][e] : dw[c][e];
             }
         }
     }
