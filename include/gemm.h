@@ -662,7 +662,7 @@ gemm_status_t gemm_route_plan_create(gemm_route_plan_t *out, const gemm_route_de
 gemm_status_t gemm_route_workspace_bytes(gemm_route_plan_t plan, size_t *bytes);
 
 /*
- * Enqueues the routing on `stream`: one kernel for few rows, else three.  mask, slope and loss: NULL
+ * Enqueues the routing on `stream`: one kernel for few rows, else two.  mask, slope and loss: NULL
  * leaves them out.  workspace: 4-byte aligned, of workspace_bytes >= gemm_route_workspace_bytes bytes.
  * Returns INVALID_VALUE for a NULL plan, a missing pointer, one off its element's alignment or a
  * workspace too small; HIP_ERROR when a launch fails.

@@ -66,6 +66,7 @@ struct LayerParams : GroupedParams {
     void *Z;
     int act, grad;
     int stream;              // stores past the caches
+    int once;                // few rows: weights past them too
 };
 using LayerLaunchFn = hipError_t (*)(const LayerParams &, unsigned grid, hipStream_t);
 struct LayerEntry {
@@ -234,7 +235,7 @@ const GroupedEntry *grouped_rows16_f16_f32(int op_b, int cg);
 const GroupedEntry *grouped_rows16_bf16_bf16(int op_b, int cg);
 const GroupedEntry *grouped_rows16_bf16_f32(int op_b, int cg);
 
-// A layer's products: the kernels of GROUP_ROWS, under the same preconditions.
+// A layer's products: any and fast are the kernels of GROUP_ROWS, under the same preconditions.
 const LayerEntry *layer_any_f32_f32(int op_b, int cfg);
 const LayerEntry *layer_any_f16_f16(int op_b, int cfg);
 const LayerEntry *layer_any_f16_f32(int op_b, int cfg);
@@ -244,10 +245,12 @@ const LayerEntry *layer_fast_f16_f16(int op_b, int tile, int rs);
 const LayerEntry *layer_fast_f16_f32(int op_b, int tile, int rs);
 const LayerEntry *layer_fast_bf16_bf16(int op_b, int tile, int rs);
 const LayerEntry *layer_fast_bf16_f32(int op_b, int tile, int rs);
-const LayerEntry *layer_rows16_f16_f16(int op_b, int cg);
-const LayerEntry *layer_rows16_f16_f32(int op_b, int cg);
-const LayerEntry *layer_rows16_bf16_bf16(int op_b, int cg);
-const LayerEntry *layer_rows16_bf16_f32(int op_b, int cg);
+//   rows   16 * rt rows and 16 * cg columns per workgroup (rt 1, 2 or 4; cg 4, or 1 when op_b is T, 2
+//          when it is N): K >= 8, N >= 8 when op_b is N
+const LayerEntry *layer_rows_f16_f16(int op_b, int rt, int cg);
+const LayerEntry *layer_rows_f16_f32(int op_b, int rt, int cg);
+const LayerEntry *layer_rows_bf16_bf16(int op_b, int rt, int cg);
+const LayerEntry *layer_rows_bf16_f32(int op_b, int rt, int cg);
 
 // Products with 4-bit weights (gemm_quant.hip): W_e[n][k] = scale * (code - zero), codes packed
 // two per byte along k (low half: even k), one scale (of A's type) and zero point (uint8; nullptr:
@@ -323,7 +326,7 @@ hipError_t norm_join(const float *part, int count, int N, float *dweight, float 
 // Routing of rows to experts (route.hip).  A row belongs to `lanes` lanes (16, 32 or 64) of a wave
 // with `per` consecutive experts each (lanes * per >= experts).  Workgroup b takes rows b *
 // block_rows .. + block_rows - 1.
-constexpr int ROUTE_MAX_K = 16, ROUTE_MAX_EXPERTS = 1024;
+constexpr int ROUTE_MAX_K = 16, ROUTE_MAX_EXPERTS = 1024, ROUTE_MAX_BLOCKS = 256;
 struct RouteParams {
     const void *logits;      // rows x experts, ldl
     const uint8_t *mask;     // one per row, 0: left out; nullptr: none is
@@ -335,21 +338,25 @@ struct RouteParams {
     // gradient
     const float *dweight, *dloss;    // rows x k; 1 (nullptr: 0)
     void *dlogits;           // ldl
-    // workspace, blocks workgroups: choices per expert and used rows (blocks x (experts + 1)), summed
-    // probabilities (blocks x experts), and their totals
-    int32_t *hist, *total;
-    float *psum, *ptotal;
+    // workspace: each workgroup's choices per expert and used rows (blocks x (experts + 1)) and summed
+    // probabilities (blocks x experts)
+    int32_t *hist;
+    float *psum;
     int rows, experts, k, ldl, normalize;
     int block_rows, blocks;
 };
 struct RouteShape {
     int lanes, per;
 };
+// Waves of a choosing workgroup: 16, or 8 where its rows of sums would need too much LDS; and the rows that
+// one workgroup routes alone, at most (block_rows with blocks == 1).
+constexpr int route_waves(int width) { return width <= 256 ? 16 : 8; }
+constexpr int route_one_rows(int waves, int lanes) { return 4 * waves * (64 / lanes); }
 // Choice, weights and the workgroups' sums; with one workgroup everything.
 hipError_t route_choose_f32(const RouteParams &p, RouteShape s, hipStream_t stream);
 hipError_t route_choose_f16(const RouteParams &p, RouteShape s, hipStream_t stream);
 hipError_t route_choose_bf16(const RouteParams &p, RouteShape s, hipStream_t stream);
-// The rest for several workgroups: running sums over them, then order, place, offsets, slope, loss.
+// The rest for several workgroups: order, place, offsets, slope, loss.
 hipError_t route_place(const RouteParams &p, hipStream_t stream);
 hipError_t route_grad_f32(const RouteParams &p, RouteShape s, unsigned grid, hipStream_t stream);
 hipError_t route_grad_f16(const RouteParams &p, RouteShape s, unsigned grid, hipStream_t stream);

@@ -74,14 +74,16 @@ gemm_status_t gemm_route_plan_create(gemm_route_plan_t *out, const gemm_route_de
     p.rows = d->rows; p.experts = d->experts; p.k = d->k; p.ldl = d->ldl;
     p.type = type; p.normalize = d->normalize;
     p.shape = shape_of(d->experts);
-    const int64_t slots = 4 * (64 / p.shape.lanes);    // rows that a workgroup works on at a time
-    // one workgroup does a few rows in one launch; more take three, with up to 1024 workgroups
-    const int64_t fill = ceil_div(ceil_div(d->rows, 1024), slots) * slots;
-    p.block_rows = d->rows <= 8 * slots ? 8 * slots : fill;
+    const int waves = tge::route_waves(p.shape.lanes * p.shape.per);
+    const int64_t slots = waves * (64 / p.shape.lanes);    // rows that a workgroup chooses for at a time
+    // one workgroup does a few rows in one launch; more take two, with up to ROUTE_MAX_BLOCKS workgroups
+    const int64_t fill = ceil_div(ceil_div(d->rows, tge::ROUTE_MAX_BLOCKS), slots) * slots;
+    const int64_t one = tge::route_one_rows(waves, p.shape.lanes);
+    p.block_rows = d->rows <= one ? one : fill;
     p.blocks = d->rows > 0 ? ceil_div(d->rows, p.block_rows) : 1;
-    const int64_t need = ceil_div(d->rows, slots);
+    const int64_t need = ceil_div(d->rows, 4 * (64 / p.shape.lanes));
     p.grid_grad = need < 2048 ? need : 2048;
-    p.workspace = p.blocks > 1 ? (size_t)((p.blocks + 1) * (2 * p.experts + 1) * 4) : 0;
+    p.workspace = p.blocks > 1 ? (size_t)((2 * p.experts + 1) * p.blocks * 4) : 0;
     gemm_route_plan *q = new (std::nothrow) gemm_route_plan(p);
     if (!q) return GEMM_STATUS_ALLOC_FAILED;
     snprintf(q->desc, sizeof q->desc, "route %s experts %lld k %lld%s lanes %d x %d blocks %lld of %lld rows", type_name(type),
@@ -112,9 +114,7 @@ gemm_status_t gemm_route_run(gemm_route_plan_t p, const void *logits, const uint
     q.offsets = offsets; q.slope = slope; q.loss = loss;
     if (p->blocks > 1) {
         q.hist = static_cast<int32_t *>(workspace);
-        q.total = q.hist + p->blocks * (p->experts + 1);
-        q.psum = reinterpret_cast<float *>(q.total + p->experts + 1);
-        q.ptotal = q.psum + p->blocks * p->experts;
+        q.psum = reinterpret_cast<float *>(q.hist + (p->experts + 1) * p->blocks);
     }
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (choose_of(p->type)(q, p->shape, st) != hipSuccess) return GEMM_STATUS_HIP_ERROR;
