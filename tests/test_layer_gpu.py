@@ -16,7 +16,7 @@ NAN = float("nan")
 PAIRS = [("f16", "f16"), ("f16", "f32"), ("bf16", "bf16"), ("bf16", "f32")]
 KERNELS = [("general", 64), ("general", 128), ("fast", 64), ("fast", 128), ("fast", 256), ("staged", 64),
            ("staged", 128), ("skinny", 64), ("skinny", 16)]
-NAMES = {"general": "gemm_mfma", "fast": "gemm_fast", "staged": "_rs", "skinny": "rows16"}
+NAMES = {"general": "gemm_mfma", "fast": "gemm_fast", "staged": "_rs", "skinny": "layer_rows"}
 
 
 @pytest.fixture(autouse=True)

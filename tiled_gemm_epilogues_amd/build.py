@@ -53,7 +53,7 @@ def steps():
         for pair in pairs:
             add(name + ".hip", f"grouped_{name}_{pair.lower()}", f"-DTGE_PAIR_{pair}", "-DTGE_GROUPED")
     for pair in GROUPED_PAIRS:
-        for name in ("gemm_rows16", "gemm_quant"):
+        for name in ("gemm_rows16", "gemm_quant", "layer_rows"):
             add(name + ".hip", f"{name}_{pair.lower()}", f"-DTGE_PAIR_{pair}")
     # the same kernels with a layer's epilogue
     for name, pairs in (("gemm_kernels", GROUPED_PAIRS + ["F32_F32"]), ("gemm_fast", GROUPED_PAIRS)):

@@ -27,7 +27,6 @@
 
 #include "device_common.hpp"
 #include "gemm_internal.h"
-#include "layer_epilogue.hpp"
 
 namespace tge {
 namespace {
@@ -52,9 +51,9 @@ __device__ __forceinline__ void wave_order() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// BT: B stored N x K; CG: groups of 16 columns; KC: k per chunk; GRP: GROUP_ROWS or GROUP_LAYER.
-template <class TI, class TO, bool BT, int CG, int KC, int GRP>
-__global__ __launch_bounds__(WAVES * 64, 2) void gemm_rows16(ParamsOf<GRP> p) {
+// BT: B stored N x K; CG: groups of 16 columns; KC: k per chunk.
+template <class TI, class TO, bool BT, int CG, int KC>
+__global__ __launch_bounds__(WAVES * 64, 2) void gemm_rows16(GroupedParams p) {
     using T = typename TO::T;
     static_assert(BT || ((CG == 4 || CG == 2) && KC == 64), "rows of 64 or 32 columns");
     constexpr int NI = KC / 32;                              // 16x16x32 instructions per chunk and group
@@ -66,11 +65,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void gemm_rows16(ParamsOf<GRP> p) {
     __shared__ __attribute__((aligned(16))) uint8_t smem[WAVES * SLOT];
 
     int tn;
-    if constexpr (GRP == GROUP_LAYER) {
-        if (!select_layer<2, (int)sizeof(T)>(p, blockIdx.x, 16, tn)) return;
-    } else {
-        if (!select_rows<2, (int)sizeof(T)>(p, blockIdx.x, 16, tn)) return;
-    }
+    if (!select_rows<2, (int)sizeof(T)>(p, blockIdx.x, 16, tn)) return;
     const int lane = threadIdx.x & 63, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane >> 2, lq = lane & 3;                 // load order of rows along K: row, piece
@@ -198,30 +193,6 @@ __global__ __launch_bounds__(WAVES * 64, 2) void gemm_rows16(ParamsOf<GRP> p) {
     const float bias = p.has_bias ? static_cast<const float *>(p.bias)[n] : 0.0f;
     const T *C = static_cast<const T *>(p.C);
     T *D = static_cast<T *>(p.D);
-    if constexpr (GRP == GROUP_LAYER) {
-        // rows past the range take its last one's values; they are not stored
-        const T *X = static_cast<const T *>(p.grad ? p.Z : p.C);
-        T *Z = p.grad ? nullptr : static_cast<T *>(p.Z);
-        float v[4];
-        T x[4], out[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            v[r] = __builtin_fmaf(p.alpha, sum[r], bias);
-            x[r] = p.grad || p.has_beta ? X[(int64_t)min(4 * g + r, p.M - 1) * p.ldc + n] : (T)0;
-        }
-        if (Z) {
-            round_values(v, out);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (4 * g + r < p.M) Z[(int64_t)(4 * g + r) * p.ldc + n] = out[r];
-        }
-        finish_values<4, (int)sizeof(T)>(p, v, x);
-        round_values(v, out);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (4 * g + r < p.M) D[(int64_t)(4 * g + r) * p.ldc + n] = out[r];
-        return;
-    }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int m = 4 * g + r;
@@ -236,18 +207,18 @@ __global__ __launch_bounds__(WAVES * 64, 2) void gemm_rows16(ParamsOf<GRP> p) {
     }
 }
 
-template <class TI, class TO, bool BT, int CG, int KC, int GRP>
-hipError_t launch(const ParamsOf<GRP> &p, unsigned grid, hipStream_t s) {
-    hipLaunchKernelGGL((gemm_rows16<TI, TO, BT, CG, KC, GRP>), dim3(grid), dim3(WAVES * 64), 0, s, p);
+template <class TI, class TO, bool BT, int CG, int KC>
+hipError_t launch(const GroupedParams &p, unsigned grid, hipStream_t s) {
+    hipLaunchKernelGGL((gemm_rows16<TI, TO, BT, CG, KC>), dim3(grid), dim3(WAVES * 64), 0, s, p);
     return hipGetLastError();
 }
 
-template <class TI, class TO, int GRP, class Entry>
-const Entry *lookup(int op_b, int cg) {
-    static const Entry n[2] = {{launch<TI, TO, false, 2, 64, GRP>, 16, 32, "gemm_rows16_16x32"},
-                               {launch<TI, TO, false, 4, 64, GRP>, 16, 64, "gemm_rows16_16x64"}};
-    static const Entry t[2] = {{launch<TI, TO, true, 1, 128, GRP>, 16, 16, "gemm_rows16_16x16"},
-                               {launch<TI, TO, true, 4, 64, GRP>, 16, 64, "gemm_rows16_16x64"}};
+template <class TI, class TO>
+const GroupedEntry *lookup(int op_b, int cg) {
+    static const GroupedEntry n[2] = {{launch<TI, TO, false, 2, 64>, 16, 32, "gemm_rows16_16x32"},
+                                      {launch<TI, TO, false, 4, 64>, 16, 64, "gemm_rows16_16x64"}};
+    static const GroupedEntry t[2] = {{launch<TI, TO, true, 1, 128>, 16, 16, "gemm_rows16_16x16"},
+                                      {launch<TI, TO, true, 4, 64>, 16, 64, "gemm_rows16_16x64"}};
     if (op_b == 0) return cg == 2 ? &n[0] : cg == 4 ? &n[1] : nullptr;
     return op_b == 1 ? (cg == 1 ? &t[0] : cg == 4 ? &t[1] : nullptr) : nullptr;
 }
@@ -255,17 +226,13 @@ const Entry *lookup(int op_b, int cg) {
 }  // namespace
 
 #if defined(TGE_PAIR_F16_F16)
-const GroupedEntry *grouped_rows16_f16_f16(int b, int cg) { return lookup<TF16, OF16, GROUP_ROWS, GroupedEntry>(b, cg); }
-const LayerEntry *layer_rows16_f16_f16(int b, int cg) { return lookup<TF16, OF16, GROUP_LAYER, LayerEntry>(b, cg); }
+const GroupedEntry *grouped_rows16_f16_f16(int b, int cg) { return lookup<TF16, OF16>(b, cg); }
 #elif defined(TGE_PAIR_F16_F32)
-const GroupedEntry *grouped_rows16_f16_f32(int b, int cg) { return lookup<TF16, OF32, GROUP_ROWS, GroupedEntry>(b, cg); }
-const LayerEntry *layer_rows16_f16_f32(int b, int cg) { return lookup<TF16, OF32, GROUP_LAYER, LayerEntry>(b, cg); }
+const GroupedEntry *grouped_rows16_f16_f32(int b, int cg) { return lookup<TF16, OF32>(b, cg); }
 #elif defined(TGE_PAIR_BF16_BF16)
-const GroupedEntry *grouped_rows16_bf16_bf16(int b, int cg) { return lookup<TBF16, OBF16, GROUP_ROWS, GroupedEntry>(b, cg); }
-const LayerEntry *layer_rows16_bf16_bf16(int b, int cg) { return lookup<TBF16, OBF16, GROUP_LAYER, LayerEntry>(b, cg); }
+const GroupedEntry *grouped_rows16_bf16_bf16(int b, int cg) { return lookup<TBF16, OBF16>(b, cg); }
 #elif defined(TGE_PAIR_BF16_F32)
-const GroupedEntry *grouped_rows16_bf16_f32(int b, int cg) { return lookup<TBF16, OF32, GROUP_ROWS, GroupedEntry>(b, cg); }
-const LayerEntry *layer_rows16_bf16_f32(int b, int cg) { return lookup<TBF16, OF32, GROUP_LAYER, LayerEntry>(b, cg); }
+const GroupedEntry *grouped_rows16_bf16_f32(int b, int cg) { return lookup<TBF16, OF32>(b, cg); }
 #else
 #error "define one TGE_PAIR_* macro of a 16-bit float type"
 #endif

@@ -98,6 +98,14 @@ gemm_status_t launch(const gemm_grouped_plan &p, const void *A, const void *B, c
                                                                                 : GEMM_STATUS_HIP_ERROR;
 }
 
+// Whether the kernel for few rows (16 rows per workgroup, K split over its waves) beats the tiles,
+// which waste most of a tile but move more weights per workgroup: for a few rows per expert, and as
+// long as its 16 x 64 workgroups (`few`) are about one round.  Measured (bf16, B not transposed, N 2048,
+// K 4096; few rows -> best tile): 1 row per expert, 64 experts, 107 vs 146 us; 1 expert, 128 rows (272
+// workgroups) 13 vs 30; 8 experts, 256 rows (640) 35 vs 44, 512 (1152) 49 vs 46, 1024 (2176) 81 vs 50;
+// 64 experts, 512 rows (2048) 196 vs 193, 2048 (5120) 254 vs 200.
+bool few_rows_pay(int64_t avg, double few) { return avg <= 6 || few <= 700; }
+
 // Hands a finished plan out, with its description.
 gemm_status_t finish_plan(gemm_grouped_plan_t *out, const gemm_grouped_plan &p, const char *what) {
     const GroupedEntry *k = p.fast ? p.fast : p.any;

@@ -40,14 +40,6 @@ inline int64_t row_tiles(int64_t rows, int64_t groups, int64_t bm) {
     return n + (rows - n) / bm;
 }
 
-// Whether the kernel for few rows (16 rows per workgroup, K split over its waves) beats the tiles,
-// which waste most of a tile but move more weights per workgroup: for a few rows per expert, and as
-// long as its 16 x 64 workgroups (`few`) are about one round.  Measured (bf16, B not transposed, N 2048,
-// K 4096; few rows -> best tile): 1 row per expert, 64 experts, 107 vs 146 us; 1 expert, 128 rows (272
-// workgroups) 13 vs 30; 8 experts, 256 rows (640) 35 vs 44, 512 (1152) 49 vs 46, 1024 (2176) 81 vs 50;
-// 64 experts, 512 rows (2048) 196 vs 193, 2048 (5120) 254 vs 200.
-inline bool few_rows_pay(int64_t avg, double few) { return avg <= 6 || few <= 700; }
-
 // Whether the 256-wide tiles (one workgroup per CU) beat the 128-wide ones (two): with rows enough
 // to fill them and a few rounds of them.  Measured (bf16, B not transposed; 128 -> 256): 8192 x 4096
 // x 4096 over 8 experts 310 -> 275 us, 4096 x 14336 x 4096 over 8 562 -> 490, 16384 x 8192 x 2048

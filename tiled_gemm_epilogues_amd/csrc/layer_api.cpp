@@ -1,6 +1,6 @@
 // C ABI of a layer's products (bias, activation, residual; the gradient through the activation): plan
 // creation and validation, kernel choice, launch.  Host code only; the kernels are the layer
-// instances of gemm_kernels.hip, gemm_fast.hip and gemm_rows16.hip.
+// instances of gemm_kernels.hip and gemm_fast.hip, and layer_rows.hip.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -46,9 +46,9 @@ FastFn fast_table(int ab, int cd) {
     if (ab == GEMM_BF16) return cd == GEMM_BF16 ? tge::layer_fast_bf16_bf16 : tge::layer_fast_bf16_f32;
     return nullptr;
 }
-TableFn rows16_table(int ab, int cd) {
-    if (ab == GEMM_F16) return cd == GEMM_F16 ? tge::layer_rows16_f16_f16 : tge::layer_rows16_f16_f32;
-    if (ab == GEMM_BF16) return cd == GEMM_BF16 ? tge::layer_rows16_bf16_bf16 : tge::layer_rows16_bf16_f32;
+FastFn rows_table(int ab, int cd) {
+    if (ab == GEMM_F16) return cd == GEMM_F16 ? tge::layer_rows_f16_f16 : tge::layer_rows_f16_f32;
+    if (ab == GEMM_BF16) return cd == GEMM_BF16 ? tge::layer_rows_bf16_bf16 : tge::layer_rows_bf16_f32;
     return nullptr;
 }
 
@@ -64,6 +64,15 @@ bool stream_stores(const gemm_layer_plan &p, const LayerEntry &k, const void *D,
     const int ecd = elem_bytes(p.cd);
     const bool apart = (((uintptr_t)D | (uintptr_t)(p.ldc * ecd)) & 63) != 0 && p.K <= (staged ? 32 : 512 / ecd);
     return !apart && grid > (k.bm == 256 ? 256 : 512);
+}
+
+// Whether the kernel for few rows reads the weights past the caches: where one workgroup reads each of them
+// and all of them are more than half of the 256 MB cache, so that they would not be found there
+// anyway.  B transposed, 16 rows: 16384 x 4096 (128 MiB) in turn with three others 28.2 -> 23.3 us, alone
+// 22.0 and 21.7; but 8192 x 4096 in turn 16.9 and 17.6, alone 13.3 and 17.1.  B not transposed (whose short
+// pieces of rows lose their second halves): 4096 x 4096 in turn 12.5 -> 19.9.
+bool read_once(const gemm_layer_plan &p, const LayerEntry &k) {
+    return ceil_div(p.rows, p.groups) <= k.bm && (double)p.groups * p.K * p.N * elem_bytes(p.ab) >= (double)(128 << 20);
 }
 
 gemm_status_t launch(const gemm_layer_plan &p, LayerParams &prm, const void *A, const void *B, void *D,
@@ -84,6 +93,7 @@ gemm_status_t launch(const gemm_layer_plan &p, LayerParams &prm, const void *A, 
     prm.tiles_m = (int)ceil_div(p.rows, k->bm);
     prm.tiles_n = (int)ceil_div(p.N, k->bn);
     const int64_t grid = grid_of(p, *k);
+    prm.once = read_once(p, *k);
     prm.stream = stream_stores(p, *k, D, grid, !direct);
     return k->launch(prm, (unsigned)grid, static_cast<hipStream_t>(stream)) == hipSuccess ? GEMM_STATUS_SUCCESS
                                                                                           : GEMM_STATUS_HIP_ERROR;
@@ -142,8 +152,8 @@ gemm_status_t gemm_layer_plan_create(gemm_layer_plan_t *out, const gemm_layer_de
     p.rows = d->rows; p.N = d->N; p.K = d->K; p.groups = d->groups;
     p.lda = d->lda; p.ldb = d->ldb; p.ldc = d->ldc; p.stride_b = d->stride_b; p.stride_bias = d->stride_bias;
     p.ab = ab; p.cd = cd; p.act = act;
-    // Kernels: `any` runs whatever the pointers' alignment is, `fast` on aligned ones.  The rules are
-    // those of the grouped plans.
+    // Kernels: `any` runs whatever the pointers' alignment is, `fast` on aligned ones.  The rules for the
+    // tiles are those of the grouped plans, where they are measured.
     const bool t = op_b == GEMM_OP_T;
     const int64_t avg = ceil_div(d->rows, d->groups);                      // rows of an expert, on average
     const int64_t n = d->rows < d->groups ? d->rows : d->groups;           // experts with rows, at most
@@ -154,18 +164,39 @@ gemm_status_t gemm_layer_plan_create(gemm_layer_plan_t *out, const gemm_layer_de
     p.any = any_table(ab, cd)(op_b, small ? tge::CFG_64 : tge::CFG_128);
     const bool offsets_ok = d->lda * eab * 256 < LIM31;                    // 32-bit offsets within a tile's rows
     const bool staged_ok = eab == 2 && d->N >= 8 && d->K > 0 && offsets_ok;
-    const bool rows16_ok = eab == 2 && d->K >= 8 && (t || d->N >= 8);
+    const bool rows_ok = eab == 2 && d->K >= 8 && (t || d->N >= 8) && d->lda * eab * 64 < LIM31;
     // direct loads: whole 16-byte chunks
     const bool fast_ok = eab == 2 && d->K >= FAST_MIN_K && d->lda % 8 == 0 && d->ldb % 8 == 0 &&
                          d->stride_b % 8 == 0 && (t || (d->N % 8 == 0 && d->N > 0)) && offsets_ok;
-    const auto rows16 = [&]() {
-        p.any = rows16_table(ab, cd)(op_b, 4);
-        if (grid_of(p, *p.any) < 256) p.any = rows16_table(ab, cd)(op_b, t ? 1 : 2);
+    // Few rows: as many in a workgroup as there are on average.  64 columns where such workgroups are enough:
+    // with 16 rows, or B not transposed, one for every CU (16 x 4096 x 4096 9.6 vs 12.8 us in 16 columns, 16
+    // x 16384 x 4096 29.6 vs 29.0; not transposed 100 x 4096 x 16384, 128 of them, 71 vs 99 in 32, 200, 256 of
+    // them, 112 vs 93); with more rows, each of which narrow workgroups read again, a few less (64 x 6144 x
+    // 4096, 96 of them, 23.6 vs 20.1, but 64 x 4096 x 16384, 64 of them, 47 vs 76).
+    const int rt = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
+    const auto rows_kernel = [&]() {
+        p.any = rows_table(ab, cd)(op_b, rt, 4);
+        if (grid_of(p, *p.any) < (t && rt > 1 ? 96 : 256)) p.any = rows_table(ab, cd)(op_b, rt, t ? 1 : 2);
+    };
+    // Whether that kernel beats the tiles.  One matrix, gelu: up to 64 rows (64 x 65536 x 4096 121 -> 110
+    // us), and while its workgroups are one round, or two of long sums (256 x 4096 x 4096 32 -> 21, 384 x
+    // 4096 x 16384 175 -> 124, but 512 x 4096 x 4096 32 vs 36, 192 x 16384 x 4096 58 vs 66).  Experts' ranges
+    // are ragged, and read weights of their own, by ever more waves (us, tiles -> few rows; B transposed): 8
+    // rows each, 128 of 1536 x 2048 147 -> 138, 64 of 2048 x 4096 174 -> 169; 16 and 24 rows, 64 of 768 x 2048
+    // 52 -> 47 and 53 -> 49, 8 of 2048 x 4096 46 -> 33 and 46 -> 38, but 64 of 2048 x 4096 174 vs 200 and 180 vs
+    // 204; 64 rows, 16 of 1024 x 2048 21 vs 25.  Not transposed: 2 rows, 64 of 2048 x 4096 165 -> 157, 8 and
+    // 24 rows, 8 of them, 39 -> 26 and 40 -> 38, but 8 rows, 64 of 768 x 2048 38 vs 50.
+    const auto few_rows = [&]() {
+        if (d->groups == 1) {
+            const int64_t wide = ceil_div(d->rows, 16 * rt) * ceil_div(d->N, 64);
+            return d->rows <= 64 || wide <= 256 || (wide <= 512 && d->K >= 8192);
+        }
+        return t ? avg <= 8 || (avg <= 32 && few <= 1600) : avg <= 4 || few <= 700;
     };
     switch (algo) {
     case GEMM_ALGO_SKINNY:
-        if (rows16_ok && tile) p.any = rows16_table(ab, cd)(op_b, tile / 16);
-        else if (rows16_ok) rows16();
+        if (rows_ok && tile) p.any = rows_table(ab, cd)(op_b, rt, tile / 16);
+        else if (rows_ok) rows_kernel();
         break;
     case GEMM_ALGO_FAST:
         if (fast_ok) p.fast = fast_table(ab, cd)(op_b, tile ? tile : 128, 0);
@@ -174,11 +205,14 @@ gemm_status_t gemm_layer_plan_create(gemm_layer_plan_t *out, const gemm_layer_de
         if (staged_ok) p.any = fast_table(ab, cd)(op_b, tile ? tile : 128, 1);
         break;
     case GEMM_ALGO_AUTO:
-        if (rows16_ok && few_rows_pay(avg, few)) {
-            rows16();
+        if (rows_ok && few_rows()) {
+            rows_kernel();
         } else {
             if (fast_ok) {
-                const int tl = wide_tiles_pay(d->rows, d->groups, n, avg, d->N, d->K) ? 256 : tiles < 200 ? 64 : 128;
+                // 64-wide tiles also for short ranges of a transposed B: 24 rows, 64 experts of 2048 x 4096 184
+                // -> 180 us, 16 rows, 128 of 1536 x 2048 159 -> 150; 32 rows 187 vs 219
+                const int tl = wide_tiles_pay(d->rows, d->groups, n, avg, d->N, d->K) ? 256
+                               : tiles < 200 || (t && avg <= 24) ? 64 : 128;
                 p.fast = fast_table(ab, cd)(op_b, tl, 0);
             }
             if (staged_ok) p.any = fast_table(ab, cd)(op_b, tiles < 400 ? 64 : 128, 1);
