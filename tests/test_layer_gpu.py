@@ -162,13 +162,16 @@ def test_ranges_in_every_kernel(algo, tile, op_b, ab, cd):
 
 
 @pytest.mark.parametrize("op_b", ["N", "T"])
-@pytest.mark.parametrize("tile", [64, 128])
-def test_fp32(op_b, tile):
+@pytest.mark.parametrize("algo,tile", [("general", 64), ("general", 128), ("skinny", 64), ("skinny", 16)])
+def test_fp32(algo, tile, op_b):
+    tile = tile_of(algo, tile, op_b)
     for i, (rows, N, K, groups, counts) in enumerate([(130, 140, 70, 1, None), (1, 1, 1, 1, None),
-                                                      (90, 33, 35, 4, [0, 50, 2, 30])]):
+                                                      (90, 33, 35, 4, [0, 50, 2, 30]), (17, 65, 4, 1, None),
+                                                      (48, 70, 300, 3, [3, 20, 24]), (28, 64, 1001, 2, [10, 17])]):
         p = Problem(20 + i, rows, N, K, op_b, "f32", "f32", groups, counts, pad=(1, 3, 5))
         for act in ACTS:
-            plan = p.plan(act, "general", tile)
+            plan = p.plan(act, algo, tile)
+            assert K == 1 or NAMES[algo] in plan.describe(), plan.describe()
             check_forward(p, act, plan)
             check_grad(p, act, plan)
 

@@ -53,9 +53,11 @@ def steps():
         for pair in pairs:
             add(name + ".hip", f"grouped_{name}_{pair.lower()}", f"-DTGE_PAIR_{pair}", "-DTGE_GROUPED")
     for pair in GROUPED_PAIRS:
-        for name in ("gemm_rows16", "gemm_quant", "layer_rows"):
+        for name in ("gemm_rows16", "gemm_quant"):
             add(name + ".hip", f"{name}_{pair.lower()}", f"-DTGE_PAIR_{pair}")
     # the same kernels with a layer's epilogue
+    for pair in GROUPED_PAIRS + ["F32_F32"]:
+        add("layer_rows.hip", f"layer_rows_{pair.lower()}", f"-DTGE_PAIR_{pair}")
     for name, pairs in (("gemm_kernels", GROUPED_PAIRS + ["F32_F32"]), ("gemm_fast", GROUPED_PAIRS)):
         for pair in pairs:
             add(name + ".hip", f"layer_{name}_{pair.lower()}", f"-DTGE_PAIR_{pair}", "-DTGE_LAYER")

@@ -84,6 +84,17 @@ struct TF32 {
         }
         return c;
     }
+    using accv16_t = f32x4;
+    // 16x16 output: the 16 lanes of a group supply 4 consecutive k, the groups 16 in all
+    __device__ static accv16_t mma16(u32x4 a, u32x4 b, accv16_t c) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t aj = a[j], bj = b[j];
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, aj),
+                                                     __builtin_bit_cast(float, bj), c, 0, 0, 0);
+        }
+        return c;
+    }
 };
 
 // output element types

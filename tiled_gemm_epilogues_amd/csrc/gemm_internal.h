@@ -246,7 +246,8 @@ const LayerEntry *layer_fast_f16_f32(int op_b, int tile, int rs);
 const LayerEntry *layer_fast_bf16_bf16(int op_b, int tile, int rs);
 const LayerEntry *layer_fast_bf16_f32(int op_b, int tile, int rs);
 //   rows   16 * rt rows and 16 * cg columns per workgroup (rt 1, 2 or 4; cg 4, or 1 when op_b is T, 2
-//          when it is N): K >= 8, N >= 8 when op_b is N
+//          when it is N): K of a 16-byte chunk, N too when op_b is N; 64 rows of A within 2^31 bytes
+const LayerEntry *layer_rows_f32_f32(int op_b, int rt, int cg);
 const LayerEntry *layer_rows_f16_f16(int op_b, int rt, int cg);
 const LayerEntry *layer_rows_f16_f32(int op_b, int rt, int cg);
 const LayerEntry *layer_rows_bf16_bf16(int op_b, int rt, int cg);

@@ -40,13 +40,14 @@ TableFn any_table(int ab, int cd) {
     return nullptr;
 }
 
-// The tables of the 16-bit kernels (nullptr for fp32).
+// The tables of the fast kernel (nullptr for fp32) and of the one for few rows.
 FastFn fast_table(int ab, int cd) {
     if (ab == GEMM_F16) return cd == GEMM_F16 ? tge::layer_fast_f16_f16 : tge::layer_fast_f16_f32;
     if (ab == GEMM_BF16) return cd == GEMM_BF16 ? tge::layer_fast_bf16_bf16 : tge::layer_fast_bf16_f32;
     return nullptr;
 }
 FastFn rows_table(int ab, int cd) {
+    if (ab == GEMM_F32) return tge::layer_rows_f32_f32;
     if (ab == GEMM_F16) return cd == GEMM_F16 ? tge::layer_rows_f16_f16 : tge::layer_rows_f16_f32;
     if (ab == GEMM_BF16) return cd == GEMM_BF16 ? tge::layer_rows_bf16_bf16 : tge::layer_rows_bf16_f32;
     return nullptr;
@@ -164,19 +165,28 @@ gemm_status_t gemm_layer_plan_create(gemm_layer_plan_t *out, const gemm_layer_de
     p.any = any_table(ab, cd)(op_b, small ? tge::CFG_64 : tge::CFG_128);
     const bool offsets_ok = d->lda * eab * 256 < LIM31;                    // 32-bit offsets within a tile's rows
     const bool staged_ok = eab == 2 && d->N >= 8 && d->K > 0 && offsets_ok;
-    const bool rows_ok = eab == 2 && d->K >= 8 && (t || d->N >= 8) && d->lda * eab * 64 < LIM31;
+    const bool rows_ok = d->K >= 16 / eab && (t || d->N >= 16 / eab) && d->lda * eab * 64 < LIM31;
     // direct loads: whole 16-byte chunks
     const bool fast_ok = eab == 2 && d->K >= FAST_MIN_K && d->lda % 8 == 0 && d->ldb % 8 == 0 &&
                          d->stride_b % 8 == 0 && (t || (d->N % 8 == 0 && d->N > 0)) && offsets_ok;
-    // Few rows: as many in a workgroup as there are on average.  64 columns where such workgroups are enough:
-    // with 16 rows, or B not transposed, one for every CU (16 x 4096 x 4096 9.6 vs 12.8 us in 16 columns, 16
-    // x 16384 x 4096 29.6 vs 29.0; not transposed 100 x 4096 x 16384, 128 of them, 71 vs 99 in 32, 200, 256 of
-    // them, 112 vs 93); with more rows, each of which narrow workgroups read again, a few less (64 x 6144 x
-    // 4096, 96 of them, 23.6 vs 20.1, but 64 x 4096 x 16384, 64 of them, 47 vs 76).
-    const int rt = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
-    const auto rows_kernel = [&]() {
-        p.any = rows_table(ab, cd)(op_b, rt, 4);
-        if (grid_of(p, *p.any) < (t && rt > 1 ? 96 : 256)) p.any = rows_table(ab, cd)(op_b, rt, t ? 1 : 2);
+    // The kernel for few rows.  Its workgroups load some 50 GB/s each, so a shape costs what one of them
+    // loads, 16 (rt + cg) rows of K, times the rounds of 256; and, in fp32, part of its matrix instructions:
+    // 16 x 4096 x 4096 9.6 us in 16 columns (256 workgroups), 12.8 in 64 (64 of them); 64 x 4096 x 16384 47 in
+    // 64 x 16, 76 in 64 x 64; 64 x 6144 x 4096 23.6 and 20.1; fp32, 64 x 1024 x 8192 53 in 64 x 16, 19 in 16 x 16.
+    const auto rows_kernel = [&](int cg) {
+        double least = 0;
+        for (const int r : {1, 2, 4})
+            for (const int c : {4, t ? 1 : 2}) {
+                const double per = (double)avg / (16 * r) + 0.5;               // row tiles of an expert
+                const double down = d->groups == 1 ? (double)ceil_div(d->rows, 16 * r) : (double)n * (per > 1 ? per : 1);
+                const double grid = down * (double)ceil_div(d->N, 16 * c);
+                const double rounds = grid <= 256 ? 1.0 : d->groups == 1 ? (double)ceil_div((int64_t)grid, 256) : grid / 256;
+                const double cost = rounds * (r + c + (eab == 4 ? 0.4 * r * c : 0.0));
+                if ((cg == 0 || c == cg) && (least == 0 || cost < least)) {
+                    least = cost;
+                    p.any = rows_table(ab, cd)(op_b, r, c);
+                }
+            }
     };
     // Whether that kernel beats the tiles.  One matrix, gelu: up to 64 rows (64 x 65536 x 4096 121 -> 110
     // us), and while its workgroups are one round, or two of long sums (256 x 4096 x 4096 32 -> 21, 384 x
@@ -186,17 +196,19 @@ gemm_status_t gemm_layer_plan_create(gemm_layer_plan_t *out, const gemm_layer_de
     // 52 -> 47 and 53 -> 49, 8 of 2048 x 4096 46 -> 33 and 46 -> 38, but 64 of 2048 x 4096 174 vs 200 and 180 vs
     // 204; 64 rows, 16 of 1024 x 2048 21 vs 25.  Not transposed: 2 rows, 64 of 2048 x 4096 165 -> 157, 8 and
     // 24 rows, 8 of them, 39 -> 26 and 40 -> 38, but 8 rows, 64 of 768 x 2048 38 vs 50.
+    // fp32: always but where 128-wide tiles of the general kernel fill the chip twice over (us, they, 64-wide
+    // ones and this kernel: 1024 x 4096 x 4096 333, 349 and 327, 2048 x 4096 x 1024 168, 187 and 184).
     const auto few_rows = [&]() {
+        if (eab == 4) return avg < 128 || d->N < 128 || tiles < 400;
         if (d->groups == 1) {
-            const int64_t wide = ceil_div(d->rows, 16 * rt) * ceil_div(d->N, 64);
+            const int64_t wide = ceil_div(d->rows, 64) * ceil_div(d->N, 64);
             return d->rows <= 64 || wide <= 256 || (wide <= 512 && d->K >= 8192);
         }
         return t ? avg <= 8 || (avg <= 32 && few <= 1600) : avg <= 4 || few <= 700;
     };
     switch (algo) {
     case GEMM_ALGO_SKINNY:
-        if (rows_ok && tile) p.any = rows_table(ab, cd)(op_b, rt, tile / 16);
-        else if (rows_ok) rows_kernel();
+        if (rows_ok) rows_kernel(tile / 16);
         break;
     case GEMM_ALGO_FAST:
         if (fast_ok) p.fast = fast_table(ab, cd)(op_b, tile ? tile : 128, 0);
@@ -206,7 +218,7 @@ gemm_status_t gemm_layer_plan_create(gemm_layer_plan_t *out, const gemm_layer_de
         break;
     case GEMM_ALGO_AUTO:
         if (rows_ok && few_rows()) {
-            rows_kernel();
+            rows_kernel(0);
         } else {
             if (fast_ok) {
                 // 64-wide tiles also for short ranges of a transposed B: 24 rows, 64 experts of 2048 x 4096 184
