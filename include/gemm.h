@@ -586,7 +586,7 @@ typedef struct {
  */
 gemm_status_t gemm_norm_plan_create(gemm_norm_plan_t *out, const gemm_norm_desc_t *desc);
 
-/* Bytes of workspace that gemm_norm_grad_run needs for dweight or dbias (at most 4 MiB per 1024
+/* Bytes of workspace that gemm_norm_grad_run needs for dweight or dbias (at most 2 MiB per 1024
  * columns). */
 gemm_status_t gemm_norm_workspace_bytes(gemm_norm_plan_t plan, size_t *bytes);
 

@@ -903,7 +903,9 @@ class _WorkspaceBase(_GroupedBase):
             return None, 0
         if workspace is None:
             workspace = self._torch.empty(self.workspace_bytes, dtype=self._torch.uint8, device=f"cuda:{device}")
-        return self._ptr("workspace", workspace, device), workspace.numel()
+        # a raw pointer, as every operand may be one, is taken to have the bytes that are needed
+        have = self.workspace_bytes if isinstance(workspace, int) else workspace.numel()
+        return self._ptr("workspace", workspace, device), have
 
     def _own_stream(self, workspace, needed, stream):
         if needed and workspace is None and stream is not None:

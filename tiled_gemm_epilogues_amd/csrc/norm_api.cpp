@@ -63,7 +63,7 @@ gemm_status_t gemm_norm_plan_create(gemm_norm_plan_t *out, const gemm_norm_desc_
     if (type > GEMM_BF16) return GEMM_STATUS_NOT_SUPPORTED;
     const int es = elem_bytes(type);
     // the kernels step over the rows by less than 2^20 in 32 bits
-    if (d->rows >= LIM31 - (1 << 20) || d->N * es > MAX_ROW_BYTES || d->N >= LIM31 || d->ldx >= LIM31 || d->ldy >= LIM31)
+    if (d->rows >= LIM31 - (1 << 20) || d->N > MAX_ROW_BYTES / es || d->ldx >= LIM31 || d->ldy >= LIM31)
         return GEMM_STATUS_NOT_SUPPORTED;
     gemm_norm_plan p = {};
     p.rows = d->rows; p.N = d->N; p.ldx = d->ldx; p.ldy = d->ldy;
@@ -74,8 +74,8 @@ gemm_status_t gemm_norm_plan_create(gemm_norm_plan_t *out, const gemm_norm_desc_
     p.grad = tge::norm_shape(units, true);
     // as many workgroups as the chip holds at once, each with rows enough to keep the next one's loads
     // in flight
-    const int64_t fw = p.forward.waves * p.forward.teams, gw = p.grad.waves * p.grad.teams;
-    const int64_t most_f = 256 * (16 / fw > 1 ? 16 / fw : 1), most_g = 256 * (8 / gw > 1 ? 8 / gw : 1);
+    const int64_t fw = p.forward.waves * p.forward.teams;
+    const int64_t most_f = 256 * (16 / fw > 1 ? 16 / fw : 1), most_g = 256;
     const int64_t need_f = ceil_div(d->rows, p.forward.teams), need_g = ceil_div(d->rows, p.grad.teams);
     p.grid_forward = need_f < most_f ? need_f : most_f;
     p.grid_grad = need_g < most_g ? need_g : most_g;

@@ -68,7 +68,7 @@ gemm_status_t gemm_route_plan_create(gemm_route_plan_t *out, const gemm_route_de
         d->ldl < d->experts || !in(d->normalize, 0, 1))
         return GEMM_STATUS_INVALID_VALUE;
     if (type > GEMM_BF16 || d->experts > tge::ROUTE_MAX_EXPERTS || d->k > tge::ROUTE_MAX_K || d->ldl >= LIM31 ||
-        d->rows * d->k >= LIM31 - (1 << 20) || d->rows >= LIM31 - (1 << 20))
+        d->rows >= LIM31 - (1 << 20) || d->rows * d->k >= LIM31 - (1 << 20))
         return GEMM_STATUS_NOT_SUPPORTED;
     gemm_route_plan p = {};
     p.rows = d->rows; p.experts = d->experts; p.k = d->k; p.ldl = d->ldl;
