@@ -124,6 +124,29 @@ def test_rows(T):
         check(logits_of(T, T, E, "bf16", ties=True), k, "bf16", False)
 
 
+@pytest.mark.parametrize("E", EXPERTS)
+def test_logits_that_differ_in_their_last_bits(E):
+    # and their zeros of both signs, the smallest and the lowest numbers: everything that a key with fewer
+    # bits than the logit could get wrong, in some of the rows
+    g = torch.Generator().manual_seed(E)
+    T = 300
+    r = lambda n: torch.randint(0, n, (T, E), generator=g)
+    tiny, low = torch.finfo(torch.float32).tiny, torch.finfo(torch.float32).min
+    near = (1 + r(40) * 2.0 ** -23) * torch.where(r(2) == 1, 1.0, -1.0)
+    zeros = torch.where(r(2) == 1, torch.zeros(T, E), -torch.zeros(T, E))
+    small = r(5) * (tiny / 4) - tiny / 2
+    least = torch.where(r(3) == 0, torch.full((T, E), low), torch.full((T, E), -INF))
+    infinite = torch.where(r(E) < 3, torch.full((T, E), -INF), near)
+    rows = torch.arange(T)[:, None] % 7
+    x = torch.randn(T, E, generator=g)
+    for i, other in enumerate((near, zeros, small, least, infinite)):
+        x = torch.where(rows == i, other, x)
+    for k in sorted({1, min(3, E), min(8, E), min(9, E), min(16, E)}):
+        check(x, k, "f32", normalize=k == 3)
+    check(x.half(), min(5, E), "f16", normalize=True)
+    check(x[:9], min(11, E), "f32", normalize=False)
+
+
 def test_all_rows_choose_one_expert():
     for T in (100, 3000):
         x = torch.zeros(T, 64)
