@@ -390,6 +390,35 @@ def test_two_streams_share_a_plan():
     assert torch.equal(D, outs[0])
 
 
+def test_weights_past_the_caches():
+    # few rows of weights of 128 MiB and more: read without the caches, in every shape of the kernel, whole
+    # chunks and a rest, and by expert; the sums are exact
+    for rows, N, K, groups, counts in ((1, 16400, 4104, 1, None), (17, 4100, 16400, 1, None), (60, 16400, 4104, 1, None),
+                                       (40, 2056, 4160, 8, [3, 0, 9, 1, 8, 8, 0, 10])):
+        p = Problem(N + rows, rows, N, K, "T", "bf16", "bf16", groups=groups, counts=counts)
+        plan = p.plan("silu")
+        assert "layer_rows" in plan.describe() and groups * N * K * 2 >= 128 << 20
+        check_forward(p, "silu", plan)
+
+
+def test_refusals_name_the_operand():
+    plan = tge.LayerPlan(8, 16, 16, act="gelu")
+    z = lambda *s: torch.zeros(*s, dtype=torch.float16, device=DEV)
+    A, B, D = z(8, 16), z(16, 16), z(8, 16)
+    for args, err in (((A.cpu(), B, None, D), "A must be a device tensor"), ((A, B[:15], None, D), "B holds"),
+                      ((A, B, None, D[:7]), "D holds")):
+        with pytest.raises(ValueError, match=err):
+            plan.run(*args)
+    with pytest.raises(TypeError, match="pre must be"):
+        plan.run(A, B, None, D, pre=D.float())
+    for call in (lambda: plan.run(A, B, None, D, beta=1.0), lambda: plan.run(A, B, None, D, pre=D),
+                 lambda: plan.run(A, B, D, z(8, 16), pre=D, beta=1.0), lambda: plan.run_grad(A, B, None, D),
+                 lambda: plan.run(A, B, None, D, alpha=NAN),
+                 lambda: tge.LayerPlan(8, 16, 16, 2).run(A, z(2, 16, 16), None, D)):
+        with pytest.raises(tge.GemmError, match="INVALID_VALUE"):
+            call()
+
+
 def test_offsets_beyond_32_bits():
     # D of more than 2^32 bytes: the last rows are where they belong
     rows, N, K = 300000, 8192, 64

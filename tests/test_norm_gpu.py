@@ -203,6 +203,54 @@ def test_in_place():
     assert torch.equal(dX, dX2) and torch.equal(dX, dX3)
 
 
+@pytest.mark.parametrize("type,N", [("f32", 8449), ("f32", 12290), ("bf16", 17925), ("bf16", 25609), ("f16", 4099), ("f32", 259)])
+def test_gradient_added_in_place_where_waves_share_columns(type, N):
+    # the row's last chunk is that of a wave's first lane, and shares columns with the wave before
+    rows = 600
+    X, weight, bias, dY, C = (t.to(DEV) for t in inputs(N, rows, N, type))
+    plan = tge.NormPlan(rows, N, type=type, eps=EPS)
+    Y, mean, rstd = torch.empty_like(X), torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    plan.run(X, weight, bias, Y, mean, rstd)
+    apart, inside = torch.empty_like(X), C.clone()
+    sums = [torch.empty(N, device=DEV) for _ in range(4)]
+    plan.run_grad(dY, X, weight, mean, rstd, apart, sums[0], sums[1], C, 0.5)
+    for turn in range(5):
+        inside.copy_(C)
+        plan.run_grad(dY, X, weight, mean, rstd, inside, sums[2], sums[3], inside, 0.5)
+        assert torch.equal(inside, apart) and torch.equal(sums[0], sums[2]) and torch.equal(sums[1], sums[3])
+    same = X.clone()                                # the forward pass over its own input
+    plan.run(same, weight, bias, same)
+    assert torch.equal(same, Y)
+    own = dY.clone()                                # and the gradient over the one that comes in
+    plan.run_grad(own, X, weight, mean, rstd, own, sums[2], sums[3], C, 0.5)
+    assert torch.equal(own, apart)
+    check_grad(*(t.cpu() for t in (dY, X, weight, mean, rstd, C)), 0.5, apart, sums[0], sums[1], type)
+    # without a weight
+    plan.run_grad(dY, X, None, mean, rstd, apart)
+    one = torch.ones(N, device=DEV)
+    plan.run_grad(dY, X, one, mean, rstd, inside)
+    assert torch.equal(apart, inside)
+    plan.run(X, None, None, Y)
+    plan.run(X, one, torch.zeros(N, device=DEV), same)
+    assert torch.equal(Y, same)
+
+
+def test_refusals_name_the_operand():
+    plan = tge.NormPlan(8, 16, type="f32")
+    X, v, r = torch.zeros(8, 16, device=DEV), torch.zeros(16, device=DEV), torch.zeros(8, device=DEV)
+    for args, err in (((X.cpu(), v, v, X), "X must be a device tensor"), ((X, v[:15], v, X), "weight holds"),
+                      ((X, v, v, X[:7]), "Y holds")):
+        with pytest.raises(ValueError, match=err):
+            plan.run(*args)
+    short = torch.zeros(plan.workspace_bytes - 1, dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError, match="workspace holds"):
+        plan.run_grad(X, X, v, r, r, X.clone(), v.clone(), None, workspace=short)
+    with pytest.raises(ValueError, match="needs a workspace"):
+        plan.run_grad(X, X, v, r, r, X.clone(), v.clone(), None, stream=torch.cuda.Stream())
+    with pytest.raises(tge.GemmError, match="INVALID_VALUE"):
+        plan.run_grad(X, X, v, r, r, X.clone(), beta=1.0)
+
+
 def test_means_far_from_zero_do_not_cancel():
     # deviations of 1 around 1000: the squares of the values would leave no digits of the variance
     for N in (300, 2048, 9000):

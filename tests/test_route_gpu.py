@@ -297,6 +297,24 @@ def test_indices_outside_are_skipped():
     assert out.isfinite().all()
 
 
+def test_refusals_name_the_operand():
+    plan = tge.RoutePlan(3000, 8, 2)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device=DEV)
+    x, args = torch.zeros(3000, 8, device=DEV), [i(3000, 2), torch.zeros(3000, 2, device=DEV), i(6000), i(3000, 2), i(9)]
+    with pytest.raises(ValueError, match="logits must be a device tensor"):
+        plan.run(x.cpu(), *args)
+    with pytest.raises(ValueError, match="offsets holds"):
+        plan.run(x, *args[:4], i(8))
+    with pytest.raises(TypeError, match="mask must be"):
+        plan.run(x, *args, mask=torch.ones(3000, dtype=torch.bool, device=DEV))
+    with pytest.raises(ValueError, match="workspace holds"):
+        plan.run(x, *args, workspace=torch.zeros(plan.workspace_bytes - 1, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError, match="needs a workspace"):
+        plan.run(x, *args, stream=torch.cuda.Stream())
+    with pytest.raises(tge.GemmError, match="INVALID_VALUE"):
+        plan.run(x, None, *args[1:])
+
+
 def test_no_rows():
     plan = tge.RoutePlan(0, 9, 2)
     i, f = torch.zeros(0, dtype=torch.int32, device=DEV), torch.zeros(0, device=DEV)

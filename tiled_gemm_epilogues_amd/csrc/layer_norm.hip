@@ -353,6 +353,9 @@ __global__ __launch_bounds__(W * 64 * TEAMS) void norm_grad(NormParams p) {
                 forget(y[c]);
                 if (!KEEP && p.has_beta) res[c] = part.load(Cm + (int64_t)row * p.ldx, c);
             }
+            // C may be dX: the chunk that is moved back shares columns with the lane before, which may be in
+            // another wave (the other loads stand before the row's exchange)
+            if (!KEEP && p.has_beta) __syncthreads();
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 float (&wc)[VE] = w[KEEP ? c : 0];
