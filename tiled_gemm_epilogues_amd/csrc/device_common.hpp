@@ -317,6 +317,20 @@ __device__ __forceinline__ int wave_scan_add(int v) {
     v += lane_move<0x143, 0xc>(v);
     return v;
 }
+// Sum of the wave's 64 values, the same in every lane (scalar), by the same moves.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float add_moved(float v) {
+    return v + __builtin_bit_cast(float, lane_move<CTRL, ROWS>(__builtin_bit_cast(int, v)));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    v = add_moved<0x111, 0xf>(v);
+    v = add_moved<0x112, 0xf>(v);
+    v = add_moved<0x114, 0xf>(v);
+    v = add_moved<0x118, 0xf>(v);
+    v = add_moved<0x142, 0xa>(v);
+    v = add_moved<0x143, 0xc>(v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
 __device__ __forceinline__ int wave_scan_max(int v) {
     v = max(v, lane_move<0x111, 0xf>(v));
     v = max(v, lane_move<0x112, 0xf>(v));

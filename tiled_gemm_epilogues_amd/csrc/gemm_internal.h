@@ -339,8 +339,8 @@ struct RouteParams {
     // gradient
     const float *dweight, *dloss;    // rows x k; 1 (nullptr: 0)
     void *dlogits;           // ldl
-    // workspace: each workgroup's choices per expert and used rows (blocks x (experts + 1)) and summed
-    // probabilities (blocks x experts)
+    // workspace: ROUTE_MAX_BLOCKS numbers of each expert, the workgroups' choices of it ((experts + 1) of them:
+    // the last are the used rows) and their summed probabilities
     int32_t *hist;
     float *psum;
     int rows, experts, k, ldl, normalize;

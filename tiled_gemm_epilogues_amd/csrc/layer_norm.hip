@@ -28,22 +28,6 @@ namespace {
 
 using namespace dev;
 
-// Sum over the wave's 64 lanes, in every lane (scalar): the data-parallel lane moves of
-// wave_scan_add.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float add_moved(float v) {
-    return v + __builtin_bit_cast(float, lane_move<CTRL, ROWS>(__builtin_bit_cast(int, v)));
-}
-__device__ __forceinline__ float wave_sum(float v) {
-    v = add_moved<0x111, 0xf>(v);
-    v = add_moved<0x112, 0xf>(v);
-    v = add_moved<0x114, 0xf>(v);
-    v = add_moved<0x118, 0xf>(v);
-    v = add_moved<0x142, 0xa>(v);
-    v = add_moved<0x143, 0xc>(v);
-    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
-}
-
 // A lane's part of a row: C chunks of VE elements.  Chunk c stands at column n = (c W 64 + lane) VE; one
 // that would cross the row's end is moved back to end with it, and its first `skip` elements, which the lane
 // before has too, count for nothing: they are left out of sums, and stored twice with equal values.

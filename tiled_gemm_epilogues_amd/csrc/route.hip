@@ -11,8 +11,9 @@
 // A row belongs to 16, 32 or 64 lanes of a wave with up to 16 experts each, so that maxima
 // and sums need a few lane moves and no memory.  The choice compares logits, not probabilities: of
 // equal ones the lowest expert is taken, whatever the rounding of the softmax; NaN and minus
-// infinity are never chosen.  Bound: the logits' bytes for many rows, the moves of the k choices one
-// after another per row, launches for few.
+// infinity are never chosen.  Bound: the instructions of the choice for many rows, launches for few:
+// 65536 rows of 128 fp32 logits (34 MB), 8 chosen, 18.6 us, of which the first loads 3, the choice 9 and the
+// launch and its end 4, and 10.4 us for the places; one row 5.7 us; the gradient 15.4 us (67 MB and the choices: 4.6 TB/s).
 //
 // The order is stable (by expert, then row, then choice) and has no atomics whose order shows: a
 // workgroup counts its choices per expert in LDS, and each choice's place is its expert's start + the
@@ -21,6 +22,8 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "device_common.hpp"
 #include "gemm_internal.h"
@@ -37,19 +40,36 @@ constexpr int ROUTE_THREADS = 256, ROUTE_WAVES = ROUTE_THREADS / 64;   // of the
 __device__ __forceinline__ float as_float(int v) { return __builtin_bit_cast(float, v); }
 __device__ __forceinline__ int as_int(float v) { return __builtin_bit_cast(int, v); }
 
-// v of the lane N places on in the ring of 16 lanes (N a constant), or of the lane 16 or 32 away.
-template <int N>
-__device__ __forceinline__ int ring(int v) { return __builtin_amdgcn_update_dpp(0, v, 0x120 + N, 0xf, 0xf, true); }
+// v of another lane.  MOVE: a data-parallel move inside 16 lanes (N on in their ring; mirrored in 8 lanes; the
+// neighbour, or two on, in 4), or 16 or 32: the lane that far away.
+constexpr int RING = 0x120, MIRROR_8 = 0x141, NEXT_OF_2 = 0xb1, OTHER_2 = 0x4e;
+template <int MOVE>
+__device__ __forceinline__ int moved(int v) {
+    if constexpr (MOVE == 16) return __builtin_amdgcn_ds_swizzle(v, 0x401f);
+    else if constexpr (MOVE == 32) return __shfl_xor(v, 32);
+    else return __builtin_amdgcn_update_dpp(0, v, MOVE, 0xf, 0xf, true);
+}
+// f(move) for the moves after each of which twice as many of the LANES lanes have been joined.
+template <int LANES, class F>
+__device__ __forceinline__ void lane_steps(F f) {
+    if constexpr (LANES == 8) {
+        f(std::integral_constant<int, MIRROR_8>());
+        f(std::integral_constant<int, NEXT_OF_2>());
+        f(std::integral_constant<int, OTHER_2>());
+    } else {
+        f(std::integral_constant<int, RING + 8>());
+        f(std::integral_constant<int, RING + 4>());
+        f(std::integral_constant<int, RING + 2>());
+        f(std::integral_constant<int, RING + 1>());
+        if constexpr (LANES >= 32) f(std::integral_constant<int, 16>());
+        if constexpr (LANES >= 64) f(std::integral_constant<int, 32>());
+    }
+}
 
 // Reduction over a row's lanes, the result in each of them.
 template <int LANES, class Op>
 __device__ __forceinline__ int over_lanes(int v, Op op) {
-    v = op(v, ring<8>(v));
-    v = op(v, ring<4>(v));
-    v = op(v, ring<2>(v));
-    v = op(v, ring<1>(v));
-    if constexpr (LANES >= 32) v = op(v, __builtin_amdgcn_ds_swizzle(v, 0x401f));   // lane ^ 16
-    if constexpr (LANES >= 64) v = op(v, __shfl_xor(v, 32));
+    lane_steps<LANES>([&](auto move) { v = op(v, moved<move.value>(v)); });
     return v;
 }
 template <int LANES>
@@ -265,44 +285,31 @@ __device__ __forceinline__ void scan_experts(int *v, int E) {
     __syncthreads();
 }
 
-__device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-    for (int h = 32; h > 0; h /= 2) v += __shfl_xor(v, h);
-    return v;
-}
-
 // Offsets, slope and loss from the totals: starts[E + 1] and the probabilities' sums (LDS), the used
-// rows.  In 64 bits: one value per expert.
+// rows.
 __device__ void finish_totals(const RouteParams &p, const int *starts, int used, const float *ptotal) {
     const int E = p.experts;
     for (int e = threadIdx.x; e <= E; e += blockDim.x) p.offsets[e] = starts[e];
-    const double scale = used > 0 ? (double)E / p.k / used / used : 0.0;
+    // (in 64 bits: rows have more digits than fp32)
+    const double scale = used > 0 ? (double)E / ((double)p.k * used * used) : 0.0;
     if (p.slope)
         for (int e = threadIdx.x; e < E; e += blockDim.x) p.slope[e] = (float)(scale * (starts[e + 1] - starts[e]));
     if (p.loss && threadIdx.x < 64) {
-        double s = 0.0;
-        for (int e = threadIdx.x; e < E; e += 64) s += scale * (starts[e + 1] - starts[e]) * ptotal[e];
-        s = wave_sum64(s);
-        if (threadIdx.x == 0) p.loss[0] = (float)s;
+        float s = 0.0f;
+        for (int e = threadIdx.x; e < E; e += 64) s = __builtin_fmaf((float)(scale * (starts[e + 1] - starts[e])), ptotal[e], s);
+        s = wave_sum(s);
+        if (threadIdx.x == 0) p.loss[0] = s;
     }
-}
-
-// The key of the same place in the lane 8, 4, 2 or 1 on in the ring of 16 lanes, or 16 or 32 away.
-template <int STEP>
-__device__ __forceinline__ uint32_t key_from(uint32_t v) {
-    if constexpr (STEP <= 8) return (uint32_t)ring<STEP>((int)v);
-    else if constexpr (STEP == 16) return (uint32_t)__builtin_amdgcn_ds_swizzle((int)v, 0x401f);
-    else return (uint32_t)__shfl_xor((int)v, 32);
 }
 
 // One step of a row's choice: of the sorted keys of two lanes the LEN largest, sorted, in both.  The
 // larger of the one's i-th and the other's last-but-i-th are the largest; they rise and fall once, and
-// halving exchanges sort them.
-template <int STEP, int LEN>
-__device__ __forceinline__ void merge_lanes(uint32_t (&v)[LEN]) {
+// halving exchanges sort them.  sent: what the other lane takes.
+template <int MOVE, int LEN>
+__device__ __forceinline__ void merge_lanes(uint32_t (&v)[LEN], const uint32_t (&sent)[LEN]) {
     uint32_t other[LEN];
 #pragma unroll
-    for (int i = 0; i < LEN; ++i) other[i] = key_from<STEP>(v[LEN - 1 - i]);
+    for (int i = 0; i < LEN; ++i) other[i] = (uint32_t)moved<MOVE>((int)sent[LEN - 1 - i]);
 #pragma unroll
     for (int i = 0; i < LEN; ++i) v[i] = max(v[i], other[i]);
 #pragma unroll
@@ -316,156 +323,195 @@ __device__ __forceinline__ void merge_lanes(uint32_t (&v)[LEN]) {
             }
 }
 
-// The k <= LEN largest keys of a row, lane j's result the j-th; keys: the lane's own, sorted.  unsure:
-// (uniform) whether keys may be in the wrong order, see choose_experts.
-template <int LANES, int PER, int LEN, bool EXACT>
-__device__ __forceinline__ uint32_t largest_keys(const uint32_t (&key)[PER], int l, int k, bool &unsure) {
+// Choice of the j-th largest logits, j < k, of the rows of a wave, AT of them per LANES lanes; on return lane j of
+// the u-th of AT parts of the lanes holds the j-th expert of row u (-1: none is left).  A lane's logits
+// become keys of 32 bits, their rank with its last bits replaced by the expert, lowest last, so that one
+// unsigned comparison orders values and experts and no two keys are equal; each lane sorts its own, then lanes
+// merge theirs in pairs (some 35 instructions a step, where taking one maximum after another costs as many
+// for each choice: 65536 rows of 128, 8 chosen, 23 us so).  After a merge both lanes have the same keys; so
+// with two rows at a time the first merge gives one half of the lanes to each, and the others, and all
+// that follows, serve both rows at once.
+//
+// 16-bit logits lose nothing in the key.  fp32 logits lose their last bits: where two keys in order have the
+// same bits left (the first not chosen included) it may be wrong or a tie, and the wave chooses again from
+// the logits themselves.  For random logits that is about one row in a thousand.
+template <class T, int LANES, int PER, int LEN, int AT>
+__device__ __forceinline__ int choose_experts(const float (&x)[AT][PER], int l, int k) {
+    using S = Share<T, LANES, PER>;
+    constexpr bool EXACT = sizeof(T) == 2;
     constexpr uint32_t LAST = LANES * PER - 1;
-    uint32_t v[LEN];
+    constexpr int PART = LANES / AT;
+    static_assert(PART >= LEN, "a lane per choice");
+    const bool second = l >= PART;
+    const int j = l % PART;
+    uint32_t key[AT][PER], all[AT][LEN], v[LEN];
 #pragma unroll
-    for (int i = 0; i < LEN; ++i) v[i] = i < PER ? key[i < PER ? i : 0] : 0u;
-    merge_lanes<8>(v);
-    merge_lanes<4>(v);
-    merge_lanes<2>(v);
-    merge_lanes<1>(v);
-    if constexpr (LANES >= 32) merge_lanes<16>(v);
-    if constexpr (LANES >= 64) merge_lanes<32>(v);
-    uint32_t mine = 0;
+    for (int u = 0; u < AT; ++u) {
 #pragma unroll
-    for (int j = 0; j < LEN; ++j) mine = l == j ? v[j] : mine;
-    if (l >= k) mine = 0;
+        for (int i = 0; i < PER; ++i) key[u][i] = (rank_of(x[u][i]) & ~LAST) | (LAST - S::expert(l, i));
+        sort_keys(key[u]);
+#pragma unroll
+        for (int i = 0; i < LEN; ++i) all[u][i] = i < PER ? key[u][i < PER ? i : 0] : 0u;
+    }
+    if constexpr (AT == 2) {
+        uint32_t sent[LEN];
+#pragma unroll
+        for (int i = 0; i < LEN; ++i) {
+            v[i] = second ? all[1][i] : all[0][i];
+            sent[i] = second ? all[0][i] : all[1][i];
+        }
+        merge_lanes<PART == 8 ? RING + 8 : PART>(v, sent);
+    } else {
+#pragma unroll
+        for (int i = 0; i < LEN; ++i) v[i] = all[0][i];
+    }
+    lane_steps<PART>([&](auto move) {
+        uint32_t sent[LEN];
+#pragma unroll
+        for (int i = 0; i < LEN; ++i) sent[i] = v[i];
+        merge_lanes<move.value>(v, sent);
+    });
+    uint32_t taken = 0;
+#pragma unroll
+    for (int i = 0; i < LEN; ++i) taken = j == i ? v[i] : taken;
+    if (j >= k) taken = 0;
+    int chosen = taken >= LOWEST ? (int)(LAST - (taken & LAST)) : -1;
     if constexpr (!EXACT) {
         // two neighbours of the order with the same bits left
-        const uint32_t next = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine, 0x101, 0xf, 0xf, true);   // lane j + 1's
-        const bool bad = next >= LOWEST && (next ^ mine) <= LAST;
+        const uint32_t next = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)taken, 0x101, 0xf, 0xf, true);   // lane j + 1's
+        const bool bad = j + 1 < k && next >= LOWEST && (next ^ taken) <= LAST;
         // or more keys with the last one's bits, or above, than were chosen.  No row has fewer, so the
         // numbers over the wave are equal only if they are in every row
         uint32_t kth = v[0];
 #pragma unroll
-        for (int j = 1; j < LEN; ++j) kth = j < k ? v[j] : kth;
+        for (int i = 1; i < LEN; ++i) kth = i < k ? v[i] : kth;
         const uint32_t from = max(kth & ~LAST, LOWEST);
         int above = 0;
+        if constexpr (AT == 2) {
+            const uint32_t other = (uint32_t)moved<PART == 8 ? RING + 8 : PART>((int)from);
+            const uint32_t first = second ? other : from, last = second ? from : other;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) above += __popcll(__ballot(key[i] >= from));
-        unsure = __ballot(bad) != 0 || above != __popcll(__ballot(mine >= LOWEST));
-    } else {
-        unsure = false;
-    }
-    return mine;
-}
-
-// Choice of the j-th largest logits, j < k, of the rows of a wave; on return lane j of a row holds the j-th
-// expert (-1: none is left).  A lane's logits become keys of 32 bits, their rank with its last bits
-// replaced by the expert, lowest last, so that one unsigned comparison orders values and experts and no
-// two keys are equal; each lane sorts its own, then lanes merge theirs in pairs (some 35 instructions a
-// step, where taking one maximum after another costs as many for each choice: 65536 rows of 128, 8
-// chosen, 23 us so).  16-bit logits lose nothing in the key.  fp32 logits lose their last
-// bits: where two keys in order have the same bits left (the first not chosen included) it may be wrong or
-// a tie, and the wave chooses again from the logits themselves.  For random logits that is about one
-// row in a thousand.
-template <class T, int LANES, int PER>
-__device__ __forceinline__ int choose_experts(const float (&x)[PER], int l, int k) {
-    using S = Share<T, LANES, PER>;
-    constexpr bool EXACT = sizeof(T) == 2;
-    constexpr uint32_t LAST = LANES * PER - 1;
-    uint32_t key[PER];
+            for (int i = 0; i < PER; ++i) above += __popcll(__ballot(key[0][i] >= first)) + __popcll(__ballot(key[1][i] >= last));
+        } else {
 #pragma unroll
-    for (int v = 0; v < PER; ++v) key[v] = (rank_of(x[v]) & ~LAST) | (LAST - S::expert(l, v));
-    sort_keys(key);
-    bool unsure;
-    const uint32_t taken = k <= 8 ? largest_keys<LANES, PER, 8, EXACT>(key, l, k, unsure)
-                                  : largest_keys<LANES, PER, ROUTE_MAX_K, EXACT>(key, l, k, unsure);
-    int chosen = taken >= LOWEST ? (int)(LAST - (taken & LAST)) : -1;
-    if (!EXACT && unsure) {
-        float left[PER];
-#pragma unroll
-        for (int v = 0; v < PER; ++v) left[v] = x[v] == x[v] ? x[v] : NEG_INF;
+            for (int i = 0; i < PER; ++i) above += __popcll(__ballot(key[0][i] >= from));
+        }
+        if (__ballot(bad) != 0 || above != __popcll(__ballot(taken >= LOWEST))) {
 #pragma unroll 1
-        for (int j = 0; j < k; ++j) {
-            const float best = lanes_max<LANES>(largest(left));
-            int at = 1 << 30;
+            for (int u = 0; u < AT; ++u) {
+                float left[PER];
 #pragma unroll
-            for (int v = PER - 1; v >= 0; --v) at = left[v] == best ? S::expert(l, v) : at;
-            at = lanes_min<LANES>(at);
-            if (best == NEG_INF) at = -1;
+                for (int i = 0; i < PER; ++i) {
+                    const float x0 = x[0][i], x1 = x[AT - 1][i], xi = u == 0 ? x0 : x1;
+                    left[i] = xi == xi ? xi : NEG_INF;
+                }
+#pragma unroll 1
+                for (int n = 0; n < k; ++n) {
+                    const float best = lanes_max<LANES>(largest(left));
+                    int at = 1 << 30;
 #pragma unroll
-            for (int v = 0; v < PER; ++v) left[v] = S::expert(l, v) == at ? NEG_INF : left[v];
-            chosen = l == j ? at : chosen;
+                    for (int i = PER - 1; i >= 0; --i) at = left[i] == best ? S::expert(l, i) : at;
+                    at = lanes_min<LANES>(at);
+                    if (best == NEG_INF) at = -1;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) left[i] = S::expert(l, i) == at ? NEG_INF : left[i];
+                    chosen = l == u * PART + n ? at : chosen;
+                }
+            }
         }
     }
     return chosen;
 }
 
-// ALL: one workgroup does the whole routing.
-template <class T, int LANES, int PER, bool ALL>
+// ALL: one workgroup does the whole routing.  A wave works on AT rows per LANES lanes at a time; LEN: the
+// most choices.
+template <class T, int LANES, int PER, int LEN, int AT, bool ALL>
 __global__ __launch_bounds__(route_waves(LANES *PER) * 64) void choose(RouteParams p) {
-    constexpr int ROWS = 64 / LANES;                 // rows of a wave at a time
+    constexpr int ROWS = 64 / LANES;                 // groups of lanes
     constexpr int WIDTH = LANES * PER;               // experts, rounded up
     constexpr int WAVES = route_waves(WIDTH), THREADS = WAVES * 64, SLOTS = WAVES * ROWS;
+    constexpr int PART = LANES / AT;
     __shared__ int counts[WIDTH];
     __shared__ int starts[WIDTH + 1];
     __shared__ float ptotal[WIDTH];
     // the rows at work, then the waves' summed probabilities, then their counters
-    __shared__ __attribute__((aligned(16))) int shared[SLOTS * WIDTH];
+    __shared__ __attribute__((aligned(16))) int shared[AT * SLOTS * WIDTH];
     __shared__ int used_rows[WAVES];
     __shared__ int kept[ALL ? route_one_rows(WAVES, LANES) * ROUTE_MAX_K : 1];   // the choices, for their places
     const int E = p.experts, k = p.k;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     using S = Share<T, LANES, PER>;
     const int slot = lane / LANES, l = lane % LANES;
+    const int part = l / PART, j = l % PART;         // the row whose j-th choice is this lane's
     const int row0 = blockIdx.x * p.block_rows, rows = min(p.block_rows, p.rows - row0);
     const T *logits = static_cast<const T *>(p.logits) + (int64_t)row0 * p.ldl;
-    float *const psum = reinterpret_cast<float *>(shared), *const values = psum + (wave * ROWS + slot) * WIDTH;
+    float *const psum = reinterpret_cast<float *>(shared), *const values = psum + (wave * ROWS + slot) * AT * WIDTH;
     for (int e = threadIdx.x; e < WIDTH; e += THREADS) counts[e] = 0;
     __syncthreads();
-    float ps[PER], next[PER];
+    float ps[PER], next[AT][PER];
 #pragma unroll
     for (int v = 0; v < PER; ++v) ps[v] = 0.0f;
     int used = 0;
-    int next_on = 0;
+    int next_on[AT];
     // (loads side by side, none waiting for another)
     auto fetch = [&](int r) {
-        next_on = r < rows;
-        if (r < rows) {
-            if (p.mask) next_on = p.mask[row0 + r];
-            S::load(logits + (int64_t)r * p.ldl, l, E, next);
+#pragma unroll
+        for (int u = 0; u < AT; ++u) {
+            const int at = r + u * SLOTS;
+            next_on[u] = at < rows;
+            if (at < rows) {
+                if (p.mask) next_on[u] = p.mask[row0 + at];
+                S::load(logits + (int64_t)at * p.ldl, l, E, next[u]);
+            }
         }
     };
     const int end = (rows + ROWS - 1) / ROWS * ROWS; // (a wave's rows stay together)
     fetch(wave * ROWS + slot);
 #pragma unroll 1
-    for (int r = wave * ROWS + slot; r < end; r += SLOTS) {
-        const int64_t row = row0 + r;
-        float x[PER];
+    for (int r = wave * ROWS + slot; r < end; r += AT * SLOTS) {
+        float x[AT][PER];
 #pragma unroll
-        for (int v = 0; v < PER; ++v) x[v] = next_on ? next[v] : NEG_INF;
-        if (end - r > SLOTS) fetch(r + SLOTS);
-        // the row in LDS, where its lanes find the chosen logits
+        for (int u = 0; u < AT; ++u)
 #pragma unroll
-        for (int v = 0; v < PER; ++v) values[S::expert(l, v)] = x[v];
-        const int chosen = choose_experts<T, LANES, PER>(x, l, k);
+            for (int v = 0; v < PER; ++v) x[u][v] = next_on[u] ? next[u][v] : NEG_INF;
+        if (end - r > AT * SLOTS) fetch(r + AT * SLOTS);
+        // the rows in LDS, where their lanes find the chosen logits
+#pragma unroll
+        for (int u = 0; u < AT; ++u)
+#pragma unroll
+            for (int v = 0; v < PER; ++v) values[u * WIDTH + S::expert(l, v)] = x[u][v];
+        const int chosen = choose_experts<T, LANES, PER, LEN, AT>(x, l, k);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        const float value = chosen >= 0 ? values[chosen] : 0.0f;
+        const float value = chosen >= 0 ? values[part * WIDTH + chosen] : 0.0f;
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        const float m = lanes_max<LANES>(largest(x));
-        const float s = exponentials<LANES>(x, m), inv = s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);
+        float m = 0.0f, s = 0.0f, inv = 0.0f;
 #pragma unroll
-        for (int v = 0; v < PER; ++v) ps[v] = __builtin_fmaf(x[v], inv, ps[v]);
-        if (m > NEG_INF && l == 0) ++used;
+        for (int u = 0; u < AT; ++u) {
+            const float mu = lanes_max<LANES>(largest(x[u]));
+            const float su = exponentials<LANES>(x[u], mu), iu = su == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(su);
+#pragma unroll
+            for (int v = 0; v < PER; ++v) ps[v] = __builtin_fmaf(x[u][v], iu, ps[v]);
+            if (mu > NEG_INF && l == 0) ++used;
+            m = part == u ? mu : m;
+            s = part == u ? su : s;
+            inv = part == u ? iu : inv;
+        }
         float w = chosen >= 0 ? __builtin_amdgcn_exp2f((value - m) * ROUTE_LOG2E) : 0.0f;
         // NaN among the logits makes the weights NaN
         if (p.normalize) {
-            const float all = lanes_sum<LANES>(w);
+            const float all = lanes_sum<PART>(w);
             w = s == s ? (chosen >= 0 ? w * __builtin_amdgcn_rcpf(all) : 0.0f) : chosen >= 0 ? s : 0.0f;
         } else {
             w *= chosen >= 0 ? inv : 0.0f;
         }
-        if (r < rows && l < k) {
-            p.index[row * k + l] = chosen;
-            p.weight[row * k + l] = w;
-            if constexpr (ALL) kept[r * k + l] = chosen;
+        const int at = r + part * SLOTS;
+        if (at < rows && j < k) {
+            const int64_t to = (int64_t)(row0 + at) * k + j;
+            p.index[to] = chosen;
+            p.weight[to] = w;
+            if constexpr (ALL) kept[at * k + j] = chosen;
             if (chosen >= 0) atomicAdd(&counts[chosen], 1);
         }
     }
@@ -491,12 +537,12 @@ __global__ __launch_bounds__(route_waves(LANES *PER) * 64) void choose(RoutePara
             ptotal[e] = t;
             starts[e] = counts[e];
         } else {
-            p.psum[(int64_t)blockIdx.x * E + e] = t;
-            p.hist[(int64_t)blockIdx.x * (E + 1) + e] = counts[e];
+            p.psum[(int64_t)e * ROUTE_MAX_BLOCKS + blockIdx.x] = t;
+            p.hist[(int64_t)e * ROUTE_MAX_BLOCKS + blockIdx.x] = counts[e];
         }
     }
     if constexpr (!ALL) {
-        if (threadIdx.x == 0) p.hist[(int64_t)blockIdx.x * (E + 1) + E] = all_used;
+        if (threadIdx.x == 0) p.hist[(int64_t)E * ROUTE_MAX_BLOCKS + blockIdx.x] = all_used;
     } else {
         __syncthreads();
         scan_experts(starts, E);
@@ -507,66 +553,70 @@ __global__ __launch_bounds__(route_waves(LANES *PER) * 64) void choose(RoutePara
     }
 }
 
-// The rest for several workgroups: each sums the counts of all and of those before it (every thread
-// those of one expert over a run of workgroups; no launch between) and places its choices; one more
-// writes the totals.
+// The rest for several workgroups: each sums the counts of all and of those before it (no launch between) and
+// places its choices; one more writes the totals.  The counts and probabilities of an expert stand side by
+// side, ROUTE_MAX_BLOCKS of each, so that a wave has them with one load.
 constexpr int PLACE_THREADS = 1024, PLACE_COUNTERS = 8192;
-__global__ __launch_bounds__(PLACE_THREADS) void place_blocks(RouteParams p) {
-    static_assert(PLACE_COUNTERS >= 2 * (PLACE_THREADS + ROUTE_MAX_EXPERTS + 1), "runs of counters");
-    __shared__ int hist[PLACE_COUNTERS];             // the runs' sums, then the waves' counters
+__global__ __launch_bounds__(PLACE_THREADS, 8) void place_blocks(RouteParams p) {
+    static_assert(ROUTE_MAX_BLOCKS == 64 * 4, "four workgroups to a lane");
+    typedef int i32x4a __attribute__((ext_vector_type(4), aligned(4)));
+    typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
+    constexpr int WAVES = PLACE_THREADS / 64, SIDE = 8;
+    __shared__ int hist[PLACE_COUNTERS];             // the waves' counters
     __shared__ int starts[ROUTE_MAX_EXPERTS + 1], before[ROUTE_MAX_EXPERTS + 1];
-    const int E = p.experts, cols = E + 1, me = blockIdx.x;
+    const int E = p.experts, me = blockIdx.x;
     const bool totals = me == p.blocks;
     const int row0 = me * p.block_rows;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    float *const ptotal = reinterpret_cast<float *>(before);
     Choices<false> mine;
     mine.init(p, p.index + (int64_t)row0 * p.k, totals ? 0 : min(p.block_rows, p.rows - row0), PLACE_COUNTERS);
-    const int runs = max(PLACE_THREADS / cols, 1), per = (p.blocks + runs - 1) / runs;
-    for (int i = threadIdx.x; i < runs * cols; i += PLACE_THREADS) {   // (one turn, or two with 1024 experts)
-        const int run = i / cols, e = i - run * cols;
-        const int b0 = min(run * per, p.blocks), b1 = min(b0 + per, p.blocks), bm = min(max(me, b0), b1);
-        const int *h = p.hist + e;
-        int low = 0, high = 0;
-#pragma unroll 16
-        for (int b = b0; b < bm; ++b) low += h[(int64_t)b * cols];
-#pragma unroll 16
-        for (int b = bm; b < b1; ++b) high += h[(int64_t)b * cols];
-        hist[2 * i] = low;
-        hist[2 * i + 1] = low + high;
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < cols; e += PLACE_THREADS) {
-        int low = 0, all = 0;
-        for (int r = 0; r < runs; ++r) {
-            low += hist[2 * (r * cols + e)];
-            all += hist[2 * (r * cols + e) + 1];
+    // (lanes past the last workgroup read the first ones' and drop them)
+    const int b0 = 4 * lane < p.blocks ? 4 * lane : 0, have = min(max(p.blocks - 4 * lane, 0), 4), low_have = min(max(me - 4 * lane, 0), 4);
+    for (int e0 = wave; e0 <= E; e0 += WAVES * SIDE) {
+        i32x4a h[SIDE];
+#pragma unroll
+        for (int n = 0; n < SIDE; ++n) h[n] = *reinterpret_cast<const i32x4a *>(p.hist + (int64_t)min(e0 + n * WAVES, E) * ROUTE_MAX_BLOCKS + b0);
+#pragma unroll
+        for (int n = 0; n < SIDE; ++n) {
+            const int e = e0 + n * WAVES;
+            if (e > E) break;
+            int all = 0, low = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                all += i < have ? h[n][i] : 0;
+                low += i < low_have ? h[n][i] : 0;
+            }
+            all = wave_scan_add(all);
+            low = wave_scan_add(low);
+            if (lane == 63) {
+                starts[e] = all;
+                if (!totals) before[e] = low;
+            }
         }
-        before[e] = low;
-        starts[e] = all;
+    }
+    if (totals && p.loss) {
+        for (int e0 = wave; e0 < E; e0 += WAVES * SIDE) {
+            f32x4a q[SIDE];
+#pragma unroll
+            for (int n = 0; n < SIDE; ++n) q[n] = *reinterpret_cast<const f32x4a *>(p.psum + (int64_t)min(e0 + n * WAVES, E - 1) * ROUTE_MAX_BLOCKS + b0);
+#pragma unroll
+            for (int n = 0; n < SIDE; ++n) {
+                const int e = e0 + n * WAVES;
+                if (e >= E) break;
+                float t = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t += i < have ? q[n][i] : 0.0f;
+                t = wave_sum(t);
+                if (lane == 0) ptotal[e] = t;
+            }
+        }
     }
     __syncthreads();
     const int used = starts[E];
     __syncthreads();
     scan_experts(starts, E);
     if (totals) {
-        float *const ptotal = reinterpret_cast<float *>(before);
-        double *const part = reinterpret_cast<double *>(hist);
-        static_assert(PLACE_COUNTERS >= 2 * (PLACE_THREADS + ROUTE_MAX_EXPERTS), "runs of sums");
-        const int sums = max(PLACE_THREADS / E, 1), each = (p.blocks + sums - 1) / sums;
-        for (int i = threadIdx.x; p.loss && i < sums * E; i += PLACE_THREADS) {
-            const int run = i / E, e = i - run * E;
-            const int b0 = min(run * each, p.blocks), b1 = min(b0 + each, p.blocks);
-            double t = 0.0;
-#pragma unroll 16
-            for (int b = b0; b < b1; ++b) t += p.psum[(int64_t)b * E + e];
-            part[i] = t;
-        }
-        __syncthreads();
-        for (int e = threadIdx.x; p.loss && e < E; e += PLACE_THREADS) {
-            double t = 0.0;
-            for (int r = 0; r < sums; ++r) t += part[r * E + e];
-            ptotal[e] = (float)t;
-        }
-        __syncthreads();
         finish_totals(p, starts, used, ptotal);
         return;
     }
@@ -665,11 +715,25 @@ __global__ __launch_bounds__(ROUTE_THREADS) void grad(RouteParams p) {
     }
 }
 
-template <class T, int LANES, int PER>
+template <class T, int LANES, int PER, int LEN>
 hipError_t launch_choose(const RouteParams &p, hipStream_t s) {
-    constexpr int THREADS = route_waves(LANES * PER) * 64;
-    if (p.blocks == 1) hipLaunchKernelGGL((choose<T, LANES, PER, true>), dim3(1), dim3(THREADS), 0, s, p);
-    else hipLaunchKernelGGL((choose<T, LANES, PER, false>), dim3(p.blocks), dim3(THREADS), 0, s, p);
+    constexpr int WIDTH = LANES * PER, WAVES = route_waves(WIDTH), SLOTS = WAVES * 64 / LANES;
+    // two rows at a time where every wave has them (us, one and two: 131072 rows of 16, 2 chosen, 22.0 and 17.2;
+    // 65536 of 64, 6 chosen, 20.9 and 18.5; 16384 of 256, 8 chosen, 24.7 and 23.4; but 16384 of 64, one to a wave,
+    // 13.1 and 14.7) and the registers for them (16384 of 1024, 16 chosen, 103 and 117)
+    constexpr bool PAIRS = LANES / 2 >= LEN && WIDTH <= 512;
+    const dim3 grid(p.blocks), threads(WAVES * 64);
+    if (p.blocks == 1) {
+        hipLaunchKernelGGL((choose<T, LANES, PER, LEN, 1, true>), grid, threads, 0, s, p);
+        return hipGetLastError();
+    }
+    if constexpr (PAIRS) {
+        if (p.block_rows >= 2 * SLOTS) {
+            hipLaunchKernelGGL((choose<T, LANES, PER, LEN, 2, false>), grid, threads, 0, s, p);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((choose<T, LANES, PER, LEN, 1, false>), grid, threads, 0, s, p);
     return hipGetLastError();
 }
 template <class T, int LANES, int PER>
@@ -683,7 +747,7 @@ hipError_t by_shape(const RouteParams &p, RouteShape s, unsigned grid, hipStream
 #define TGE_ROUTE_CASE(L, P)                                                     \
     case (L) * 32 + (P):                                                         \
         if constexpr (GRAD) return launch_grad<T, L, P>(p, grid, stream);        \
-        else return launch_choose<T, L, P>(p, stream)
+        else return p.k <= 8 ? launch_choose<T, L, P, 8>(p, stream) : launch_choose<T, L, P, ROUTE_MAX_K>(p, stream)
     switch (s.lanes * 32 + s.per) {
         TGE_ROUTE_CASE(16, 1);
         TGE_ROUTE_CASE(16, 2);
