@@ -28,9 +28,9 @@ hipError_t launch(const LayerParams &p, unsigned grid, hipStream_t) {
     require(!p.has_beta || p.C, "C");
     const int64_t line = (int64_t)p.lda * ES;
     if (KIND == DIRECT)
-        require(ES == 2 && p.K >= 64 && whole(p.A, 16) && whole(p.B, 16) && p.lda % 8 == 0 && p.ldb % 8 == 0 &&
-                    p.stride_b % 8 == 0 && (OPB || p.N % 8 == 0) && line * 256 < (int64_t)1 << 31, "direct loads");
-    if (KIND == STAGED) require(ES == 2 && p.K > 0 && p.N >= 8 && line * 256 < (int64_t)1 << 31, "staged loads");
+        require(p.K * ES >= 128 && whole(p.A, 16) && whole(p.B, 16) && p.lda * ES % 16 == 0 && p.ldb * ES % 16 == 0 &&
+                    p.stride_b * ES % 16 == 0 && (OPB || p.N * ES % 16 == 0) && line * 256 < (int64_t)1 << 31, "direct loads");
+    if (KIND == STAGED) require(p.K > 0 && p.N * ES >= 16 && line * 256 < (int64_t)1 << 31, "staged loads");
     if (KIND == ROWS) require(p.K * ES >= 16 && (OPB || p.N * ES >= 16) && line * 64 < (int64_t)1 << 31, "few rows");
     ++layer_launches;
     return hipSuccess;
@@ -48,10 +48,11 @@ template <int ES>
 const LayerEntry *any(int op_b, int cfg) {
     return cfg == CFG_128 ? of<128, 128, ANY, ES>(op_b, "any128") : cfg == CFG_64 ? of<64, 64, ANY, ES>(op_b, "any64") : nullptr;
 }
+template <int ES>
 const LayerEntry *fast(int op_b, int tile, int rs) {
-    if (rs) return tile == 128 ? of<128, 128, STAGED, 2>(op_b, "rs") : tile == 64 ? of<64, 64, STAGED, 2>(op_b, "rs64") : nullptr;
-    return tile == 256 ? of<256, 256, DIRECT, 2>(op_b, "fast256") : tile == 128 ? of<128, 128, DIRECT, 2>(op_b, "fast128")
-           : tile == 64 ? of<64, 64, DIRECT, 2>(op_b, "fast64") : nullptr;
+    if (rs) return tile == 128 ? of<128, 128, STAGED, ES>(op_b, "rs") : tile == 64 ? of<64, 64, STAGED, ES>(op_b, "rs64") : nullptr;
+    return tile == 256 ? of<256, 256, DIRECT, ES>(op_b, "fast256") : tile == 128 ? of<128, 128, DIRECT, ES>(op_b, "fast128")
+           : tile == 64 ? of<64, 64, DIRECT, ES>(op_b, "fast64") : nullptr;
 }
 template <int BM, int ES>
 const LayerEntry *rows_of(int op_b, int cg) {
@@ -99,10 +100,11 @@ const LayerEntry *layer_any_f16_f16(int b, int c) { return any<2>(b, c); }
 const LayerEntry *layer_any_f16_f32(int b, int c) { return any<2>(b, c); }
 const LayerEntry *layer_any_bf16_bf16(int b, int c) { return any<2>(b, c); }
 const LayerEntry *layer_any_bf16_f32(int b, int c) { return any<2>(b, c); }
-const LayerEntry *layer_fast_f16_f16(int b, int t, int r) { return fast(b, t, r); }
-const LayerEntry *layer_fast_f16_f32(int b, int t, int r) { return fast(b, t, r); }
-const LayerEntry *layer_fast_bf16_bf16(int b, int t, int r) { return fast(b, t, r); }
-const LayerEntry *layer_fast_bf16_f32(int b, int t, int r) { return fast(b, t, r); }
+const LayerEntry *layer_fast_f32_f32(int b, int t, int r) { return fast<4>(b, t, r); }
+const LayerEntry *layer_fast_f16_f16(int b, int t, int r) { return fast<2>(b, t, r); }
+const LayerEntry *layer_fast_f16_f32(int b, int t, int r) { return fast<2>(b, t, r); }
+const LayerEntry *layer_fast_bf16_bf16(int b, int t, int r) { return fast<2>(b, t, r); }
+const LayerEntry *layer_fast_bf16_f32(int b, int t, int r) { return fast<2>(b, t, r); }
 const LayerEntry *layer_rows_f32_f32(int b, int r, int c) { return rows<4>(b, r, c); }
 const LayerEntry *layer_rows_f16_f16(int b, int r, int c) { return rows<2>(b, r, c); }
 const LayerEntry *layer_rows_f16_f32(int b, int r, int c) { return rows<2>(b, r, c); }

@@ -206,13 +206,17 @@ def test_layer_kernel_choice():
     assert _kernel(L(64, 2048, 4096, 64)).startswith("layer_rows_16x")
     f = dict(ab="f32", cd="f32")
     assert _kernel(L(64, 1024, 8192, **f)) == "layer_rows_16x16"
-    assert _kernel(L(1024, 4096, 4096, **f)) == "layer_rows_64x64"
-    assert _kernel(L(2048, 4096, 4096, **f)) == "gemm_mfma_128x128"
+    assert _kernel(L(128, 4096, 4096, **f)) == "layer_rows_32x64"
+    assert _kernel(L(256, 4096, 4096, **f)) == "gemm_fast_64x64"
+    assert _kernel(L(2048, 4096, 4096, **f)) == "gemm_fast_128x128"
+    assert _kernel(L(2048, 4095, 4095, **f)) == "gemm_fast_128x128_rs"
+    assert _kernel(L(300, 8191, 511, **f)) == "gemm_fast_64x64_rs"
+    assert _kernel(L(8, 1024, 2048, 16, **f)).startswith("layer_rows_16x")
     assert _kernel(L(64, 64, 7)) == "gemm_fast_64x64_rs"
     # sums and rows too short for whole loads, and pinned kernels whose preconditions do not hold: the
     # general one
-    for p in (L(64, 7, 64, op_b="N", algo="skinny"), L(64, 64, 3, **f), L(64, 64, 0),
-              L(64, 64, 7, algo="fast"), L(64, 64, 64, algo="staged", **f)):
+    for p in (L(64, 7, 64, op_b="N", algo="skinny"), L(64, 3, 3, **f), L(64, 64, 0), L(64, 64, 0, **f),
+              L(64, 64, 7, algo="fast"), L(64, 64, 30, algo="fast", **f)):
         assert _kernel(p).startswith("gemm_mfma"), p.describe()
 
 

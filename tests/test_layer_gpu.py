@@ -134,7 +134,7 @@ def check_grad(p, act, plan, in_place=False):
     untouched(p, used, D)
 
 
-@pytest.mark.parametrize("ab,cd", PAIRS)
+@pytest.mark.parametrize("ab,cd", PAIRS + [("f32", "f32")])
 @pytest.mark.parametrize("op_b", ["N", "T"])
 @pytest.mark.parametrize("algo,tile", KERNELS)
 def test_every_kernel(algo, tile, op_b, ab, cd):
@@ -149,7 +149,7 @@ def test_every_kernel(algo, tile, op_b, ab, cd):
         check_forward(p, "gelu", p.plan("gelu", algo, tile_of(algo, tile, op_b)), bias=False, residual=False, pre=False)
 
 
-@pytest.mark.parametrize("ab,cd", PAIRS)
+@pytest.mark.parametrize("ab,cd", PAIRS + [("f32", "f32")])
 @pytest.mark.parametrize("op_b", ["N", "T"])
 @pytest.mark.parametrize("algo,tile", KERNELS)
 def test_ranges_in_every_kernel(algo, tile, op_b, ab, cd):
@@ -162,7 +162,7 @@ def test_ranges_in_every_kernel(algo, tile, op_b, ab, cd):
 
 
 @pytest.mark.parametrize("op_b", ["N", "T"])
-@pytest.mark.parametrize("algo,tile", [("general", 64), ("general", 128), ("skinny", 64), ("skinny", 16)])
+@pytest.mark.parametrize("algo,tile", [k for k in KERNELS if k[0] != "fast"])
 def test_fp32(algo, tile, op_b):
     tile = tile_of(algo, tile, op_b)
     for i, (rows, N, K, groups, counts) in enumerate([(130, 140, 70, 1, None), (1, 1, 1, 1, None),

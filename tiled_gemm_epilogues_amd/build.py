@@ -58,8 +58,8 @@ def steps():
     # the same kernels with a layer's epilogue
     for pair in GROUPED_PAIRS + ["F32_F32"]:
         add("layer_rows.hip", f"layer_rows_{pair.lower()}", f"-DTGE_PAIR_{pair}")
-    for name, pairs in (("gemm_kernels", GROUPED_PAIRS + ["F32_F32"]), ("gemm_fast", GROUPED_PAIRS)):
-        for pair in pairs:
+    for name in ("gemm_kernels", "gemm_fast"):
+        for pair in GROUPED_PAIRS + ["F32_F32"]:
             add(name + ".hip", f"layer_{name}_{pair.lower()}", f"-DTGE_PAIR_{pair}", "-DTGE_LAYER")
     for name in ("layer_norm", "route"):
         for t in TYPES:

@@ -52,8 +52,14 @@
 //    without it).  128-wide gradients wait for their slabs, two stages deep (MFMAs a third busy), and
 //    store fp32 sums: 16384 rows, 16 of 4096 x 2048, 366 us (0.75 PFLOP/s).  64-wide ones fill the
 //    chip where the others leave CUs empty: 1003 rows, 8 gradients of 1024 x 704, 8.4 us.
+//  * a layer's products (GRP = GROUP_LAYER) are the same with the epilogue of layer_epilogue.hpp, and
+//    have fp32 instances: slabs of 32 k, four 16x16x4 instructions to a fragment, [k][mn] operands
+//    read one k at a time.  These take so long (32 cycles each) that everything else hides behind
+//    them: 8192 x 16384 x 4096 bf16 with gelu and z kept 881 us (1.25 PFLOP/s), its gradient 873; fp32 2048 x
+//    4096 x 4096 463 us in 128-wide tiles (148 TFLOP/s of the 157 there are), 256 x 4096 x 4096 72 us in
+//    64-wide ones.
 //
-// Preconditions (checked by the host): 16- or 8-bit inputs and K of at least one slab; for the
+// Preconditions (checked by the host): 16- or 8-bit (a layer's: also 32-bit) inputs and K of at least one slab; for the
 // direct loads also A/B base pointers, leading dimensions and batch strides 16-byte aligned and
 // M (if A is stored transposed) and N (if B is not transposed) multiples of 16 bytes' worth of
 // elements, or stored rows zero-padded to whole chunks (the copies); for the register-staged
@@ -123,6 +129,10 @@ __device__ __forceinline__ int swz_mc(int k) {
         // of a k group read 4 rows at 2 adjacent chunks, the group served with it 16 rows on
         static_assert(MF == 16, "16x16 shape");
         return (((k >> 1) & 1) << 1) | (((k >> 4) & 1) << 2);
+    } else if constexpr (E == 4) {
+        // 32-bit rows of TL / 4 chunks (a multiple of all banks): the 16 lanes of a k group read 4 adjacent
+        // chunks of one row, the other groups rows 4 apart: each group its quarter of the banks
+        return ((k >> 2) & 3) << 2;
     } else if constexpr (E == 2) {
         const int q = k & 3;
         return (4 * q + 2 * (q >> 1)) ^ (MF == 16 ? ((k >> 4) & 1) << 1 : 0);
@@ -304,6 +314,10 @@ struct Frag {
 #pragma unroll
                 for (int j = 0; j < S::NS; ++j)
                     addr[t][j] = opbase + (uint32_t)off_kc(r, (S::KSB / 16) * j + kgrp<MF>(lg));
+            } else if constexpr (E == 4) {
+                // no transposing read of 32-bit elements: one read per k, lane i of a group column i
+                const int k = 4 * kgrp<MF>(lg), col = wrow + MF * t + lr;
+                addr[t][0] = opbase + (uint32_t)(k * ROWB + (((col >> 2) ^ swz_mc<4, MF, TL>(k)) << 4) + (col & 3) * 4);
             } else if constexpr (E == 2) {
                 // ds_read_b64_tr_b16: in each group of 16 lanes, lane i receives element i % 4
                 // of the 8-byte chunks addressed by lanes i/4 + 4e, e = 0..3.  Lane a of the
@@ -328,6 +342,11 @@ struct Frag {
     __device__ __forceinline__ void read(int stage, int t, int j, u32x4 &dst) const {
         if constexpr (KC) {
             dst = *(const __attribute__((address_space(3))) u32x4 *)(uintptr_t)(addr[t][j] + stage * KCB);
+        } else if constexpr (E == 4) {
+            // k rows j*KS/4 + (0..3) past the lane's base: the same swizzle
+            const uint32_t a = addr[t][0] + stage * KCB + ((S::KSB / 4) * j) * ROWB;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[e] = *(const __attribute__((address_space(3))) uint32_t *)(uintptr_t)(a + e * ROWB);
         } else if constexpr (E == 2) {
             // k rows j*KS/2 + (0..3) and + (4..7) past the lane's base: the swizzle depends on
             // k & 3 and (16x16 shape) k bit 4, which these offsets leave unchanged
@@ -982,7 +1001,9 @@ const LayerEntry *lookup_layer(int op_b, int tile, int rs) {
 }  // namespace
 
 #if defined(TGE_LAYER)
-#if defined(TGE_PAIR_F16_F16)
+#if defined(TGE_PAIR_F32_F32)
+const LayerEntry *layer_fast_f32_f32(int b, int t, int rs) { return lookup_layer<TF32, OF32>(b, t, rs); }
+#elif defined(TGE_PAIR_F16_F16)
 const LayerEntry *layer_fast_f16_f16(int b, int t, int rs) { return lookup_layer<TF16, OF16>(b, t, rs); }
 #elif defined(TGE_PAIR_F16_F32)
 const LayerEntry *layer_fast_f16_f32(int b, int t, int rs) { return lookup_layer<TF16, OF32>(b, t, rs); }
@@ -991,7 +1012,7 @@ const LayerEntry *layer_fast_bf16_bf16(int b, int t, int rs) { return lookup_lay
 #elif defined(TGE_PAIR_BF16_F32)
 const LayerEntry *layer_fast_bf16_f32(int b, int t, int rs) { return lookup_layer<TBF16, OF32>(b, t, rs); }
 #else
-#error "define one TGE_PAIR_* macro of a 16-bit float type"
+#error "define one TGE_PAIR_* macro of a float type"
 #endif
 #elif defined(TGE_GROUPED)
 // the grouped instances are a build of their own (one object per type pair)

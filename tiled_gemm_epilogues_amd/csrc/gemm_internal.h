@@ -241,6 +241,7 @@ const LayerEntry *layer_any_f16_f16(int op_b, int cfg);
 const LayerEntry *layer_any_f16_f32(int op_b, int cfg);
 const LayerEntry *layer_any_bf16_bf16(int op_b, int cfg);
 const LayerEntry *layer_any_bf16_f32(int op_b, int cfg);
+const LayerEntry *layer_fast_f32_f32(int op_b, int tile, int rs);
 const LayerEntry *layer_fast_f16_f16(int op_b, int tile, int rs);
 const LayerEntry *layer_fast_f16_f32(int op_b, int tile, int rs);
 const LayerEntry *layer_fast_bf16_bf16(int op_b, int tile, int rs);

@@ -2,6 +2,7 @@
 // creation and validation, kernel choice, launch.  Host code only; the kernels are the layer
 // instances of gemm_kernels.hip and gemm_fast.hip, and layer_rows.hip.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <stdio.h>
 
@@ -26,7 +27,7 @@ struct gemm_layer_plan {
 
 namespace {
 
-constexpr int64_t FAST_MIN_K = 64;         // one slab of the fast kernel (16-bit inputs)
+constexpr int64_t SLAB_BYTES = 128;        // of K: the fast kernel needs one
 
 using TableFn = const LayerEntry *(*)(int, int);
 using FastFn = const LayerEntry *(*)(int, int, int);
@@ -40,8 +41,9 @@ TableFn any_table(int ab, int cd) {
     return nullptr;
 }
 
-// The tables of the fast kernel (nullptr for fp32) and of the one for few rows.
+// The tables of the fast kernel and of the one for few rows.
 FastFn fast_table(int ab, int cd) {
+    if (ab == GEMM_F32) return tge::layer_fast_f32_f32;
     if (ab == GEMM_F16) return cd == GEMM_F16 ? tge::layer_fast_f16_f16 : tge::layer_fast_f16_f32;
     if (ab == GEMM_BF16) return cd == GEMM_BF16 ? tge::layer_fast_bf16_bf16 : tge::layer_fast_bf16_f32;
     return nullptr;
@@ -164,11 +166,19 @@ gemm_status_t gemm_layer_plan_create(gemm_layer_plan_t *out, const gemm_layer_de
     const bool small = algo == GEMM_ALGO_GENERAL && tile ? tile == 64 : avg < 128 || d->N < 128;
     p.any = any_table(ab, cd)(op_b, small ? tge::CFG_64 : tge::CFG_128);
     const bool offsets_ok = d->lda * eab * 256 < LIM31;                    // 32-bit offsets within a tile's rows
-    const bool staged_ok = eab == 2 && d->N >= 8 && d->K > 0 && offsets_ok;
-    const bool rows_ok = d->K >= 16 / eab && (t || d->N >= 16 / eab) && d->lda * eab * 64 < LIM31;
+    const int64_t ve = 16 / eab;
+    const bool staged_ok = d->N >= ve && d->K > 0 && offsets_ok;
+    const bool rows_ok = d->K >= ve && (t || d->N >= ve) && d->lda * eab * 64 < LIM31;
     // direct loads: whole 16-byte chunks
-    const bool fast_ok = eab == 2 && d->K >= FAST_MIN_K && d->lda % 8 == 0 && d->ldb % 8 == 0 &&
-                         d->stride_b % 8 == 0 && (t || (d->N % 8 == 0 && d->N > 0)) && offsets_ok;
+    const bool fast_ok = d->K >= SLAB_BYTES / eab && d->lda % ve == 0 && d->ldb % ve == 0 &&
+                         d->stride_b % ve == 0 && (t || (d->N % ve == 0 && d->N > 0)) && offsets_ok;
+    // Rounds of 256 workgroups that the tiles make (about, with ranges).
+    const auto rounds = [&](int bm, int bn) {
+        const double per = (double)avg / bm + 0.5;                             // row tiles of an expert
+        const double down = d->groups == 1 ? (double)ceil_div(d->rows, bm) : (double)n * (per > 1 ? per : 1);
+        const double grid = down * (double)ceil_div(d->N, bn);
+        return grid <= 256 ? 1.0 : d->groups == 1 ? (double)ceil_div((int64_t)grid, 256) : grid / 256;
+    };
     // The kernel for few rows.  Its workgroups load some 50 GB/s each, so a shape costs what one of them
     // loads, 16 (rt + cg) rows of K, times the rounds of 256; and, in fp32, part of its matrix instructions:
     // 16 x 4096 x 4096 9.6 us in 16 columns (256 workgroups), 12.8 in 64 (64 of them); 64 x 4096 x 16384 47 in
@@ -177,16 +187,13 @@ gemm_status_t gemm_layer_plan_create(gemm_layer_plan_t *out, const gemm_layer_de
         double least = 0;
         for (const int r : {1, 2, 4})
             for (const int c : {4, t ? 1 : 2}) {
-                const double per = (double)avg / (16 * r) + 0.5;               // row tiles of an expert
-                const double down = d->groups == 1 ? (double)ceil_div(d->rows, 16 * r) : (double)n * (per > 1 ? per : 1);
-                const double grid = down * (double)ceil_div(d->N, 16 * c);
-                const double rounds = grid <= 256 ? 1.0 : d->groups == 1 ? (double)ceil_div((int64_t)grid, 256) : grid / 256;
-                const double cost = rounds * (r + c + (eab == 4 ? 0.4 * r * c : 0.0));
+                const double cost = rounds(16 * r, 16 * c) * (r + c + (eab == 4 ? 0.4 * r * c : 0.0));
                 if ((cg == 0 || c == cg) && (least == 0 || cost < least)) {
                     least = cost;
                     p.any = rows_table(ab, cd)(op_b, r, c);
                 }
             }
+        return least;
     };
     // Whether that kernel beats the tiles.  One matrix, gelu: up to 64 rows (64 x 65536 x 4096 121 -> 110
     // us), and while its workgroups are one round, or two of long sums (256 x 4096 x 4096 32 -> 21, 384 x
@@ -196,10 +203,7 @@ gemm_status_t gemm_layer_plan_create(gemm_layer_plan_t *out, const gemm_layer_de
     // 52 -> 47 and 53 -> 49, 8 of 2048 x 4096 46 -> 33 and 46 -> 38, but 64 of 2048 x 4096 174 vs 200 and 180 vs
     // 204; 64 rows, 16 of 1024 x 2048 21 vs 25.  Not transposed: 2 rows, 64 of 2048 x 4096 165 -> 157, 8 and
     // 24 rows, 8 of them, 39 -> 26 and 40 -> 38, but 8 rows, 64 of 768 x 2048 38 vs 50.
-    // fp32: always but where 128-wide tiles of the general kernel fill the chip twice over (us, they, 64-wide
-    // ones and this kernel: 1024 x 4096 x 4096 333, 349 and 327, 2048 x 4096 x 1024 168, 187 and 184).
     const auto few_rows = [&]() {
-        if (eab == 4) return avg < 128 || d->N < 128 || tiles < 400;
         if (d->groups == 1) {
             const int64_t wide = ceil_div(d->rows, 64) * ceil_div(d->N, 64);
             return d->rows <= 64 || wide <= 256 || (wide <= 512 && d->K >= 8192);
@@ -217,7 +221,18 @@ gemm_status_t gemm_layer_plan_create(gemm_layer_plan_t *out, const gemm_layer_de
         if (staged_ok) p.any = fast_table(ab, cd)(op_b, tile ? tile : 128, 1);
         break;
     case GEMM_ALGO_AUTO:
-        if (rows_ok && few_rows()) {
+        if (eab == 4) {
+            // The least of what a round costs, in the kernel for few rows' unit (1.5 us per 1000 of K): bound by
+            // the matrix instructions, of 64 x 64 tiles 10.5, of 128 x 128 ones 37 (a start that nothing hides in
+            // short sums), register-staged 15 and 45.  us of 64 x 64, 128 x 128 tiles and the kernel for few rows,
+            // K 4096, N 4096: 128 rows 67, 233, 50; 256 rows 72, 234, 88; 512 rows 132, 233, 170; 2048 rows 490, 464,
+            // 628; register-staged 512 rows 177, 287; 2048 rows 642, 541; N 1024, 4096 rows, K 256 24, 28, 38
+            const double k = (double)(d->K > 1 ? d->K : 1), start = 2000.0 / k, r64 = rounds(64, 64), r128 = rounds(128, 128);
+            const double rows_cost = rows_ok ? rows_kernel(0) * (1.0 + 100.0 / k) : INFINITY;
+            const double fast64 = 10.5 * r64, fast128 = (37.0 + start) * r128, staged64 = 15.0 * r64, staged128 = (45.0 + start) * r128;
+            if (staged_ok && fmin(staged64, staged128) < rows_cost) p.any = fast_table(ab, cd)(op_b, staged64 <= staged128 ? 64 : 128, 1);
+            if (fast_ok && fmin(fast64, fast128) < rows_cost) p.fast = fast_table(ab, cd)(op_b, fast64 <= fast128 ? 64 : 128, 0);
+        } else if (rows_ok && few_rows()) {
             rows_kernel(0);
         } else {
             if (fast_ok) {
