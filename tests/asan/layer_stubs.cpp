@@ -82,7 +82,8 @@ hipError_t choose(const RouteParams &p, RouteShape s, hipStream_t) {
     require(p.rows == 0 || (whole(p.logits, ES) && p.index && p.weight && p.order && p.place), "route operands");
     require(p.offsets && s.lanes * s.per >= p.experts && p.k <= 16 && p.k <= p.experts, "route sizes");
     require(p.blocks >= 1 && p.blocks <= ROUTE_MAX_BLOCKS && (int64_t)p.blocks * p.block_rows >= p.rows, "route blocks");
-    require(p.blocks == 1 || (p.hist && p.psum && p.psum == (float *)(p.hist + (p.experts + 1) * ROUTE_MAX_BLOCKS)), "route workspace");
+    require(p.blocks == 1 || (p.hist && p.psum && p.psum == (float *)(p.hist + (p.experts + 1) * p.stride) && p.stride >= p.blocks && p.stride <= ROUTE_MAX_BLOCKS &&
+            (p.stride & (p.stride - 1)) == 0 && p.stride >= 4), "route workspace");
     ++route_launches;
     return hipSuccess;
 }

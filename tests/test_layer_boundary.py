@@ -260,7 +260,8 @@ def test_route_blocks_cover_every_row():
         p = tge.RoutePlan(rows, experts, min(experts, rng.randint(1, 16)))
         lanes, per, blocks, each = map(int, re.search(r"lanes (\d+) x (\d+) blocks (\d+) of (\d+)", p.describe()).groups())
         assert lanes * per >= experts and blocks * each >= rows and (blocks - 1) * each <= max(rows - 1, 0) and blocks <= 256
-        assert p.workspace_bytes == ((2 * experts + 1) * 256 * 4 if blocks > 1 else 0)
+        side = max(4, 1 << (blocks - 1).bit_length())
+        assert p.workspace_bytes == ((2 * experts + 1) * side * 4 if blocks > 1 else 0)
 
 
 def test_binding_checks():

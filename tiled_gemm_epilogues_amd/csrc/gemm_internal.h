@@ -340,20 +340,21 @@ struct RouteParams {
     // gradient
     const float *dweight, *dloss;    // rows x k; 1 (nullptr: 0)
     void *dlogits;           // ldl
-    // workspace: ROUTE_MAX_BLOCKS numbers of each expert, the workgroups' choices of it ((experts + 1) of them:
-    // the last are the used rows) and their summed probabilities
+    // workspace: `stride` numbers of each expert, the workgroups' choices of it ((experts + 1) of them: the last
+    // are the used rows) and their summed probabilities; 4 times a power of two, at least blocks
     int32_t *hist;
     float *psum;
     int rows, experts, k, ldl, normalize;
-    int block_rows, blocks;
+    int block_rows, blocks, stride;
 };
 struct RouteShape {
     int lanes, per;
 };
 // Waves of a choosing workgroup: 16, or 8 where its rows of sums would need too much LDS; and the rows that
-// one workgroup routes alone, at most (block_rows with blocks == 1).
+// one workgroup routes alone, two rounds of its waves at most (block_rows with blocks == 1; us, alone and as several:
+// 64 experts, 8 chosen, 96 rows 8.4 and 8.9, 192 rows 12.1 and 9.2; 512 experts 16 rows 9.3 and 10.2, 32 rows 15.8 and 9.8).
 constexpr int route_waves(int width) { return width <= 256 ? 16 : 8; }
-constexpr int route_one_rows(int waves, int lanes) { return 4 * waves * (64 / lanes); }
+constexpr int route_one_rows(int waves, int lanes) { return 2 * waves * (64 / lanes); }
 // Choice, weights and the workgroups' sums; with one workgroup everything.
 hipError_t route_choose_f32(const RouteParams &p, RouteShape s, hipStream_t stream);
 hipError_t route_choose_f16(const RouteParams &p, RouteShape s, hipStream_t stream);

@@ -177,7 +177,7 @@ __device__ __forceinline__ void sort_keys(uint32_t (&v)[N]) {
 }
 
 // The choices of a wave's piece, 64 of them in each of up to AHEAD chunks that are loaded at once.  As
-// many waves take part as there are rows of counters for.  index: the workgroup's choices, in memory
+// many waves take part as there are rows of counters for, and choices.  index: the workgroup's choices, in memory
 // or (KEPT) in LDS.
 constexpr int AHEAD = 4;
 template <bool KEPT>
@@ -191,8 +191,9 @@ struct Choices {
         index = from;
         n = rows * p.k;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        waves = min((int)blockDim.x / 64, counters / p.experts);
-        const int chunks = (n + 63) / 64, per = (chunks + waves - 1) / waves;
+        const int chunks = (n + 63) / 64;
+        waves = max(min(min((int)blockDim.x / 64, counters / p.experts), chunks), 1);
+        const int per = (chunks + waves - 1) / waves;
         c0 = min(wave * per, chunks);
         c1 = min(c0 + per, chunks);
         load(c0);
@@ -239,11 +240,16 @@ __device__ void place_choices(const RouteParams &p, int row0, Choices<KEPT> &min
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int at = start[e];
-#pragma unroll 8
-        for (int w = 0; w < waves; ++w) {
-            const int h = hist[w * E + e];
-            hist[w * E + e] = at;
-            at += h;
+        constexpr int SIDE = 8;                          // (read side by side, then written)
+        for (int w = 0; w < waves; w += SIDE) {
+            int h[SIDE];
+#pragma unroll
+            for (int n = 0; n < SIDE; ++n) h[n] = hist[min(w + n, waves - 1) * E + e];
+#pragma unroll
+            for (int n = 0; n < SIDE; ++n) {
+                if (w + n < waves) hist[(w + n) * E + e] = at;
+                at += h[n];
+            }
         }
     }
     __syncthreads();
@@ -537,12 +543,12 @@ __global__ __launch_bounds__(route_waves(LANES *PER) * 64) void choose(RoutePara
             ptotal[e] = t;
             starts[e] = counts[e];
         } else {
-            p.psum[(int64_t)e * ROUTE_MAX_BLOCKS + blockIdx.x] = t;
-            p.hist[(int64_t)e * ROUTE_MAX_BLOCKS + blockIdx.x] = counts[e];
+            p.psum[e * p.stride + blockIdx.x] = t;
+            p.hist[e * p.stride + blockIdx.x] = counts[e];
         }
     }
     if constexpr (!ALL) {
-        if (threadIdx.x == 0) p.hist[(int64_t)E * ROUTE_MAX_BLOCKS + blockIdx.x] = all_used;
+        if (threadIdx.x == 0) p.hist[E * p.stride + blockIdx.x] = all_used;
     } else {
         __syncthreads();
         scan_experts(starts, E);
@@ -555,13 +561,14 @@ __global__ __launch_bounds__(route_waves(LANES *PER) * 64) void choose(RoutePara
 
 // The rest for several workgroups: each sums the counts of all and of those before it (no launch between) and
 // places its choices; one more writes the totals.  The counts and probabilities of an expert stand side by
-// side, ROUTE_MAX_BLOCKS of each, so that a wave has them with one load.
+// side, p.stride of each: a lane has four, and a wave those of 1 to 64 experts with one load.
 constexpr int PLACE_THREADS = 1024, PLACE_COUNTERS = 8192;
+template <bool WHOLE>                                // a wave to an expert
 __global__ __launch_bounds__(PLACE_THREADS, 8) void place_blocks(RouteParams p) {
     static_assert(ROUTE_MAX_BLOCKS == 64 * 4, "four workgroups to a lane");
     typedef int i32x4a __attribute__((ext_vector_type(4), aligned(4)));
     typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
-    constexpr int WAVES = PLACE_THREADS / 64, SIDE = 8;
+    constexpr int WAVES = PLACE_THREADS / 64, SIDE = WHOLE ? 8 : 4;
     __shared__ int hist[PLACE_COUNTERS];             // the waves' counters
     __shared__ int starts[ROUTE_MAX_EXPERTS + 1], before[ROUTE_MAX_EXPERTS + 1];
     const int E = p.experts, me = blockIdx.x;
@@ -571,44 +578,58 @@ __global__ __launch_bounds__(PLACE_THREADS, 8) void place_blocks(RouteParams p) 
     float *const ptotal = reinterpret_cast<float *>(before);
     Choices<false> mine;
     mine.init(p, p.index + (int64_t)row0 * p.k, totals ? 0 : min(p.block_rows, p.rows - row0), PLACE_COUNTERS);
-    // (lanes past the last workgroup read the first ones' and drop them)
-    const int b0 = 4 * lane < p.blocks ? 4 * lane : 0, have = min(max(p.blocks - 4 * lane, 0), 4), low_have = min(max(me - 4 * lane, 0), 4);
-    for (int e0 = wave; e0 <= E; e0 += WAVES * SIDE) {
+    // lanes of an expert (a power of two), experts of a load; this lane's workgroups b0 .. b0 + 3, and how many of
+    // them there are, and are before this one
+    const int per = WHOLE ? 64 : p.stride / 4, side = 64 / per, sub = WHOLE ? 0 : lane / per, in = lane & (per - 1);
+    const int b0 = 4 * in;
+    const int have = min(max(p.blocks - b0, 0), 4), low_have = min(max(me - b0, 0), 4);
+    const int loads = WHOLE ? E + 1 : (E + side) / side;   // of E + 1 counts
+    for (int c = wave; c < loads; c += WAVES * SIDE) {
         i32x4a h[SIDE];
 #pragma unroll
-        for (int n = 0; n < SIDE; ++n) h[n] = *reinterpret_cast<const i32x4a *>(p.hist + (int64_t)min(e0 + n * WAVES, E) * ROUTE_MAX_BLOCKS + b0);
+        for (int n = 0; n < SIDE; ++n)
+            h[n] = *reinterpret_cast<const i32x4a *>(p.hist + min((c + n * WAVES) * side + sub, E) * p.stride + b0);
 #pragma unroll
         for (int n = 0; n < SIDE; ++n) {
-            const int e = e0 + n * WAVES;
-            if (e > E) break;
+            if (c + n * WAVES >= loads) break;
+            const int e = (c + n * WAVES) * side + sub;
             int all = 0, low = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                all += i < have ? h[n][i] : 0;
-                low += i < low_have ? h[n][i] : 0;
+                all += (WHOLE || e <= E) && i < have ? h[n][i] : 0;
+                low += (WHOLE || e <= E) && i < low_have ? h[n][i] : 0;
             }
+            // an expert's sum is what the running sum grows by over its lanes
             all = wave_scan_add(all);
             low = wave_scan_add(low);
-            if (lane == 63) {
+            if constexpr (!WHOLE) {
+                const int all_to = __shfl_up(all, per), low_to = __shfl_up(low, per);
+                all -= lane >= per ? all_to : 0;
+                low -= lane >= per ? low_to : 0;
+            }
+            if (in == per - 1 && (WHOLE || e <= E)) {
                 starts[e] = all;
                 if (!totals) before[e] = low;
             }
         }
     }
     if (totals && p.loss) {
-        for (int e0 = wave; e0 < E; e0 += WAVES * SIDE) {
+        for (int c = wave; c < loads; c += WAVES * SIDE) {
             f32x4a q[SIDE];
 #pragma unroll
-            for (int n = 0; n < SIDE; ++n) q[n] = *reinterpret_cast<const f32x4a *>(p.psum + (int64_t)min(e0 + n * WAVES, E - 1) * ROUTE_MAX_BLOCKS + b0);
+            for (int n = 0; n < SIDE; ++n)
+                q[n] = *reinterpret_cast<const f32x4a *>(p.psum + min((c + n * WAVES) * side + sub, E - 1) * p.stride + b0);
 #pragma unroll
             for (int n = 0; n < SIDE; ++n) {
-                const int e = e0 + n * WAVES;
-                if (e >= E) break;
+                if (c + n * WAVES >= loads) break;
+                const int e = (c + n * WAVES) * side + sub;
                 float t = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) t += i < have ? q[n][i] : 0.0f;
-                t = wave_sum(t);
-                if (lane == 0) ptotal[e] = t;
+                if constexpr (WHOLE) t = wave_sum(t);
+                else
+                    for (int s = per / 2; s > 0; s /= 2) t += __shfl_xor(t, s);
+                if (in == 0 && e < E) ptotal[e] = t;
             }
         }
     }
@@ -768,7 +789,8 @@ hipError_t route_choose_f32(const RouteParams &p, RouteShape s, hipStream_t st) 
 hipError_t route_grad_f32(const RouteParams &p, RouteShape s, unsigned g, hipStream_t st) { return by_shape<float, true>(p, s, g, st); }
 
 hipError_t route_place(const RouteParams &p, hipStream_t stream) {
-    hipLaunchKernelGGL(place_blocks, dim3(p.blocks + 1), dim3(PLACE_THREADS), 0, stream, p);
+    if (p.stride == ROUTE_MAX_BLOCKS) hipLaunchKernelGGL(place_blocks<true>, dim3(p.blocks + 1), dim3(PLACE_THREADS), 0, stream, p);
+    else hipLaunchKernelGGL(place_blocks<false>, dim3(p.blocks + 1), dim3(PLACE_THREADS), 0, stream, p);
     return hipGetLastError();
 }
 #elif defined(TGE_TYPE_F16)

@@ -18,7 +18,7 @@ struct gemm_route_plan {
     int64_t rows, experts, k, ldl;
     int type, normalize;
     RouteShape shape;
-    int64_t block_rows, blocks, grid_grad;
+    int64_t block_rows, blocks, stride, grid_grad;
     size_t workspace;
     char desc[256];
 };
@@ -50,6 +50,7 @@ RouteParams params(const gemm_route_plan &p) {
     q.normalize = p.normalize;
     q.block_rows = (int)p.block_rows;
     q.blocks = (int)p.blocks;
+    q.stride = (int)p.stride;
     return q;
 }
 
@@ -83,7 +84,9 @@ gemm_status_t gemm_route_plan_create(gemm_route_plan_t *out, const gemm_route_de
     p.blocks = d->rows > 0 ? ceil_div(d->rows, p.block_rows) : 1;
     const int64_t need = ceil_div(d->rows, 4 * (64 / p.shape.lanes));
     p.grid_grad = need < 2048 ? need : 2048;
-    p.workspace = p.blocks > 1 ? (size_t)((2 * p.experts + 1) * tge::ROUTE_MAX_BLOCKS * 4) : 0;
+    p.stride = 4;
+    while (p.stride < p.blocks) p.stride *= 2;
+    p.workspace = p.blocks > 1 ? (size_t)((2 * p.experts + 1) * p.stride * 4) : 0;
     gemm_route_plan *q = new (std::nothrow) gemm_route_plan(p);
     if (!q) return GEMM_STATUS_ALLOC_FAILED;
     snprintf(q->desc, sizeof q->desc, "route %s experts %lld k %lld%s lanes %d x %d blocks %lld of %lld rows", type_name(type),
@@ -114,7 +117,7 @@ gemm_status_t gemm_route_run(gemm_route_plan_t p, const void *logits, const uint
     q.offsets = offsets; q.slope = slope; q.loss = loss;
     if (p->blocks > 1) {
         q.hist = static_cast<int32_t *>(workspace);
-        q.psum = reinterpret_cast<float *>(q.hist + (p->experts + 1) * tge::ROUTE_MAX_BLOCKS);
+        q.psum = reinterpret_cast<float *>(q.hist + (p->experts + 1) * p->stride);
     }
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (choose_of(p->type)(q, p->shape, st) != hipSuccess) return GEMM_STATUS_HIP_ERROR;
