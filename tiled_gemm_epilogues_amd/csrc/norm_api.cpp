@@ -20,7 +20,8 @@ struct gemm_norm_plan {
     int type;
     float eps;
     NormShape forward, grad;
-    int64_t grid_forward, grid_grad;   // workgroups; the gradient's write one partial sum each
+    int64_t grid_forward;              // workgroups
+    int64_t grid_grad, grid_rows;      // the gradient's: with column sums (a partial sum each), and without
     size_t workspace;
     char desc[256];
 };
@@ -75,10 +76,16 @@ gemm_status_t gemm_norm_plan_create(gemm_norm_plan_t *out, const gemm_norm_desc_
     // as many workgroups as the chip holds at once, each with rows enough to keep the next one's loads
     // in flight
     const int64_t fw = p.forward.waves * p.forward.teams;
-    const int64_t most_f = 256 * (16 / fw > 1 ? 16 / fw : 1), most_g = 256;
+    const int64_t most_f = 256 * (16 / fw > 1 ? 16 / fw : 1);
     const int64_t need_f = ceil_div(d->rows, p.forward.teams), need_g = ceil_div(d->rows, p.grad.teams);
     p.grid_forward = need_f < most_f ? need_f : most_f;
+    // The gradient's write and join a partial sum each, 16 N bytes moved at some 5 TB/s, against 3 us for each turn
+    // of rows that others do not take: the least of both together, at most one to a CU.  us by workgroups: 300
+    // rows of 16384 64 24.5, 133 20.8; 1200 rows of 8192 180 23.7, 256 20.5; 60 rows of 4096 30 7.5, 15 8.8
+    const double both = sqrt((double)need_g * 3e-6 * 5e12 / (16.0 * (double)(d->N > 1 ? d->N : 1)));
+    const int64_t most_g = both < 256.0 ? (int64_t)both + 1 : 256;
     p.grid_grad = need_g < most_g ? need_g : most_g;
+    p.grid_rows = need_g < 256 ? need_g : 256;
     p.workspace = (size_t)(p.grid_grad * 2 * d->N * 4);
     gemm_norm_plan *q = new (std::nothrow) gemm_norm_plan(p);
     if (!q) return GEMM_STATUS_ALLOC_FAILED;
@@ -131,7 +138,8 @@ gemm_status_t gemm_norm_grad_run(gemm_norm_plan_t p, const void *dY, const void 
         q.part = part;
         q.beta = beta;
         q.has_beta = beta != 0.0f;
-        if (grad_of(p->type)(q, p->grad, (unsigned)p->grid_grad, st) != hipSuccess) return GEMM_STATUS_HIP_ERROR;
+        const int64_t grid = sums ? p->grid_grad : p->grid_rows;
+        if (grad_of(p->type)(q, p->grad, (unsigned)grid, st) != hipSuccess) return GEMM_STATUS_HIP_ERROR;
     }
     // without rows the sums are 0
     if (sums && tge::norm_join(part, has_rows ? (int)p->grid_grad : 0, (int)p->N, dweight, dbias, st) != hipSuccess)
