@@ -138,6 +138,14 @@ def test_rows(rows, type):
         run_all(rows, N, type, seed=rows, beta=1.0)
 
 
+@pytest.mark.parametrize("type", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 3, 8, 9, 31, 32, 33, 64, 65, 100, 128, 129, 200, 256, 257])
+def test_short_rows(N, type):
+    # rows that share a wave, all of them there and not
+    for rows in (1, 2, 5, 31, 33, 65, 517, 9001):
+        run_all(rows, N, type, seed=rows, pad=rows % 3, beta=0.5 * (rows % 2))
+
+
 @pytest.mark.parametrize("type", ["bf16", "f32"])
 @pytest.mark.parametrize("off", [1, 2, 5])
 def test_pointers_off_the_16_byte_grid(off, type):

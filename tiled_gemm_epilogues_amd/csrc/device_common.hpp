@@ -331,6 +331,39 @@ __device__ __forceinline__ float wave_sum(float v) {
     v = add_moved<0x143, 0xc>(v);
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
+// v of another lane.  MOVE: a data-parallel move inside 16 lanes (N on in their ring; mirrored in 8 lanes; the
+// neighbour, or two on, in 4), or 16 or 32: the lane that far away.
+constexpr int RING = 0x120, MIRROR_8 = 0x141, NEXT_OF_2 = 0xb1, OTHER_2 = 0x4e;
+template <int MOVE>
+__device__ __forceinline__ int moved(int v) {
+    if constexpr (MOVE == 16) return __builtin_amdgcn_ds_swizzle(v, 0x401f);
+    else if constexpr (MOVE == 32) return __shfl_xor(v, 32);
+    else return __builtin_amdgcn_update_dpp(0, v, MOVE, 0xf, 0xf, true);
+}
+// f(move) for the moves after each of which twice as many of the LANES lanes have been joined.
+template <int LANES, class F>
+__device__ __forceinline__ void lane_steps(F f) {
+    if constexpr (LANES == 8) {
+        f(std::integral_constant<int, MIRROR_8>());
+        f(std::integral_constant<int, NEXT_OF_2>());
+        f(std::integral_constant<int, OTHER_2>());
+    } else {
+        f(std::integral_constant<int, RING + 8>());
+        f(std::integral_constant<int, RING + 4>());
+        f(std::integral_constant<int, RING + 2>());
+        f(std::integral_constant<int, RING + 1>());
+        if constexpr (LANES >= 32) f(std::integral_constant<int, 16>());
+        if constexpr (LANES >= 64) f(std::integral_constant<int, 32>());
+    }
+}
+
+// Sum over LANES lanes side by side, in each of them.
+template <int LANES>
+__device__ __forceinline__ float side_sum(float v) {
+    if constexpr (LANES == 64) return wave_sum(v);
+    lane_steps<LANES>([&](auto move) { v += __builtin_bit_cast(float, moved<move.value>(__builtin_bit_cast(int, v))); });
+    return v;
+}
 __device__ __forceinline__ int wave_scan_max(int v) {
     v = max(v, lane_move<0x111, 0xf>(v));
     v = max(v, lane_move<0x112, 0xf>(v));

@@ -287,7 +287,8 @@ const QuantEntry *quant_tile_bf16_f32(int block);
 // Layer norm (layer_norm.hip).  A row belongs to a team of `waves` waves, whose lanes hold 16-byte
 // chunks lane, lane + 64 * waves, ... (`chunks` of them) of it; N elements fill at most the team's
 // chunks.  Workgroups have `teams` teams and take rows blockIdx * teams + team, then every
-// grid * teams-th.  Pointers need their elements' alignment only.
+// grid * teams-th; a row that needs fewer lanes than a wave has `lanes` of them, and 64 / lanes rows stand side by
+// side in a team.  Pointers need their elements' alignment only.
 struct NormParams {
     const void *X;           // rows x N, ldx
     const float *weight, *bias;      // nullptr: 1 and 0
@@ -302,18 +303,20 @@ struct NormParams {
     int has_beta;
 };
 struct NormShape {
-    int waves, chunks, teams;
+    int waves, chunks, teams, lanes;
 };
 // Teams of a workgroup, which so has 4 waves, or 8 in the gradient, unless one row needs more.
 constexpr int norm_teams(int waves, bool grad) { return waves < (grad ? 8 : 4) ? (grad ? 8 : 4) / waves : 1; }
-// The team of a row of `units` (1 to 64) KiB: one chunk per lane, or two, in as few waves as hold it; more
-// than two (of 16 waves) for the longest rows only, as they cost the registers that keep the next
+// The team of a row of `pieces` (1 to 4096) 16-byte chunks: one per lane, or two, in as few waves as hold it;
+// more than two (of 16 waves) for the longest rows only, as they cost the registers that keep the next
 // row on its way.
-inline NormShape norm_shape(int64_t units, bool grad) {
+inline NormShape norm_shape(int64_t pieces, bool grad) {
+    const int64_t units = (pieces + 63) / 64;
     int waves = 1, chunks = units <= 1 ? 1 : 2;
+    const int lanes = pieces <= 8 ? 8 : pieces <= 16 ? 16 : pieces <= 32 ? 32 : 64;
     while (waves * chunks < units && waves < 16) waves = waves < 4 ? waves + 1 : waves % 3 ? waves / 2 * 3 : waves / 3 * 4;
     while (waves * chunks < units) ++chunks;
-    return {waves, chunks, norm_teams(waves, grad)};
+    return {waves, chunks, norm_teams(waves, grad), lanes};
 }
 constexpr int NORM_SUM_COLS = 32;    // columns of a workgroup that joins partial sums
 hipError_t norm_forward_f32(const NormParams &p, NormShape s, unsigned grid, hipStream_t stream);

@@ -70,14 +70,15 @@ gemm_status_t gemm_norm_plan_create(gemm_norm_plan_t *out, const gemm_norm_desc_
     p.rows = d->rows; p.N = d->N; p.ldx = d->ldx; p.ldy = d->ldy;
     p.type = type;
     p.eps = d->eps;
-    const int64_t units = d->N > 0 ? ceil_div(d->N * es, 1024) : 1;
-    p.forward = tge::norm_shape(units, false);
-    p.grad = tge::norm_shape(units, true);
+    const int64_t pieces = d->N > 0 ? ceil_div(d->N * es, 16) : 1;
+    p.forward = tge::norm_shape(pieces, false);
+    p.grad = tge::norm_shape(pieces, true);
     // as many workgroups as the chip holds at once, each with rows enough to keep the next one's loads
     // in flight
     const int64_t fw = p.forward.waves * p.forward.teams;
     const int64_t most_f = 256 * (16 / fw > 1 ? 16 / fw : 1);
-    const int64_t need_f = ceil_div(d->rows, p.forward.teams), need_g = ceil_div(d->rows, p.grad.teams);
+    const int64_t side = 64 / p.forward.lanes;       // rows of a team
+    const int64_t need_f = ceil_div(d->rows, p.forward.teams * side), need_g = ceil_div(d->rows, p.grad.teams * side);
     p.grid_forward = need_f < most_f ? need_f : most_f;
     // The gradient's write and join a partial sum each, 16 N bytes moved at some 5 TB/s, against 3 us for each turn
     // of rows that others do not take: the least of both together, at most one to a CU.  us by workgroups: 300

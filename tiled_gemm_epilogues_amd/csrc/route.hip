@@ -23,8 +23,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 #include "device_common.hpp"
 #include "gemm_internal.h"
 
@@ -39,32 +37,6 @@ constexpr int ROUTE_THREADS = 256, ROUTE_WAVES = ROUTE_THREADS / 64;   // of the
 
 __device__ __forceinline__ float as_float(int v) { return __builtin_bit_cast(float, v); }
 __device__ __forceinline__ int as_int(float v) { return __builtin_bit_cast(int, v); }
-
-// v of another lane.  MOVE: a data-parallel move inside 16 lanes (N on in their ring; mirrored in 8 lanes; the
-// neighbour, or two on, in 4), or 16 or 32: the lane that far away.
-constexpr int RING = 0x120, MIRROR_8 = 0x141, NEXT_OF_2 = 0xb1, OTHER_2 = 0x4e;
-template <int MOVE>
-__device__ __forceinline__ int moved(int v) {
-    if constexpr (MOVE == 16) return __builtin_amdgcn_ds_swizzle(v, 0x401f);
-    else if constexpr (MOVE == 32) return __shfl_xor(v, 32);
-    else return __builtin_amdgcn_update_dpp(0, v, MOVE, 0xf, 0xf, true);
-}
-// f(move) for the moves after each of which twice as many of the LANES lanes have been joined.
-template <int LANES, class F>
-__device__ __forceinline__ void lane_steps(F f) {
-    if constexpr (LANES == 8) {
-        f(std::integral_constant<int, MIRROR_8>());
-        f(std::integral_constant<int, NEXT_OF_2>());
-        f(std::integral_constant<int, OTHER_2>());
-    } else {
-        f(std::integral_constant<int, RING + 8>());
-        f(std::integral_constant<int, RING + 4>());
-        f(std::integral_constant<int, RING + 2>());
-        f(std::integral_constant<int, RING + 1>());
-        if constexpr (LANES >= 32) f(std::integral_constant<int, 16>());
-        if constexpr (LANES >= 64) f(std::integral_constant<int, 32>());
-    }
-}
 
 // Reduction over a row's lanes, the result in each of them.
 template <int LANES, class Op>
