@@ -305,3 +305,23 @@ def test_binding_checks():
                       (tge.RoutePlan, (10, 8, 9)), (tge.RoutePlan, (10, 2000, 2))):
         with pytest.raises(tge.GemmError):
             cls(*args)
+
+
+def test_operands_checked_together():
+    # the module gives pointers for what passes as it is, and nothing where a tensor does not fit (the checks
+    # one by one then name it)
+    from tiled_gemm_epilogues_amd import _operands
+    p = tge.NormPlan(4, 8, "f32")
+    assert tuple(p._pointers(0, 1, None, 3, 4, 5, 6)) == (1, None, 3, 4, 5, 6)
+    for what, args in (("X", (torch.zeros(4, 8), None, None, None, None, None)), ("rstd", (1, None, None, 4, 5, torch.zeros(4)))):
+        with pytest.raises(ValueError, match=f"{what} must be a device tensor"):
+            p._pointers(0, *args)
+    one = _operands.Operands(((torch.float32, 4, 2),))
+    assert one(0, None) == (None,) and one(0, 7) == (7,)
+    for t in (torch.zeros(2, 2), "no tensor", torch.zeros(2, 2, device="meta")):
+        assert one(0, t) is None
+    for bad in (lambda: _operands.Operands(1), lambda: _operands.Operands(((1, 2, 3),)),
+                lambda: _operands.Operands(((torch.float32, 2, "x"),)), lambda: one(0), lambda: one(0, 1, 2), lambda: one("x", 1),
+                lambda: one(0, t=1)):
+        with pytest.raises(TypeError):
+            bad()

@@ -662,6 +662,18 @@ class _GroupedBase:
         import torch
         self._torch, self._entry = torch, entry
 
+    def _together(self, *names):
+        """A function (device, *tensors) that gives the device pointers of the named operands: checked in one
+        call (csrc/operands.cpp), and one by one only where that finds something to say."""
+        import torch  # noqa: F401  (the module needs its libraries)
+        from . import _operands
+        fits = _operands.Operands(tuple(self._spec[n] for n in names))
+
+        def pointers(device, *tensors):
+            got = fits(device, *tensors)
+            return got if got is not None else [self._ptr(n, t, device) for n, t in zip(names, tensors)]
+        return pointers
+
     def _stream(self, stream, device):
         if stream is None:
             return self._torch._C._cuda_getCurrentRawStream(device)
@@ -866,6 +878,8 @@ class LayerPlan(_GroupedBase):
             "C": cdn, "D": cdn, "pre": cdn,
             "bias": (torch.float32, (groups - 1) * self.stride_bias + N if N else 0, None),
             "offsets": (torch.int32, groups + 1, None)}
+        self._pointers = self._together("A", "B", "C", "D", "pre", "bias", "offsets")
+        self._grad_pointers = self._together("A", "B", "pre", "D", "offsets")
 
     def run(self, A, B, C, D, offsets=None, bias=None, pre=None, alpha=1.0, beta=0.0, stream=None):
         """Enqueue the forward product on `stream` (as Plan.run).  C is read when beta != 0; bias: None
@@ -873,11 +887,8 @@ class LayerPlan(_GroupedBase):
         all rows.  Rows of D and pre outside the ranges are left as they are.  Raises ValueError /
         TypeError before anything is enqueued when a tensor does not fit the plan."""
         dev = self._torch.cuda.current_device()
-        ptr = self._ptr
-        st = self._entry(
-            self._h, ptr("A", A, dev), ptr("B", B, dev), ptr("C", C, dev) if beta != 0 else None,
-            ptr("D", D, dev), ptr("pre", pre, dev), ptr("bias", bias, dev), ptr("offsets", offsets, dev),
-            float(alpha), float(beta), self._stream(stream, dev))
+        st = self._entry(self._h, *self._pointers(dev, A, B, C if beta != 0 else None, D, pre, bias, offsets),
+                         float(alpha), float(beta), self._stream(stream, dev))
         if st != STATUS_SUCCESS:
             raise GemmError(st, "gemm_layer_run")
 
@@ -885,10 +896,8 @@ class LayerPlan(_GroupedBase):
         """Enqueue the gradient product: D = act'(pre) * alpha * A * op(B), pre as run() left it (None
         with act "none"; D may be pre itself)."""
         dev = self._torch.cuda.current_device()
-        ptr = self._ptr
-        st = self._grad(
-            self._h, ptr("A", A, dev), ptr("B", B, dev), ptr("pre", pre, dev), ptr("D", D, dev),
-            ptr("offsets", offsets, dev), float(alpha), self._stream(stream, dev))
+        st = self._grad(self._h, *self._grad_pointers(dev, A, B, pre, D, offsets), float(alpha),
+                        self._stream(stream, dev))
         if st != STATUS_SUCCESS:
             raise GemmError(st, "gemm_layer_grad_run")
 
@@ -937,15 +946,14 @@ class NormPlan(_WorkspaceBase):
         self._spec = {"X": x, "dX": x, "C": x, "Y": y, "dY": y, "weight": cols, "bias": cols, "dweight": cols,
                       "dbias": cols, "mean": per_row, "rstd": per_row,
                       "workspace": (torch.uint8, self.workspace_bytes, None)}
+        self._pointers = self._together("X", "weight", "bias", "Y", "mean", "rstd")
+        self._grad_pointers = self._together("dY", "X", "weight", "mean", "rstd", "C", "dX", "dweight", "dbias")
 
     def run(self, X, weight, bias, Y, mean=None, rstd=None, stream=None):
         """Enqueue the forward pass on `stream` (as Plan.run).  weight None is 1, bias None is 0; mean
         and rstd receive what run_grad needs.  Y may be X itself."""
         dev = self._torch.cuda.current_device()
-        ptr = self._ptr
-        st = self._entry(
-            self._h, ptr("X", X, dev), ptr("weight", weight, dev), ptr("bias", bias, dev), ptr("Y", Y, dev),
-            ptr("mean", mean, dev), ptr("rstd", rstd, dev), self._stream(stream, dev))
+        st = self._entry(self._h, *self._pointers(dev, X, weight, bias, Y, mean, rstd), self._stream(stream, dev))
         if st != STATUS_SUCCESS:
             raise GemmError(st, "gemm_norm_run")
 
@@ -956,13 +964,11 @@ class NormPlan(_WorkspaceBase):
         workspace_bytes, used by one run at a time); None takes one from torch's allocator for the
         current stream."""
         dev = self._torch.cuda.current_device()
-        ptr = self._ptr
         sums = (dweight is not None or dbias is not None) and self.workspace_bytes > 0
         self._own_stream(workspace, sums, stream)
-        args = (self._h, ptr("dY", dY, dev), ptr("X", X, dev), ptr("weight", weight, dev), ptr("mean", mean, dev),
-                ptr("rstd", rstd, dev), ptr("C", C, dev) if beta != 0 else None, ptr("dX", dX, dev),
-                ptr("dweight", dweight, dev), ptr("dbias", dbias, dev), float(beta))
-        st = self._grad(*args, *self._workspace(workspace, sums, dev), self._stream(stream, dev))
+        ptrs = self._grad_pointers(dev, dY, X, weight, mean, rstd, C if beta != 0 else None, dX, dweight, dbias)
+        st = self._grad(self._h, *ptrs, float(beta), *self._workspace(workspace, sums, dev),
+                        self._stream(stream, dev))
         if st != STATUS_SUCCESS:
             raise GemmError(st, "gemm_norm_grad_run")
 
@@ -993,6 +999,9 @@ class RoutePlan(_WorkspaceBase):
                       "offsets": (torch.int32, experts + 1, None), "slope": (torch.float32, experts, None),
                       "loss": (torch.float32, 1, None), "dloss": (torch.float32, 1, None),
                       "workspace": (torch.uint8, self.workspace_bytes, None)}
+        self._pointers = self._together("logits", "mask", "index", "weight", "order", "place", "offsets", "slope",
+                                        "loss")
+        self._grad_pointers = self._together("logits", "mask", "index", "dweight", "slope", "dloss", "dlogits")
 
     def run(self, logits, index, weight, order, place, offsets, slope=None, loss=None, mask=None,
             workspace=None, stream=None):
@@ -1000,12 +1009,10 @@ class RoutePlan(_WorkspaceBase):
         uint8 per row, 0 leaves it out.  Many rows need a workspace (uint8, at least workspace_bytes,
         used by one run at a time); None takes one from torch's allocator for the current stream."""
         dev = self._torch.cuda.current_device()
-        ptr = self._ptr
         self._own_stream(workspace, self.workspace_bytes, stream)
-        args = (self._h, ptr("logits", logits, dev), ptr("mask", mask, dev), ptr("index", index, dev),
-                ptr("weight", weight, dev), ptr("order", order, dev), ptr("place", place, dev),
-                ptr("offsets", offsets, dev), ptr("slope", slope, dev), ptr("loss", loss, dev))
-        st = self._entry(*args, *self._workspace(workspace, self.workspace_bytes, dev), self._stream(stream, dev))
+        ptrs = self._pointers(dev, logits, mask, index, weight, order, place, offsets, slope, loss)
+        st = self._entry(self._h, *ptrs, *self._workspace(workspace, self.workspace_bytes, dev),
+                         self._stream(stream, dev))
         if st != STATUS_SUCCESS:
             raise GemmError(st, "gemm_route_run")
 
@@ -1014,10 +1021,7 @@ class RoutePlan(_WorkspaceBase):
         fp32 value on the device; None: 0), with index, slope and mask of the forward run.  dlogits may
         be logits itself."""
         dev = self._torch.cuda.current_device()
-        ptr = self._ptr
-        st = self._grad(
-            self._h, ptr("logits", logits, dev), ptr("mask", mask, dev), ptr("index", index, dev),
-            ptr("dweight", dweight, dev), ptr("slope", slope, dev), ptr("dloss", dloss, dev),
-            ptr("dlogits", dlogits, dev), self._stream(stream, dev))
+        ptrs = self._grad_pointers(dev, logits, mask, index, dweight, slope, dloss, dlogits)
+        st = self._grad(self._h, *ptrs, self._stream(stream, dev))
         if st != STATUS_SUCCESS:
             raise GemmError(st, "gemm_route_grad_run")

@@ -1,4 +1,5 @@
-"""Builds the HIP library tiled_gemm_epilogues_amd/libtge.so for gfx950 with hipcc.
+"""Builds the HIP library tiled_gemm_epilogues_amd/libtge.so for gfx950 with hipcc, and the Python module
+_operands (the binding's checks of tensors) with g++ against the installed torch.
 
 The kernel source is compiled once per (input, output) type pair, in parallel, and linked with
 the host API into one shared library that exports the C ABI declared in include/gemm.h.
@@ -13,6 +14,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtge.so")
+OPERANDS = os.path.join(HERE, "_operands.so")
 
 PAIRS = ["F32_F32", "F16_F16", "F16_F32", "BF16_BF16", "BF16_F32", "I8_I32"]
 FAST_PAIRS = ["F16_F16", "F16_F32", "BF16_BF16", "BF16_F32", "I8_I32"]
@@ -71,6 +73,19 @@ def steps():
     return out
 
 
+def operands_step():
+    """The command that builds the Python module (its output is OPERANDS + ".tmp")."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            "-I", sysconfig.get_paths()["include"], "-o", OPERANDS + ".tmp", os.path.join(CSRC, "operands.cpp"),
+            "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def build(verbose=False, jobs=None):
     os.makedirs(BUILD, exist_ok=True)
     jobs = jobs or min(8, os.cpu_count() or 1)
@@ -81,6 +96,8 @@ def build(verbose=False, jobs=None):
     tmp = LIB + ".tmp"
     _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB)
+    _run(operands_step(), verbose)
+    os.replace(OPERANDS + ".tmp", OPERANDS)
     return LIB
 
 
