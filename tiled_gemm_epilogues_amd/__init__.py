@@ -662,17 +662,26 @@ class _GroupedBase:
         import torch
         self._torch, self._entry = torch, entry
 
-    def _together(self, *names):
-        """A function (device, *tensors) that gives the device pointers of the named operands: checked in one
-        call (csrc/operands.cpp), and one by one only where that finds something to say."""
-        import torch  # noqa: F401  (the module needs its libraries)
-        from . import _operands
-        fits = _operands.Operands(tuple(self._spec[n] for n in names))
+    # The operands of run() and run_grad() in plans that check them together: in one call (csrc/operands.cpp), and one
+    # by one only where that finds something to say.
+    _RUN, _GRAD = (), ()
 
-        def pointers(device, *tensors):
-            got = fits(device, *tensors)
-            return got if got is not None else [self._ptr(n, t, device) for n, t in zip(names, tensors)]
-        return pointers
+    def _together(self):
+        import torch  # noqa: F401  (the module needs its libraries)
+        try:
+            from . import _operands
+        except ImportError as e:
+            raise ImportError(f"tiled_gemm_epilogues_amd/_operands.so is not built or does not load: {e}") from e
+        self._run_fits, self._grad_fits = (_operands.Operands(tuple(self._spec[n] for n in names))
+                                           for names in (self._RUN, self._GRAD))
+
+    def _pointers(self, device, *tensors):
+        got = self._run_fits(device, *tensors)
+        return got if got is not None else [self._ptr(n, t, device) for n, t in zip(self._RUN, tensors)]
+
+    def _grad_pointers(self, device, *tensors):
+        got = self._grad_fits(device, *tensors)
+        return got if got is not None else [self._ptr(n, t, device) for n, t in zip(self._GRAD, tensors)]
 
     def _stream(self, stream, device):
         if stream is None:
@@ -850,6 +859,8 @@ class LayerPlan(_GroupedBase):
     offsets give; B and bias as in GroupedPlan."""
 
     _destroy, _describe = staticmethod(gemm_layer_plan_destroy), staticmethod(gemm_layer_plan_describe)
+    _RUN = ("A", "B", "C", "D", "pre", "bias", "offsets")
+    _GRAD = ("A", "B", "pre", "D", "offsets")
 
     def __init__(self, rows, N, K, groups=1, op_b="T", lda=None, ldb=None, ldc=None, stride_b=None,
                  stride_bias=None, ab="f16", cd="f16", act="none", algo="auto", tile=0):
@@ -878,8 +889,7 @@ class LayerPlan(_GroupedBase):
             "C": cdn, "D": cdn, "pre": cdn,
             "bias": (torch.float32, (groups - 1) * self.stride_bias + N if N else 0, None),
             "offsets": (torch.int32, groups + 1, None)}
-        self._pointers = self._together("A", "B", "C", "D", "pre", "bias", "offsets")
-        self._grad_pointers = self._together("A", "B", "pre", "D", "offsets")
+        self._together()
 
     def run(self, A, B, C, D, offsets=None, bias=None, pre=None, alpha=1.0, beta=0.0, stream=None):
         """Enqueue the forward product on `stream` (as Plan.run).  C is read when beta != 0; bias: None
@@ -927,6 +937,8 @@ class NormPlan(_WorkspaceBase):
     dbias are fp32."""
 
     _destroy, _describe = staticmethod(gemm_norm_plan_destroy), staticmethod(gemm_norm_plan_describe)
+    _RUN = ("X", "weight", "bias", "Y", "mean", "rstd")
+    _GRAD = ("dY", "X", "weight", "mean", "rstd", "C", "dX", "dweight", "dbias")
 
     def __init__(self, rows, N, type="bf16", eps=1e-5, ldx=None, ldy=None):
         import torch
@@ -946,8 +958,7 @@ class NormPlan(_WorkspaceBase):
         self._spec = {"X": x, "dX": x, "C": x, "Y": y, "dY": y, "weight": cols, "bias": cols, "dweight": cols,
                       "dbias": cols, "mean": per_row, "rstd": per_row,
                       "workspace": (torch.uint8, self.workspace_bytes, None)}
-        self._pointers = self._together("X", "weight", "bias", "Y", "mean", "rstd")
-        self._grad_pointers = self._together("dY", "X", "weight", "mean", "rstd", "C", "dX", "dweight", "dbias")
+        self._together()
 
     def run(self, X, weight, bias, Y, mean=None, rstd=None, stream=None):
         """Enqueue the forward pass on `stream` (as Plan.run).  weight None is 1, bias None is 0; mean
@@ -979,6 +990,8 @@ class RoutePlan(_WorkspaceBase):
     that the plans over row ranges take, the balance loss, and the gradient towards the logits."""
 
     _destroy, _describe = staticmethod(gemm_route_plan_destroy), staticmethod(gemm_route_plan_describe)
+    _RUN = ("logits", "mask", "index", "weight", "order", "place", "offsets", "slope", "loss")
+    _GRAD = ("logits", "mask", "index", "dweight", "slope", "dloss", "dlogits")
 
     def __init__(self, rows, experts, k, type="f32", normalize=False, ldl=None):
         import torch
@@ -999,9 +1012,7 @@ class RoutePlan(_WorkspaceBase):
                       "offsets": (torch.int32, experts + 1, None), "slope": (torch.float32, experts, None),
                       "loss": (torch.float32, 1, None), "dloss": (torch.float32, 1, None),
                       "workspace": (torch.uint8, self.workspace_bytes, None)}
-        self._pointers = self._together("logits", "mask", "index", "weight", "order", "place", "offsets", "slope",
-                                        "loss")
-        self._grad_pointers = self._together("logits", "mask", "index", "dweight", "slope", "dloss", "dlogits")
+        self._together()
 
     def run(self, logits, index, weight, order, place, offsets, slope=None, loss=None, mask=None,
             workspace=None, stream=None):
