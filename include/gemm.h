@@ -631,10 +631,10 @@ gemm_status_t gemm_norm_plan_describe(gemm_norm_plan_t plan, char *buf, size_t l
  *   loss          (1 value) the balance loss E * sum over e of f_e P_e: f_e = choices of e / (k T'), P_e =
  *                 the mean of e's probability over the T' rows in use
  *   slope[e]      (experts values) E f_e / T', the loss's derivative by every row's probability of e
- * Left out are rows whose mask is 0 and those without a logit above minus infinity: index and place
- * -1, weight 0, no part in T'.  Logits that are minus infinity or NaN are never chosen (index and place
- * -1, weight 0 where fewer than k are left); a NaN or plus infinity makes its row's weights and the loss
- * NaN, as the softmax does.
+ * Left out are rows whose mask is 0 and those without a logit above minus infinity, NaN in them or not:
+ * index and place -1, weight 0, no part in T' or the loss.  Logits that are minus infinity or NaN are never
+ * chosen (index and place -1, weight 0 where fewer than k are left); in a row that is not left out a NaN or plus
+ * infinity makes the weights of its choices and the loss NaN, as the softmax does.
  *
  *   gradient: dlogits = the derivative of  sum of dweight * weight + dloss * loss  by the logits,
  * the choice and f held constant; 0 for rows left out.

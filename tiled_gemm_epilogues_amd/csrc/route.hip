@@ -469,9 +469,11 @@ __global__ __launch_bounds__(route_waves(LANES *PER) * 64) void choose(RoutePara
         for (int u = 0; u < AT; ++u) {
             const float mu = lanes_max<LANES>(largest(x[u]));
             const float su = exponentials<LANES>(x[u], mu), iu = su == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(su);
+            if (mu > NEG_INF) {                      // (a row left out may hold NaN)
 #pragma unroll
-            for (int v = 0; v < PER; ++v) ps[v] = __builtin_fmaf(x[u][v], iu, ps[v]);
-            if (mu > NEG_INF && l == 0) ++used;
+                for (int v = 0; v < PER; ++v) ps[v] = __builtin_fmaf(x[u][v], iu, ps[v]);
+                if (l == 0) ++used;
+            }
             m = part == u ? mu : m;
             s = part == u ? su : s;
             inv = part == u ? iu : inv;
@@ -699,7 +701,7 @@ __global__ __launch_bounds__(ROUTE_THREADS) void grad(RouteParams p) {
         order();
         if (at >= 0) share[at] = 0.0f;               // for the next row
         if (row < p.rows) {
-            if (!on) {                               // left out: 0, whatever dloss is
+            if (m == NEG_INF) {                      // left out: 0, whatever its logits and dloss are
 #pragma unroll
                 for (int v = 0; v < PER; ++v) d[v] = 0.0f;
             }
