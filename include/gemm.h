@@ -658,7 +658,7 @@ typedef struct {
  */
 gemm_status_t gemm_route_plan_create(gemm_route_plan_t *out, const gemm_route_desc_t *desc);
 
-/* Bytes of workspace that gemm_route_run needs (0 for few rows). */
+/* Bytes of workspace that gemm_route_run needs (0 for few rows, at most 2 KiB per expert and 1 KiB more). */
 gemm_status_t gemm_route_workspace_bytes(gemm_route_plan_t plan, size_t *bytes);
 
 /*
