@@ -601,6 +601,25 @@ class Plan:
             pass
 
 
+def _operands_module():
+    """The module _operands, or None where it does not load or was built for another torch (whose tensors it
+    would misread): operands are then checked one by one, which is right and takes a microsecond or two more."""
+    import torch
+    try:
+        from . import _operands
+    except ImportError as e:
+        why = str(e)
+    else:
+        built = getattr(_operands, "torch_version", None)
+        if built == str(torch.__version__):
+            return _operands
+        why = f"built for torch {built}, this is {torch.__version__}"
+    import warnings
+    warnings.warn(f"tiled_gemm_epilogues_amd/_operands.so is not used ({why}): operands are checked one by one; "
+                  "build again (python -m tiled_gemm_epilogues_amd.build)", RuntimeWarning, stacklevel=4)
+    return None
+
+
 class _GroupedBase:
     """What the plans over row ranges share: the handle, and the checks of a run's tensors."""
 
@@ -667,13 +686,10 @@ class _GroupedBase:
     _RUN, _GRAD = (), ()
 
     def _together(self):
-        import torch  # noqa: F401  (the module needs its libraries)
-        try:
-            from . import _operands
-        except ImportError as e:
-            raise ImportError(f"tiled_gemm_epilogues_amd/_operands.so is not built or does not load: {e}") from e
-        self._run_fits, self._grad_fits = (_operands.Operands(tuple(self._spec[n] for n in names))
-                                           for names in (self._RUN, self._GRAD))
+        module = _operands_module()
+        self._run_fits, self._grad_fits = (
+            module.Operands(tuple(self._spec[n] for n in names)) if module else lambda *_: None
+            for names in (self._RUN, self._GRAD))
 
     def _pointers(self, device, *tensors):
         got = self._run_fits(device, *tensors)

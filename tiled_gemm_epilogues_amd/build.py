@@ -81,6 +81,7 @@ def operands_step():
     base = os.path.dirname(torch.__file__)
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DTGE_TORCH_VERSION="{torch.__version__}"',
             "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
             "-I", sysconfig.get_paths()["include"], "-o", OPERANDS + ".tmp", os.path.join(CSRC, "operands.cpp"),
             "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]

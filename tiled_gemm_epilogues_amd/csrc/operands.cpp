@@ -116,5 +116,7 @@ PyMODINIT_FUNC PyInit__operands() {
     if (!m) return nullptr;
     Py_INCREF(&operands_type);
     if (PyModule_AddObject(m, "Operands", reinterpret_cast<PyObject *>(&operands_type)) < 0) return nullptr;
+    // (the binding uses the module with this torch only)
+    if (PyModule_AddStringConstant(m, "torch_version", TGE_TORCH_VERSION) < 0) return nullptr;
     return m;
 }
