@@ -5,7 +5,6 @@
 // the GPU some 3 us; seven operands checked one by one from Python take as long.
 #include <Python.h>
 
-#include <new>
 #include <vector>
 
 #include <torch/csrc/Dtype.h>
@@ -67,11 +66,13 @@ PyObject *call(PyObject *self, PyObject *const *args, size_t flags, PyObject *na
 PyObject *create(PyTypeObject *type, PyObject *args, PyObject *) {
     PyObject *list;
     if (!PyArg_ParseTuple(args, "O!", &PyTuple_Type, &list)) return nullptr;
-    Operands *self = reinterpret_cast<Operands *>(type->tp_alloc(type, 0));
+    Operands *self = reinterpret_cast<Operands *>(type->tp_alloc(type, 0));   // (zeroed)
     if (!self) return nullptr;
     self->call = call;
-    self->specs = new (std::nothrow) std::vector<Spec>();
-    if (!self->specs) {
+    try {
+        self->specs = new std::vector<Spec>();
+        self->specs->reserve(PyTuple_GET_SIZE(list));    // (nothing below throws)
+    } catch (...) {
         Py_DECREF(self);
         return PyErr_NoMemory();
     }
