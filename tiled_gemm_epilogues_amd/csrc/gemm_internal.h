@@ -329,8 +329,8 @@ hipError_t norm_grad_bf16(const NormParams &p, NormShape s, unsigned grid, hipSt
 hipError_t norm_join(const float *part, int count, int N, float *dweight, float *dbias, hipStream_t stream);
 
 // Routing of rows to experts (route.hip).  A row belongs to `lanes` lanes (16, 32 or 64) of a wave
-// with `per` consecutive experts each (lanes * per >= experts).  Workgroup b takes rows b *
-// block_rows .. + block_rows - 1.
+// with `per` experts each (lanes * per >= experts), in chunks of 16 bytes of logits dealt to the lanes in turn
+// (Share).  Workgroup b takes rows b * block_rows .. + block_rows - 1.
 constexpr int ROUTE_MAX_K = 16, ROUTE_MAX_EXPERTS = 1024, ROUTE_MAX_BLOCKS = 256;
 struct RouteParams {
     const void *logits;      // rows x experts, ldl

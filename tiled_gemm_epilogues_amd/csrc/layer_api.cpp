@@ -70,7 +70,7 @@ bool stream_stores(const gemm_layer_plan &p, const LayerEntry &k, const void *D,
 }
 
 // Whether the kernel for few rows reads the weights past the caches: where one workgroup reads each of them
-// and all of them are more than half of the 256 MB cache, so that they would not be found there
+// and all of them are half of the 256 MiB cache or more, so that they would not be found there
 // anyway.  B transposed, 16 rows: 16384 x 4096 (128 MiB) in turn with three others 28.2 -> 23.3 us, alone
 // 22.0 and 21.7; but 8192 x 4096 in turn 16.9 and 17.6, alone 13.3 and 17.1.  B not transposed (whose short
 // pieces of rows lose their second halves): 4096 x 4096 in turn 12.5 -> 19.9.
