@@ -209,7 +209,8 @@ __device__ __forceinline__ void store_layer_tile(const LayerParams &p, int mbase
 // 16-byte row pieces of the output type, a lane's pieces all in the same columns.  So C and Z are
 // read and written in whole lines (read in the accumulators' layout, 8 bytes of 16 rows at a time,
 // the gradient of 16384 rows by 16 experts of 8192 x 2048 took 603 us where the same product
-// without it takes 492; so it takes 523 to 563 by the activation, 463 without), the bias is 4 or 8 values per lane, and the loop over the blocks is rolled
+// without it takes 492; so it takes 523 to 563 by the activation, 463 without), the bias is 4 or 8
+// values per lane, and the loop over the blocks is rolled
 // around one copy of the activations' code (unrolled for every block it would not fit the
 // instruction cache); only the step from the accumulators, whose registers must be constants, is
 // there once per block.  C (Z) of the next block is loaded before the stores of this one, which it

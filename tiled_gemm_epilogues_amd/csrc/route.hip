@@ -11,7 +11,8 @@
 // A row belongs to 16, 32 or 64 lanes of a wave with up to 16 experts each, so that maxima
 // and sums need a few lane moves and no memory.  The choice compares logits, not probabilities: of
 // equal ones the lowest expert is taken, whatever the rounding of the softmax; NaN and minus
-// infinity are never chosen, and a row of nothing else is left out.  Bound: the instructions of the choice for many rows, launches for few:
+// infinity are never chosen, and a row of nothing else is left out.  Bound: the instructions of the
+// choice for many rows, launches for few:
 // 65536 rows of 128 fp32 logits (34 MB), 8 chosen, 18.6 us, of which the first loads 3, the choice 9 and the
 // launch and its end 4, and 10.4 us for the places; one row 5.7 us; the gradient 15.4 us (67 MB and the choices: 4.6 TB/s).
 //
